@@ -385,6 +385,198 @@ size_t moe_workspace_size(int32_t T, int32_t H, int32_t I, int32_t E, int32_t k,
 #define MOE_STATIC_SCRATCH_BYTES (64u << 20)
 int moe_fused_static(const moe_fused_args* a);
 
+/* ---- the operators around the expert step --------------------------------------------- */
+/* What a transformer layer calls next to the step above: the residual addition and RMS norm
+ * that make its quantised input, FP8 products for the layer's dense projections on the same
+ * number formats, and the gradients that train its router.  The conventions at the top of this
+ * file hold for all of them; in addition:
+ *   - outputs must not overlap each other, nor an input, except where an in-place use is named;
+ *   - a NULL optional output is not computed. */
+
+/* moe_add_rmsnorm: h = bf16_RNE(x + residual) (h = x without a residual),
+ *   y = bf16_RNE(h * r * weight),  r = 1 / sqrt(mean_c h[t, c]^2 + eps),
+ * sums and products in float32, and y's E4M3 codes and scales, exactly those of moe_quant_act /
+ * moe_quant_act_mx applied to y, so that yq, ys can be the xq, xs of moe_grouped_ffn or
+ * moe_linear.  The norm is of the rounded h: what is normalised is what the residual stream
+ * carries on, and what the backward pass reads.
+ *   T, H         rows and columns, H <= 32768; H % 8 == 0 (with codes H % 128 == 0, or
+ *                H % 32 == 0 for the 32-column schemes).
+ *   x, residual  [T, ld] bf16, first H columns used; ld % 8 == 0, 16-byte aligned; residual NULL
+ *                for none.
+ *   weight       [H] float32, 16-byte aligned.    eps >= 0, finite.
+ *   h, y         [T, H] bf16 out, 16-byte aligned, each optional (NULL).  h may be x or residual
+ *                itself, and y may be x itself (same pointer, ld = H).
+ *   yq, ys       both or neither: [T, H] E4M3 (8-byte aligned) and [T, H/128] UE8M0
+ *                (quant = MOE_QUANT_FP8_BLOCK128) or [T, H/32] (MOE_QUANT_MXFP8, MOE_QUANT_W4A8).
+ *                quant is ignored without them. */
+typedef struct moe_add_rmsnorm_args {
+    int32_t T, H;
+    const uint16_t* x;
+    int64_t         ld_x;
+    const uint16_t* residual;
+    int64_t         ld_residual;
+    const float*    weight;
+    float           eps;
+    uint16_t*       h;
+    uint16_t*       y;
+    uint8_t*        yq;
+    uint8_t*        ys;
+    int32_t         quant;
+    void*           stream;
+} moe_add_rmsnorm_args;
+int moe_add_rmsnorm(const moe_add_rmsnorm_args* a);
+
+/* moe_add_rmsnorm_backward: from dy, the gradient of y, and dh, that of h where it is also the
+ * next residual (NULL: none), with xhat = h * r and g = dy * weight:
+ *   dx[t, :]   = bf16_RNE( r * (g - xhat * mean_c(g * xhat)) + dh )   (the gradient of x and of
+ *                residual alike);
+ *   dweight[c] = sum_t dy[t, c] * xhat[t, c]                          (float32, optional).
+ * r is formed again from h.  The codes' rounding has no gradient of its own: dy is the gradient
+ * with respect to y, whether it came through y or through yq.
+ *   dy, h, dh, dx  [T, H] bf16, contiguous, 16-byte aligned; dx may be dy or dh itself.
+ *   workspace      >= moe_add_rmsnorm_backward_workspace_size(T, H) bytes, 256-byte aligned; used
+ *                  for dweight only (may be NULL without it).
+ * Deterministic: the weight gradient's partial sums are added in a fixed order. */
+typedef struct moe_add_rmsnorm_backward_args {
+    int32_t T, H;
+    const uint16_t* dy;
+    const uint16_t* h;
+    const float*    weight;
+    float           eps;
+    const uint16_t* dh;
+    uint16_t*       dx;
+    float*          dweight;
+    void*           workspace;
+    size_t          workspace_bytes;
+    void*           stream;
+} moe_add_rmsnorm_backward_args;
+int moe_add_rmsnorm_backward(const moe_add_rmsnorm_backward_args* a);
+size_t moe_add_rmsnorm_backward_workspace_size(int32_t T, int32_t H);
+
+/* Activations of moe_linear's epilogue. */
+#define MOE_ACT_NONE       0
+#define MOE_ACT_RELU       1
+#define MOE_ACT_SILU       2   /* v / (1 + exp(-v))                                        */
+#define MOE_ACT_GELU       3   /* v * (1 + erf(v / sqrt 2)) / 2                            */
+#define MOE_ACT_GELU_TANH  4   /* v * (1 + tanh(sqrt(2/pi) * (v + 0.044715 v^3))) / 2       */
+
+/* moe_linear: y = act( dequant(xq, xs) @ dequant(w, w_scale) + bias ) + residual, FP8 x FP8 with
+ * float32 accumulation and one rounding to y's type at the end.
+ *   T, K, N    K % 128 == 0, K <= 32768; N % 16 == 0; T * K < 2^31, K * N < 2^31.
+ *   quant      MOE_QUANT_FP8_BLOCK128: xq [T, K], xs [T, K/128] (moe_quant_act); w packed by
+ *              moe_prepack_weights with E = 1, w_scale [K/128, ceil(N/128)] in its logical layout.
+ *              MOE_QUANT_MXFP8: xs [T, K/32] (moe_quant_act_mx), w and w_scale packed by
+ *              moe_prepack_weights_mx with E = 1.  The other schemes: MOE_ERR_UNSUPPORTED.
+ *   xq, w      16-byte aligned; xs and w_scale 4-byte aligned for MOE_QUANT_MXFP8.
+ *   bias       [N] float32 or NULL.    activation  MOE_ACT_*.
+ *   residual   [T, ld_residual] of y's type, or NULL; may be y itself (same pointer and ld).
+ *   y          [T, ld_y] of out_dtype (MOE_DTYPE_*), the first N columns written;
+ *              ld_y, ld_residual >= N and % 8 == 0, both pointers 16-byte aligned.
+ *   workspace  >= moe_linear_workspace_size(T, K, N, quant) bytes, 256-byte aligned (NULL where
+ *              that is 0).
+ * Deterministic. */
+typedef struct moe_linear_args {
+    int32_t T, K, N;
+    const uint8_t* xq;
+    const uint8_t* xs;
+    const uint8_t* w;
+    const uint8_t* w_scale;
+    const float*   bias;
+    int32_t        activation;
+    const void*    residual;
+    int64_t        ld_residual;
+    void*          y;
+    int64_t        ld_y;
+    int32_t        out_dtype;
+    int32_t        quant;
+    void*          workspace;
+    size_t         workspace_bytes;
+    void*          stream;
+} moe_linear_args;
+int moe_linear(const moe_linear_args* a);
+size_t moe_linear_workspace_size(int32_t T, int32_t K, int32_t N, int32_t quant);
+
+/* moe_balance_loss: load-balance and z losses of a router, with per-expert counts.  The rows are
+ * num_seqs packed sequences, sequence s in rows [seq_offsets[s], seq_offsets[s+1]); seq_offsets
+ * NULL: one sequence of all T rows (num_seqs 1).  With T_s rows in sequence s, S' sequences that
+ * have rows, and T_v rows in all of them:
+ *   c[s, e]  = assignments of the sequence's rows to expert e (ids outside [0, E) count nowhere);
+ *   p[t, :]  = softmax(logits[t]), or sigmoid(logits[t]) over its sum;  P[s, e] = mean_t p[t, e];
+ *   balance  = balance_coef / S' * sum_s sum_e E * c[s, e] / (top_k * T_s) * P[s, e];
+ *   z        = z_coef / T_v * sum_t (log sum_e exp logits[t, e])^2.
+ * Counts are taken as constants in the gradient (moe_route_backward).
+ *   p           routing parameters: num_experts, top_k and scoring are used.
+ *   seq_offsets [num_seqs + 1] int32 on the device, non-decreasing within [0, T]; values outside
+ *               are taken as the nearest ones inside.  Sequences may be empty; rows before the
+ *               first and behind the last sequence are not read.
+ *   A row whose logits are all -infinity (or whose sigmoids all vanish) adds nothing to P and z.
+ *   losses      [3] float32 out: balance + z, balance, z.  (0 when no sequence has rows.)
+ *   counts      [num_seqs, E] int32 out.
+ *   mean_probs  [num_seqs, E] float32 out: P (0 for an empty sequence); optional.
+ *   workspace   >= moe_balance_loss_workspace_size(T, E, num_seqs) bytes, 256-byte aligned.
+ * Deterministic. */
+typedef struct moe_balance_loss_args {
+    const moe_route_params* route;
+    int32_t T, num_seqs;
+    const float*   router_logits;
+    const int32_t* topk_ids;
+    const int32_t* seq_offsets;
+    float          balance_coef, z_coef;
+    float*         losses;
+    int32_t*       counts;
+    float*         mean_probs;
+    void*          workspace;
+    size_t         workspace_bytes;
+    void*          stream;
+} moe_balance_loss_args;
+int moe_balance_loss(const moe_balance_loss_args* a);
+size_t moe_balance_loss_workspace_size(int32_t T, int32_t E, int32_t num_seqs);
+
+/* moe_route_backward: the gradient of the router logits, dlogits [T, E], through
+ *   - the routing weights of moe_route, from dtopk_weights [T, k] (NULL: none): softmax with and
+ *     without renormalize, or sigmoid, with routed_scaling_factor; the selection itself has no
+ *     gradient.  An id that stands in a row more than once adds up; ids outside [0, E) are dropped
+ *     assignments: they are not among those that the weights are normalised over;
+ *   - the losses of moe_balance_loss, from its counts (NULL: none, then seq_offsets only marks
+ *     the rows).  z_coef needs no counts.
+ * Rows outside the sequences get a zero gradient; their logits, ids and dtopk_weights are not
+ * read.  dlogits may be router_logits itself.  Deterministic. */
+typedef struct moe_route_backward_args {
+    const moe_route_params* route;
+    int32_t T, num_seqs;
+    const float*   router_logits;
+    const int32_t* topk_ids;
+    const float*   dtopk_weights;
+    const int32_t* counts;
+    const int32_t* seq_offsets;
+    float          balance_coef, z_coef;
+    float*         dlogits;
+    void*          stream;
+} moe_route_backward_args;
+int moe_route_backward(const moe_route_backward_args* a);
+
+/* moe_combine_backward: gradients of moe_combine, from dy [T, H] bf16:
+ *   dtopk_weights[t, j]             = sum_c dy[t, c] * expert_out[assign_pos[t*k+j], c]   (float32)
+ *   dexpert_out[assign_pos[t*k+j]]  = topk_weights[t, j] * dy[t]     (dtype, rounded once)
+ * Either output may be NULL (then expert_out, or topk_weights, may be too).  Entries of
+ * assign_pos outside [0, T*k) are dropped assignments: their weight gradient is 0, and rows of
+ * dexpert_out that no entry names are left as they were.  No two entries may name the same row
+ * with dexpert_out.
+ *   expert_out, dexpert_out  [T*k, H] of dtype MOE_DTYPE_F32 or MOE_DTYPE_BF16, 16-byte aligned;
+ *   dexpert_out may be expert_out itself.  dy 16-byte aligned.  H % 8 == 0; T * k < 2^29. */
+typedef struct moe_combine_backward_args {
+    int32_t T, k, H;
+    int32_t dtype;
+    const uint16_t* dy;
+    const void*     expert_out;
+    const int32_t*  assign_pos;
+    const float*    topk_weights;
+    float*          dtopk_weights;
+    void*           dexpert_out;
+    void*           stream;
+} moe_combine_backward_args;
+int moe_combine_backward(const moe_combine_backward_args* a);
+
 /* Thread-local description of the last error returned on this thread ("" after success). */
 const char* moe_last_error(void);
 

@@ -12,3 +12,8 @@ from .binding import (  # noqa: F401
     pack_weights_mx, MOE_QUANT_FP8_BLOCK128, MOE_QUANT_MXFP8, MOE_QUANT_W4A8, MOE_QUANT_W8A16, MOE_WFMT_E4M3, MOE_WFMT_E2M1,
     QUANT_SCHEMES, MOE_FUSED_EXPERT_OUT_BF16, MOE_FUSED_SHARED_EXPERT, moe_fused_static, MOE_STATIC_SCRATCH_BYTES,
 )
+from .layer import (  # noqa: F401
+    ACTIVATIONS, LinearWeights, MoeAddRmsNorm, MoeAddRmsNormBackward, MoeBalanceLoss, MoeCombineBackward, MoeLinear,
+    MoeRouteBackward, moe_add_rmsnorm, moe_add_rmsnorm_backward, moe_balance_loss, moe_combine_backward, moe_linear,
+    moe_route_backward,
+)

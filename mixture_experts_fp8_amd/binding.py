@@ -32,7 +32,9 @@ QUANT_SCHEMES = {"fp8": MOE_QUANT_FP8_BLOCK128, "mxfp8": MOE_QUANT_MXFP8, "w4a8"
 EXPORTED = ["moe_route", "moe_route_workspace_size", "moe_quant_act", "moe_quant_weight_blocks",
             "moe_prepack_weights", "moe_grouped_ffn", "moe_ffn_workspace_size", "moe_combine",
             "moe_fused", "moe_workspace_size", "moe_last_error", "moe_quant_act_mx", "moe_quant_weight_mx",
-            "moe_prepack_weights_mx", "moe_fused_static"]
+            "moe_prepack_weights_mx", "moe_fused_static", "moe_add_rmsnorm", "moe_add_rmsnorm_backward",
+            "moe_add_rmsnorm_backward_workspace_size", "moe_linear", "moe_linear_workspace_size", "moe_balance_loss",
+            "moe_balance_loss_workspace_size", "moe_route_backward", "moe_combine_backward"]
 MOE_STATIC_SCRATCH_BYTES = 64 << 20
 
 
@@ -123,6 +125,14 @@ def lib() -> ctypes.CDLL:
         L.moe_quant_weight_mx.argtypes = [vp, i32, i32, i32, i32, vp, vp, vp]
         L.moe_prepack_weights_mx.restype = ctypes.c_int
         L.moe_prepack_weights_mx.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp, vp]
+        for name in ("moe_add_rmsnorm", "moe_add_rmsnorm_backward", "moe_linear", "moe_balance_loss",
+                     "moe_route_backward", "moe_combine_backward"):   # one argument struct each (layer.py)
+            getattr(L, name).restype = ctypes.c_int
+            getattr(L, name).argtypes = [vp]
+        for name, n in (("moe_add_rmsnorm_backward_workspace_size", 2), ("moe_linear_workspace_size", 4),
+                        ("moe_balance_loss_workspace_size", 3)):
+            getattr(L, name).restype = sz
+            getattr(L, name).argtypes = [i32] * n
         _lib = L
     return _lib
 

@@ -1,0 +1,282 @@
+// Residual addition + RMS norm with E4M3 codes, and its backward pass (gfx950).
+//
+// One pass: a row's vectors of 8 columns stay in registers between the sum of squares and the
+// output, so every input byte is read once and every output byte written once; the kernels are
+// bound by HBM.
+#include "layer_common.h"
+
+#include <algorithm>
+
+namespace moe {
+
+// Sum over the G threads of a row: a wave's sum, then (G > 64) the waves' sums through LDS in wave
+// order.  s: G / 64 floats of the row, not in use by a slower wave of an earlier call (the callers
+// alternate two of them).
+template <int G>
+__device__ __forceinline__ float row_sum(float v, float* s) {
+    v = wave_sum(v);
+    if constexpr (G > 64) {
+        const int wv = (threadIdx.x % G) >> 6;
+        if ((threadIdx.x & 63) == 0) s[wv] = v;
+        __syncthreads();
+        v = 0.f;
+#pragma unroll
+        for (int i = 0; i < G / 64; ++i) v += s[i];
+    }
+    return v;
+}
+
+// E4M3 codes of 8 values in each of LANES consecutive lanes sharing one scale (LANES * 8 columns):
+// the rule of moe_quant_act on values that are bf16 already.
+template <int LANES>
+__device__ __forceinline__ uint2 group_codes(const float (&f)[8], int& e) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));
+    m = fmaxf(m, dpp_f32<0xB1>(m));
+    m = fmaxf(m, dpp_f32<0x4E>(m));
+    if constexpr (LANES == 16) {
+        m = fmaxf(m, dpp_f32<0x124>(m));
+        m = fmaxf(m, dpp_f32<0x128>(m));
+    }
+    e = scale_exponent(m);
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = ldexpf(f[i], -e);
+    return make_uint2(cvt4_e4m3(q[0], q[1], q[2], q[3]), cvt4_e4m3(q[4], q[5], q[6], q[7]));
+}
+
+// G threads per row, VPT vectors of 8 columns per thread (G * VPT >= H / 8); a workgroup holds
+// max(1, 256 / G) rows.
+template <int G, int VPT>
+__global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_rmsnorm(NormArgs a) {
+    constexpr int RPB = G < 256 ? 256 / G : 1;
+    __shared__ float s_sum[RPB][G / 64];
+    const int sub = threadIdx.x % G, nv = a.H >> 3;
+    const int64_t t = (int64_t)blockIdx.x * RPB + threadIdx.x / G;
+    if (RPB > 1 && t >= a.T) return;   // (RPB > 1 only with G = 64: no barrier follows)
+    const uint16_t* xr = a.x + t * a.ldx;
+    const uint16_t* rr = a.res ? a.res + t * a.ldr : nullptr;
+    uint4 vx[VPT], vr[VPT];
+    float4 w0[VPT], w1[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int v = sub + i * G;
+        if (v < nv) vx[i] = *reinterpret_cast<const uint4*>(xr + v * 8);
+        else vx[i] = make_uint4(0, 0, 0, 0);
+    }
+    if (rr) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = sub + i * G;
+            if (v < nv) vr[i] = *reinterpret_cast<const uint4*>(rr + v * 8);
+            else vr[i] = make_uint4(0, 0, 0, 0);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int v = sub + i * G;
+        if (v < nv) {
+            w0[i] = *reinterpret_cast<const float4*>(a.w + v * 8);
+            w1[i] = *reinterpret_cast<const float4*>(a.w + v * 8 + 4);
+        }
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        float f[8];
+        unpack8(vx[i], f);
+        if (rr) {
+            float g[8];
+            unpack8(vr[i], g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] += g[j];
+            vx[i] = pack8(f);      // h, rounded once; kept as bf16
+            unpack8(vx[i], f);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
+    }
+    if (a.h) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = sub + i * G;
+            if (v < nv) *reinterpret_cast<uint4*>(a.h + t * a.H + v * 8) = vx[i];
+        }
+    }
+    if (!a.y && !a.yq) return;   // (uniform)
+    ss = row_sum<G>(ss, s_sum[threadIdx.x / G]);
+    const float r = 1.0f / sqrtf(ss / (float)a.H + a.eps);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int v = sub + i * G;
+        float f[8];
+        unpack8(vx[i], f);
+        const float w[8] = {w0[i].x, w0[i].y, w0[i].z, w0[i].w, w1[i].x, w1[i].y, w1[i].z, w1[i].w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = f[j] * r * w[j];
+        const uint4 o = pack8(f);
+        if (v < nv) {   // a scale's lanes are all in or all out: H is a multiple of its columns
+            if (a.y) *reinterpret_cast<uint4*>(a.y + t * a.H + v * 8) = o;
+            if (a.yq) {
+                unpack8(o, f);
+                int e;
+                if (a.group == 128) {
+                    *reinterpret_cast<uint2*>(a.yq + t * a.H + v * 8) = group_codes<16>(f, e);
+                    if ((v & 15) == 0) a.ys[t * (a.H >> 7) + (v >> 4)] = (uint8_t)(e + 127);
+                } else {
+                    *reinterpret_cast<uint2*>(a.yq + t * a.H + v * 8) = group_codes<4>(f, e);
+                    if ((v & 3) == 0) a.ys[t * (a.H >> 5) + (v >> 2)] = (uint8_t)(e + 127);
+                }
+            }
+        }
+    }
+}
+
+template <int G, int VPT>
+static void run_norm(const NormArgs& a, hipStream_t st) {
+    constexpr int RPB = G < 256 ? 256 / G : 1;
+    hipLaunchKernelGGL((k_add_rmsnorm<G, VPT>), dim3((unsigned)ceil_div(a.T, RPB)), dim3(G < 256 ? 256 : G), 0, st, a);
+}
+
+hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t st) {
+    const int nv = a.H / 8;
+    if (nv <= 64) run_norm<64, 1>(a, st);
+    else if (nv <= 256) run_norm<256, 1>(a, st);
+    else if (nv <= 512) run_norm<512, 1>(a, st);
+    else if (nv <= 1024) run_norm<1024, 1>(a, st);
+    else if (nv <= 2048) run_norm<1024, 2>(a, st);
+    else run_norm<1024, 4>(a, st);
+    return hipGetLastError();
+}
+
+// ----------------------------------------------------------------------------------------
+// Backward.  With xhat = h r and g = dy w:  dx = r (g - xhat mean(g xhat)) + dh, and the weight
+// gradient sum_t dy xhat.  A workgroup walks rows blockIdx.x, + gridDim.x, ... and keeps its
+// share of the weight gradient in registers; the workgroups' sums go to `part` and are added in
+// workgroup order by k_norm_dw.
+template <int G, int VPT>
+__global__ __launch_bounds__(G) void k_add_rmsnorm_bwd(NormBwdArgs a) {
+    __shared__ float s_sum[2][2][G / 64];
+    const int sub = threadIdx.x, nv = a.H >> 3;
+    float dw[VPT][8], w[VPT][8];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int v = sub + i * G;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            dw[i][j] = 0.f;
+            w[i][j] = v < nv ? a.w[v * 8 + j] : 0.f;
+        }
+    }
+    int par = 0;
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, par ^= 1) {
+        uint4 vh[VPT], vd[VPT], vr[VPT];
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = sub + i * G;
+            const int64_t o = t * a.H + v * 8;
+            vh[i] = vd[i] = vr[i] = make_uint4(0, 0, 0, 0);
+            if (v < nv) {
+                vh[i] = *reinterpret_cast<const uint4*>(a.h + o);
+                vd[i] = *reinterpret_cast<const uint4*>(a.dy + o);
+                if (a.dh) vr[i] = *reinterpret_cast<const uint4*>(a.dh + o);
+            }
+        }
+        // sum h^2 and sum g h in one exchange: mean(g xhat) = r sum(g h) / H
+        float ss = 0.f, gh = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            float h[8], d[8];
+            unpack8(vh[i], h);
+            unpack8(vd[i], d);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                ss = fmaf(h[j], h[j], ss);
+                gh = fmaf(d[j] * w[i][j], h[j], gh);
+            }
+        }
+        ss = wave_sum(ss);
+        gh = wave_sum(gh);
+        if constexpr (G > 64) {
+            if ((sub & 63) == 0) {
+                s_sum[par][0][sub >> 6] = ss;
+                s_sum[par][1][sub >> 6] = gh;
+            }
+            __syncthreads();
+            ss = gh = 0.f;
+#pragma unroll
+            for (int i = 0; i < G / 64; ++i) {
+                ss += s_sum[par][0][i];
+                gh += s_sum[par][1][i];
+            }
+        }
+        const float r = 1.0f / sqrtf(ss / (float)a.H + a.eps);
+        const float c = gh / (float)a.H * r * r;     // xhat mean(g xhat) = h c
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = sub + i * G;
+            float h[8], d[8], e[8];
+            unpack8(vh[i], h);
+            unpack8(vd[i], d);
+            unpack8(vr[i], e);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                dw[i][j] = fmaf(d[j], h[j] * r, dw[i][j]);
+                const float g = r * (d[j] * w[i][j] - h[j] * c);
+                e[j] = a.dh ? g + e[j] : g;
+            }
+            if (v < nv) *reinterpret_cast<uint4*>(a.dx + t * a.H + v * 8) = pack8(e);
+        }
+    }
+    if (a.dw) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = sub + i * G;
+            if (v < nv) {
+                float* p = a.part + (int64_t)blockIdx.x * a.H + v * 8;
+                *reinterpret_cast<float4*>(p) = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
+                *reinterpret_cast<float4*>(p + 4) = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+            }
+        }
+    }
+}
+
+// dweight[c] = sum of the partial rows, in order: 32 columns per workgroup, 32 row groups whose
+// sums are then added in order through LDS.
+__global__ __launch_bounds__(1024) void k_norm_dw(const float* __restrict__ part, int np, int H, float* __restrict__ dw) {
+    __shared__ float s[32][33];
+    const int c = threadIdx.x & 31, g = threadIdx.x >> 5, col = blockIdx.x * 32 + c;
+    float v = 0.f;
+    if (col < H)
+        for (int p = g; p < np; p += 32) v += part[(int64_t)p * H + col];
+    s[g][c] = v;
+    __syncthreads();
+    if (g == 0 && col < H) {
+        v = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v += s[i][c];
+        dw[col] = v;
+    }
+}
+
+template <int G, int VPT>
+static void run_norm_bwd(const NormBwdArgs& a, int grid, hipStream_t st) {
+    hipLaunchKernelGGL((k_add_rmsnorm_bwd<G, VPT>), dim3(grid), dim3(G), 0, st, a);
+}
+
+hipError_t launch_add_rmsnorm_backward(const NormBwdArgs& a, hipStream_t st) {
+    const int nv = a.H / 8, grid = norm_bwd_parts(a.T, a.H);
+    if (nv <= 64) run_norm_bwd<64, 1>(a, grid, st);
+    else if (nv <= 256) run_norm_bwd<256, 1>(a, grid, st);
+    else if (nv <= 512) run_norm_bwd<512, 1>(a, grid, st);
+    else if (nv <= 1024) run_norm_bwd<1024, 1>(a, grid, st);
+    else if (nv <= 2048) run_norm_bwd<1024, 2>(a, grid, st);
+    else run_norm_bwd<1024, 4>(a, grid, st);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !a.dw) return e;
+    hipLaunchKernelGGL(k_norm_dw, dim3((unsigned)ceil_div(a.H, 32)), dim3(1024), 0, st, a.part, grid, a.H, a.dw);
+    return hipGetLastError();
+}
+
+}  // namespace moe

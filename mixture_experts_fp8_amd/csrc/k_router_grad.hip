@@ -1,0 +1,558 @@
+// Router training (gfx950): load-balance and z losses with per-expert counts, the gradient of the
+// router logits, and the gradients of the weighted combine.
+//
+// A row of logits is held by L lanes (16 up to 256 experts, a whole wave above), 4 * Q values each;
+// lane `sub` has experts 4 * (sub + L * i) + c.  Softmax sums stay inside the L lanes.
+#include "layer_common.h"
+
+#include <algorithm>
+
+namespace moe {
+
+template <int L>
+__device__ __forceinline__ float rsum(float v) {
+    if constexpr (L == 16) return sum16(v);
+    else return wave_sum(v);
+}
+template <int L>
+__device__ __forceinline__ float rmax(float v) {
+    if constexpr (L == 16) return max16(v);
+    else return wave_max(v);
+}
+
+// Elements of row p (E of them) that the lane holds; `pad` behind the end.
+template <int L, int Q, bool VEC, typename V>
+__device__ __forceinline__ void load_row(const V* __restrict__ p, int E, int sub, V pad, V (&v)[4 * Q]) {
+    typedef V v4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+    for (int i = 0; i < Q; ++i) {
+        const int e = 4 * (sub + L * i);
+        if constexpr (VEC) {
+            v4 x = {pad, pad, pad, pad};
+            if (e < E) x = *reinterpret_cast<const v4*>(p + e);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[4 * i + c] = x[c];
+        } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[4 * i + c] = e + c < E ? p[e + c] : pad;
+        }
+    }
+}
+
+// Sequence s of the packed rows: [begin, end), clamped into [0, T].
+struct Seqs {
+    const int32_t* off;   // NULL: one sequence of all rows
+    int S, T;
+    __device__ __forceinline__ int at(int i) const { return min(max(off[i], 0), T); }
+    __device__ __forceinline__ int begin(int s) const { return off ? at(s) : 0; }
+    __device__ __forceinline__ int end(int s) const { return off ? max(at(s + 1), at(s)) : T; }
+    // the sequence that row t lies in if it lies in one: the last one that begins at or before t
+    __device__ __forceinline__ int find(int t) const {
+        if (!off) return 0;
+        int lo = 0, hi = S;   // begin(lo) <= t (or lo == 0), begin(hi) > t (or hi == S)
+        while (hi - lo > 1) {
+            const int m = (lo + hi) >> 1;
+            if (at(m) <= t) lo = m;
+            else hi = m;
+        }
+        return lo;
+    }
+};
+
+// Softmax numerators of a row: v -> exp(v - max); returns their sum (0 only where every logit is
+// -infinity) and the shift.  NaN logits make the sum NaN.
+template <int L, int Q>
+__device__ __forceinline__ float softmax_row(float (&v)[4 * Q], float& shift) {
+    float m = v[0];
+#pragma unroll
+    for (int i = 1; i < 4 * Q; ++i) m = fmaxf(m, v[i]);
+    m = rmax<L>(m);
+    shift = m == -INFINITY ? 0.f : m;
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4 * Q; ++i) {
+        v[i] = expf(v[i] - shift);
+        s += v[i];
+    }
+    return rsum<L>(s);
+}
+
+// ----------------------------------------------------------------------------------------
+// Sums of probabilities, counts and squared log-sums of each (workgroup, sequence) part.
+template <int L, int Q, bool VEC>
+__global__ __launch_bounds__(256) void k_balance_rows(BalanceArgs a, BalancePlan p) {
+    constexpr int NG = 256 / L, N = 4 * Q;
+    __shared__ __align__(16) float s_p[NG][L * N];
+    __shared__ int s_hit[L * N];
+    __shared__ float s_z[NG];
+    const int tid = threadIdx.x, g = tid / L, sub = tid % L, b = blockIdx.x;
+    if (b == 0 && tid == 0) *reinterpret_cast<int*>(a.ws + p.done) = 0;   // the second kernel's ticket
+    float* probs = reinterpret_cast<float*>(a.ws + p.probs);
+    int* hits = reinterpret_cast<int*>(a.ws + p.hits);
+    float* zs = reinterpret_cast<float*>(a.ws + p.z);
+    const Seqs sq{a.off, a.S, a.T};
+    const int lo = b * p.chunk, hi = min(a.T, lo + p.chunk);
+    for (int s = sq.find(lo); s < a.S && sq.begin(s) < hi; ++s) {
+        const int r0 = max(sq.begin(s), lo), r1 = min(sq.end(s), hi);
+        if (r0 >= r1) continue;
+        for (int e = tid; e < a.E; e += 256) s_hit[e] = 0;
+        __syncthreads();
+        for (int64_t i = (int64_t)r0 * a.k + tid; i < (int64_t)r1 * a.k; i += 256) {
+            const int id = a.ids[i];
+            if (id >= 0 && id < a.E) atomicAdd(&s_hit[id], 1);
+        }
+        float acc[N], z = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] = 0.f;
+        for (int r = r0 + g; r < r1; r += NG) {
+            float v[N];
+            load_row<L, Q, VEC>(a.logits + (int64_t)r * a.E, a.E, sub, -INFINITY, v);
+            float num[N], shift;
+            if (a.scoring == MOE_SCORING_SIGMOID) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) num[i] = 1.0f / (1.0f + expf(-v[i]));
+            }
+            const float sum = softmax_row<L, Q>(v, shift);
+            if (sum != 0.f) {
+                const float lse = shift + logf(sum);
+                z = fmaf(lse, lse, z);
+            }
+            float tot = sum;
+            if (a.scoring == MOE_SCORING_SIGMOID) {
+                float t = 0.f;
+#pragma unroll
+                for (int i = 0; i < N; ++i) t += num[i];
+                tot = rsum<L>(t);
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) num[i] = v[i];
+            }
+            const float inv = tot != 0.f ? 1.0f / tot : 0.f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) acc[i] = fmaf(num[i], inv, acc[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < Q; ++i)
+            *reinterpret_cast<float4*>(&s_p[g][4 * (sub + L * i)]) =
+                make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+        if (sub == 0) s_z[g] = z;
+        __syncthreads();
+        const int64_t slot = (int64_t)(b + s) * a.E;
+        for (int e = tid; e < a.E; e += 256) {
+            float v = 0.f;
+#pragma unroll
+            for (int i = 0; i < NG; ++i) v += s_p[i][e];
+            probs[slot + e] = v;
+            hits[slot + e] = s_hit[e];
+        }
+        if (tid == 0) {
+            float v = 0.f;
+#pragma unroll
+            for (int i = 0; i < NG; ++i) v += s_z[i];
+            zs[b + s] = v;
+        }
+        __syncthreads();
+    }
+}
+
+// Workgroup (sequence, 64 experts): the parts' sums in row order -> counts, mean probabilities and
+// the sequence's share of the losses; the last workgroup to finish adds the shares in order.
+__global__ __launch_bounds__(1024) void k_balance_reduce(BalanceArgs a, BalancePlan p) {
+    constexpr int NG = 1024 / kBalanceCols;
+    __shared__ float s_p[NG][kBalanceCols];
+    __shared__ int s_h[NG][kBalanceCols];
+    __shared__ float s_w[2][16];
+    __shared__ int s_n[2][16];
+    __shared__ int s_last;
+    const int tid = threadIdx.x, c = tid & (kBalanceCols - 1), g = tid / kBalanceCols;
+    const int ncp = (int)ceil_div(a.E, kBalanceCols);
+    const int s = blockIdx.x / ncp, cp = blockIdx.x - s * ncp, e = cp * kBalanceCols + c;
+    const Seqs sq{a.off, a.S, a.T};
+    const int t0 = sq.begin(s), t1 = sq.end(s);
+    const float* probs = reinterpret_cast<const float*>(a.ws + p.probs);
+    const int* hits = reinterpret_cast<const int*>(a.ws + p.hits);
+    const float* zs = reinterpret_cast<const float*>(a.ws + p.z);
+    float* seq = reinterpret_cast<float*>(a.ws + p.seq);
+    const int b0 = t0 / p.chunk, b1 = t1 > t0 ? (t1 - 1) / p.chunk + 1 : b0;
+    float v = 0.f;
+    int n = 0;
+    if (e < a.E)
+        for (int b = b0 + g; b < b1; b += NG) {
+            v += probs[(int64_t)(b + s) * a.E + e];
+            n += hits[(int64_t)(b + s) * a.E + e];
+        }
+    s_p[g][c] = v;
+    s_h[g][c] = n;
+    __syncthreads();
+    if (tid < 64) {
+        v = 0.f;
+        n = 0;
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+            v += s_p[i][c];
+            n += s_h[i][c];
+        }
+        const float len = (float)(t1 - t0), mean = t1 > t0 ? v / len : 0.f;
+        if (e < a.E) {
+            a.counts[(int64_t)s * a.E + e] = n;
+            if (a.mean_probs) a.mean_probs[(int64_t)s * a.E + e] = mean;
+        }
+        const float dot = wave_sum(t1 > t0 && e < a.E ? mean * ((float)n / len) : 0.f);
+        float z = 0.f;
+        if (cp == 0)
+            for (int b = b0 + c; b < b1; b += 64) z += zs[b + s];
+        z = wave_sum(z);
+        if (c == 0) {
+            __hip_atomic_store(&seq[2 * blockIdx.x], dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __hip_atomic_store(&seq[2 * blockIdx.x + 1], z, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __threadfence();
+            s_last = __hip_atomic_fetch_add(reinterpret_cast<int*>(a.ws + p.done), 1, __ATOMIC_ACQ_REL,
+                                            __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
+        }
+    }
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    float bal = 0.f, z = 0.f;
+    int live = 0, valid = 0;
+    for (int i = tid; i < (int)gridDim.x; i += 1024) {
+        bal += __hip_atomic_load(&seq[2 * i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        z += __hip_atomic_load(&seq[2 * i + 1], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    for (int i = tid; i < a.S; i += 1024) {
+        const int len = sq.end(i) - sq.begin(i);
+        live += len > 0;
+        valid += len;
+    }
+    bal = wave_sum(bal);
+    z = wave_sum(z);
+#pragma unroll
+    for (int o = 32; o; o >>= 1) {
+        live += __shfl_xor(live, o);
+        valid += __shfl_xor(valid, o);
+    }
+    if ((tid & 63) == 0) {
+        s_w[0][tid >> 6] = bal;
+        s_w[1][tid >> 6] = z;
+        s_n[0][tid >> 6] = live;
+        s_n[1][tid >> 6] = valid;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        bal = z = 0.f;
+        live = valid = 0;
+        for (int i = 0; i < 16; ++i) {
+            bal += s_w[0][i];
+            z += s_w[1][i];
+            live += s_n[0][i];
+            valid += s_n[1][i];
+        }
+        bal = live ? a.ca * bal * ((float)a.E / (float)a.k) / (float)live : 0.f;
+        z = valid ? a.cz * z / (float)valid : 0.f;
+        a.losses[0] = bal + z;
+        a.losses[1] = bal;
+        a.losses[2] = z;
+    }
+}
+
+// Experts per row -> lanes per row, vectors per lane.
+#define MOE_ROW_DISPATCH(E, VEC, CALL)                    \
+    do {                                                  \
+        if ((E) <= 64) { if (VEC) CALL(16, 1, true); else CALL(16, 1, false); }        \
+        else if ((E) <= 128) { if (VEC) CALL(16, 2, true); else CALL(16, 2, false); }  \
+        else if ((E) <= 256) { if (VEC) CALL(16, 4, true); else CALL(16, 4, false); }  \
+        else if ((E) <= 512) { if (VEC) CALL(64, 2, true); else CALL(64, 2, false); }  \
+        else { if (VEC) CALL(64, 4, true); else CALL(64, 4, false); }                  \
+    } while (0)
+
+static bool vec4(const void* p, int E) { return E % 4 == 0 && (uintptr_t)p % 16 == 0; }
+
+hipError_t launch_balance_loss(const BalanceArgs& a, hipStream_t st) {
+    const BalancePlan p = balance_plan(a.T, a.E, a.S);
+#define MOE_CALL(L, Q, V) hipLaunchKernelGGL((k_balance_rows<L, Q, V>), dim3(p.nblocks), dim3(256), 0, st, a, p)
+    MOE_ROW_DISPATCH(a.E, vec4(a.logits, a.E), MOE_CALL);
+#undef MOE_CALL
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(k_balance_reduce, dim3((unsigned)(a.S * ceil_div(a.E, kBalanceCols))), dim3(1024), 0, st, a, p);
+    return hipGetLastError();
+}
+
+// ----------------------------------------------------------------------------------------
+// Gradient of the router logits.  With p the probabilities, u_e = dL/dp_e of the balance loss
+// (the sequence's counts times a constant), s the scores and D_e = sum of dw_j over the slots that
+// chose e, m_e their number:
+//   balance, softmax   p (u - sum p u)
+//            sigmoid   p (1 - s) (u - sum p u)
+//   z                  2 cz lse / T_v softmax
+//   weights, softmax   rsf p (D - sum p D)
+//            over the chosen (softmax renormalised; sigmoid with a factor 1 - s):
+//                      rsf q (D - m sum q D),  q = score / sum m score
+constexpr int kSeqLds = 1024;   // sequence boundaries held in LDS
+template <int L, int Q, bool VEC>
+__global__ __launch_bounds__(256) void k_route_bwd(RouteBwdArgs a) {
+    constexpr int NG = 256 / L, N = 4 * Q;
+    __shared__ int s_off[kSeqLds + 1];
+    __shared__ int s_n[2][4];
+    const int tid = threadIdx.x, g = tid / L, sub = tid % L;
+    const int64_t t = (int64_t)blockIdx.x * NG + g;
+    const Seqs sq{a.off, a.S, a.T};
+    const bool staged = a.off && a.S <= kSeqLds;
+    int live = 1, valid = a.T;
+    if (a.off) {
+        live = valid = 0;
+        for (int i = tid; i < a.S; i += 256) {
+            const int b = sq.begin(i), len = sq.end(i) - b;
+            live += len > 0;
+            valid += len;
+            if (staged) s_off[i] = b;
+        }
+        if (staged && tid == 0) s_off[a.S] = sq.at(a.S);
+#pragma unroll
+        for (int o = 32; o; o >>= 1) {
+            live += __shfl_xor(live, o);
+            valid += __shfl_xor(valid, o);
+        }
+        if ((tid & 63) == 0) {
+            s_n[0][tid >> 6] = live;
+            s_n[1][tid >> 6] = valid;
+        }
+        __syncthreads();
+        live = s_n[0][0] + s_n[0][1] + s_n[0][2] + s_n[0][3];
+        valid = s_n[1][0] + s_n[1][1] + s_n[1][2] + s_n[1][3];
+    }
+    if (t >= a.T) return;
+    const Seqs sl{staged ? s_off : a.off, a.S, a.T};
+    const int s = sl.find((int)t), t0 = sl.begin(s), t1 = sl.end(s);
+    float d[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) d[i] = 0.f;
+    if (t >= t0 && t < t1) {
+        const bool sig = a.scoring == MOE_SCORING_SIGMOID;
+        float l[N], v[N], sc[N], om[N], shift;   // om: 1 - s for the sigmoid, 1 for softmax
+        load_row<L, Q, VEC>(a.logits + t * a.E, a.E, sub, -INFINITY, l);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = l[i];
+        const float sum = softmax_row<L, Q>(v, shift);
+        const float inv = sum != 0.f ? 1.0f / sum : 0.f;
+        float pinv = inv;
+        if (sig) {
+            float z = 0.f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float ex = expf(-l[i]);
+                sc[i] = 1.0f / (1.0f + ex);
+                om[i] = ex < INFINITY ? ex * sc[i] : 1.0f - sc[i];
+                z += sc[i];
+            }
+            z = rsum<L>(z);
+            pinv = z != 0.f ? 1.0f / z : 0.f;
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                sc[i] = v[i];
+                om[i] = 1.0f;
+            }
+        }
+        if (a.counts) {
+            const float len = (float)(t1 - t0);
+            const float cu = a.ca / (float)live * ((float)a.E / (float)a.k) / len / len;
+            int c[N];
+            load_row<L, Q, VEC>(a.counts + (int64_t)s * a.E, a.E, sub, 0, c);
+            float pu = 0.f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) pu = fmaf(sc[i] * pinv, cu * (float)c[i], pu);
+            pu = rsum<L>(pu);
+#pragma unroll
+            for (int i = 0; i < N; ++i) d[i] = sc[i] * pinv * om[i] * (cu * (float)c[i] - pu);
+        }
+        if (a.cz != 0.f && sum != 0.f) {
+            const float cz = 2.0f * a.cz / (float)valid * (shift + logf(sum)) * inv;
+#pragma unroll
+            for (int i = 0; i < N; ++i) d[i] = fmaf(cz, v[i], d[i]);
+        }
+        if (a.dw) {
+            float D[N], m[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) D[i] = m[i] = 0.f;
+            for (int j = 0; j < a.k; ++j) {
+                const int id = a.ids[t * a.k + j];
+                const float w = a.dw[t * a.k + j];
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const bool hit = id == 4 * (sub + L * (i / 4)) + (i & 3);
+                    D[i] += hit ? w : 0.f;
+                    m[i] += hit ? 1.f : 0.f;
+                }
+            }
+            if (!sig && !a.renorm) {
+                float pd = 0.f;
+#pragma unroll
+                for (int i = 0; i < N; ++i) pd = fmaf(v[i] * inv, D[i], pd);
+                pd = rsum<L>(pd);
+#pragma unroll
+                for (int i = 0; i < N; ++i) d[i] = fmaf(a.rsf * v[i] * inv, D[i] - pd, d[i]);
+            } else {
+                float q[N], mx = -INFINITY, z = 0.f, qd = 0.f;
+                if (!sig) {   // shifted by the largest chosen logit, as the forward weights are
+#pragma unroll
+                    for (int i = 0; i < N; ++i) mx = m[i] > 0.f ? fmaxf(mx, l[i]) : mx;
+                    mx = rmax<L>(mx);
+                    if (mx == -INFINITY) mx = 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    q[i] = m[i] > 0.f ? (sig ? sc[i] : expf(l[i] - mx)) : 0.f;
+                    z = fmaf(m[i], q[i], z);
+                    qd = fmaf(q[i], D[i], qd);
+                }
+                z = rsum<L>(z);
+                qd = rsum<L>(qd);
+                const float zi = z != 0.f ? 1.0f / z : 0.f;
+                qd *= zi;
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    d[i] = fmaf(a.rsf * q[i] * zi * om[i], D[i] - m[i] * qd, d[i]);
+            }
+        }
+    }
+    float* o = a.dlogits + t * a.E;
+#pragma unroll
+    for (int i = 0; i < Q; ++i) {
+        const int e = 4 * (sub + L * i);
+        if constexpr (VEC) {
+            if (e < a.E) *reinterpret_cast<float4*>(o + e) = make_float4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]);
+        } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (e + c < a.E) o[e + c] = d[4 * i + c];
+        }
+    }
+}
+
+hipError_t launch_route_backward(const RouteBwdArgs& a, hipStream_t st) {
+    const bool v = vec4(a.logits, a.E) && vec4(a.dlogits, a.E) && (!a.counts || vec4(a.counts, a.E));
+#define MOE_CALL(L, Q, V) \
+    hipLaunchKernelGGL((k_route_bwd<L, Q, V>), dim3((unsigned)ceil_div(a.T, 256 / L)), dim3(256), 0, st, a)
+    MOE_ROW_DISPATCH(a.E, v, MOE_CALL);
+#undef MOE_CALL
+    return hipGetLastError();
+}
+
+// ----------------------------------------------------------------------------------------
+// Gradients of the combine: G threads per token walk its columns 8 at a time; up to 8 expert rows
+// are in flight per column vector, so dy is read once for every 8 slots.  Bound by HBM: the expert
+// rows are read once and (dexpert_out) written once.
+typedef unsigned v4u_t __attribute__((ext_vector_type(4)));
+template <bool BF16, int G, bool DOUT>
+__global__ __launch_bounds__(256) void k_combine_bwd(CombineBwdArgs a) {
+    constexpr int RPB = 256 / G;
+    __shared__ float s_dot[4][8];
+    const int sub = threadIdx.x % G;
+    const int64_t t = (int64_t)blockIdx.x * RPB + threadIdx.x / G;
+    if (RPB > 1 && t >= a.T) return;   // (no barrier follows with G = 64)
+    const int nv = a.H >> 3;
+    const int64_t A = (int64_t)a.T * a.k;
+    for (int j0 = 0; j0 < a.k; j0 += 8) {
+        int64_t p[8];
+        float wj[8], dot[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int64_t f = t * a.k + j0 + u;
+            p[u] = j0 + u < a.k ? a.pos[f] : -1;
+            if (p[u] >= A) p[u] = -1;
+            wj[u] = DOUT && p[u] >= 0 ? a.wt[f] : 0.f;
+            dot[u] = 0.f;
+        }
+        for (int v = sub; v < nv; v += G) {
+            v4u_t e[8][BF16 ? 1 : 2];
+            if (a.dwt) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    if (p[u] >= 0) {
+                        const v4u_t* src = reinterpret_cast<const v4u_t*>(
+                            reinterpret_cast<const uint8_t*>(a.eo) + (p[u] * a.H + v * 8) * (BF16 ? 2 : 4));
+                        e[u][0] = __builtin_nontemporal_load(src);
+                        if constexpr (!BF16) e[u][1] = __builtin_nontemporal_load(src + 1);
+                    } else {
+                        e[u][0] = v4u_t{0, 0, 0, 0};
+                        if constexpr (!BF16) e[u][1] = v4u_t{0, 0, 0, 0};
+                    }
+                }
+            }
+            float d[8];
+            unpack8(*reinterpret_cast<const uint4*>(a.dy + t * a.H + v * 8), d);
+            if (a.dwt) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float x;
+                        if constexpr (BF16)
+                            x = i & 1 ? __uint_as_float(e[u][0][i / 2] & 0xFFFF0000u) : __uint_as_float(e[u][0][i / 2] << 16);
+                        else
+                            x = __uint_as_float(e[u][i / 4][i & 3]);
+                        dot[u] = fmaf(d[i], x, dot[u]);
+                    }
+                }
+            }
+            if constexpr (DOUT) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    if (p[u] >= 0) {
+                        v4u_t* dst = reinterpret_cast<v4u_t*>(reinterpret_cast<uint8_t*>(a.deo) +
+                                                              (p[u] * a.H + v * 8) * (BF16 ? 2 : 4));
+                        if constexpr (BF16) {
+                            __builtin_nontemporal_store(v4u_t{pack_bf16(wj[u] * d[0], wj[u] * d[1]), pack_bf16(wj[u] * d[2], wj[u] * d[3]),
+                                                              pack_bf16(wj[u] * d[4], wj[u] * d[5]), pack_bf16(wj[u] * d[6], wj[u] * d[7])}, dst);
+                        } else {
+#pragma unroll
+                            for (int q = 0; q < 2; ++q)
+                                __builtin_nontemporal_store(
+                                    v4u_t{__float_as_uint(wj[u] * d[4 * q]), __float_as_uint(wj[u] * d[4 * q + 1]),
+                                          __float_as_uint(wj[u] * d[4 * q + 2]), __float_as_uint(wj[u] * d[4 * q + 3])}, dst + q);
+                        }
+                    }
+                }
+            }
+        }
+        if (a.dwt) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) dot[u] = wave_sum(dot[u]);
+            if constexpr (G > 64) {
+                if (j0) __syncthreads();   // the previous slots' sums have been read
+                if ((sub & 63) == 0) {
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) s_dot[sub >> 6][u] = dot[u];
+                }
+                __syncthreads();
+#pragma unroll
+                for (int u = 0; u < 8; ++u) dot[u] = (s_dot[0][u] + s_dot[1][u]) + (s_dot[2][u] + s_dot[3][u]);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (sub == u && j0 + u < a.k) a.dwt[t * a.k + j0 + u] = p[u] >= 0 ? dot[u] : 0.f;
+        }
+    }
+}
+
+template <bool BF16, int G>
+static void run_combine_bwd(const CombineBwdArgs& a, hipStream_t st) {
+    const dim3 grid((unsigned)ceil_div(a.T, 256 / G));
+    if (a.deo) hipLaunchKernelGGL((k_combine_bwd<BF16, G, true>), grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((k_combine_bwd<BF16, G, false>), grid, dim3(256), 0, st, a);
+}
+
+hipError_t launch_combine_backward(const CombineBwdArgs& a, hipStream_t st) {
+    const bool wide = a.H > 1024;
+    if (a.bf16) {
+        if (wide) run_combine_bwd<true, 256>(a, st);
+        else run_combine_bwd<true, 64>(a, st);
+    } else {
+        if (wide) run_combine_bwd<false, 256>(a, st);
+        else run_combine_bwd<false, 64>(a, st);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace moe
