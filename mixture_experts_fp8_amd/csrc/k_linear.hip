@@ -9,85 +9,111 @@
 #include "layer_common.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace moe {
 
 typedef int v4i_t __attribute__((ext_vector_type(4)));
+typedef unsigned v4u_t __attribute__((ext_vector_type(4)));
 
+// exp(x) by the base-2 instruction: the product's rounding moves the result by |x| 2^-24 of it, which
+// the activations below multiply by at most x exp(-|x|).
+__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+
+// The activations take one or two transcendental instructions: with library exp, erfc and division
+// the epilogue of a 768-deep product cost as much as its K loop.
 __device__ __forceinline__ float act_fn(float v, int act) {
     switch (act) {
         case MOE_ACT_RELU: return v < 0.f ? 0.f : v;
-        case MOE_ACT_SILU: return v / (1.0f + expf(-v));
-        case MOE_ACT_GELU: return 0.5f * v * erfcf(-0.70710678118654752f * v);
+        case MOE_ACT_SILU: return v * __builtin_amdgcn_rcpf(1.0f + exp_fast(-v));
+        case MOE_ACT_GELU: {
+            // erf by Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26 (|error| <= 1.5e-7):
+            // erfc(z) = (a1 t + ... + a5 t^5) exp(-z^2), t = 1 / (1 + p z), z >= 0
+            const float z = fabsf(v) * 0.70710678f, t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, z, 1.0f));
+            float p = fmaf(1.061405429f, t, -1.453152027f);
+            p = fmaf(p, t, 1.421413741f);
+            p = fmaf(p, t, -0.284496736f);
+            p = fmaf(p, t, 0.254829592f);
+            const float c = 0.5f * p * t * exp_fast(-z * z);     // erfc(z) / 2
+            return v * (v < 0.f ? c : 1.0f - c);
+        }
         case MOE_ACT_GELU_TANH: {   // (1 + tanh u) / 2 = 1 / (1 + exp(-2 u))
-            const float u = 0.79788456080286536f * fmaf(0.044715f * v * v, v, v);
-            return v / (1.0f + expf(-2.0f * u));
+            const float u = 0.79788456f * fmaf(0.044715f * v * v, v, v);
+            return v * __builtin_amdgcn_rcpf(1.0f + exp_fast(-2.0f * u));
         }
         default: return v;
     }
 }
 
-// One output element: act(acc + bias) + residual, stored in y's type.
-__device__ __forceinline__ void put(const LinArgs& a, int row, int col, float v, float bias) {
-    v = act_fn(v + bias, a.act);
+// Four consecutive columns of a row: act(v + bias) + residual, stored in y's type.
+__device__ __forceinline__ void put4(const LinArgs& a, int64_t row, int col, v4f v) {
+    if (a.bias) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += a.bias[col + i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = act_fn(v[i], a.act);
     if (a.out_bf16) {
-        if (a.res) v += bf16_to_f32(reinterpret_cast<const uint16_t*>(a.res)[(int64_t)row * a.ldr + col]);
-        reinterpret_cast<uint16_t*>(a.y)[(int64_t)row * a.ldy + col] = (uint16_t)pack_bf16(v, v);
+        if (a.res) {
+            const uint2 r = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(a.res) + row * a.ldr + col);
+            v[0] += __uint_as_float(r.x << 16);
+            v[1] += __uint_as_float(r.x & 0xFFFF0000u);
+            v[2] += __uint_as_float(r.y << 16);
+            v[3] += __uint_as_float(r.y & 0xFFFF0000u);
+        }
+        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.y) + row * a.ldy + col) =
+            make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
     } else {
-        if (a.res) v += reinterpret_cast<const float*>(a.res)[(int64_t)row * a.ldr + col];
-        reinterpret_cast<float*>(a.y)[(int64_t)row * a.ldy + col] = v;
+        if (a.res) v += *reinterpret_cast<const v4f*>(reinterpret_cast<const float*>(a.res) + row * a.ldr + col);
+        *reinterpret_cast<v4f*>(reinterpret_cast<float*>(a.y) + row * a.ldy + col) = v;
     }
 }
 
 // Operands straight from memory into registers, no LDS in the K loop: workgroup (column tile of
 // 16 NF, row tile of 16 MF), whose WK waves take the K blocks in turn and add their sums through
-// LDS in wave order.  PF K blocks are in flight per wave; blocks past the end read as zeros
-// (outside the descriptors' range).
+// LDS in wave order.  PF K blocks are in flight per wave.
 template <bool MX, int MF, int NF, int WK, int PF>
 __global__ __launch_bounds__(64 * WK) void k_linear_stream(LinArgs a) {
     __shared__ __align__(16) v4f s_acc[WK][MF * NF][64];
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r16 = lane & 15, G = lane >> 4, KB = a.K / kGroup;
     const int n0 = blockIdx.x * NF, m0 = blockIdx.y * MF * 16, n16s = a.N / 16;
-    const rsrc_t ra = make_rsrc(a.xq, (uint32_t)a.T * (uint32_t)a.K);
+    constexpr int gpb = MX ? 4 : 1;   // row scales per K block
+    const int nbs = (a.N + kGroup - 1) / kGroup;
+    const rsrc_t rx = make_rsrc(a.xq, (uint32_t)a.T * (uint32_t)a.K);
     const rsrc_t rw = make_rsrc(a.w, (uint32_t)a.K * (uint32_t)a.N);
-    const int gpb = MX ? 4 : 1, nbs = (a.N + kGroup - 1) / kGroup;   // A scales per K block
     const rsrc_t rxs = make_rsrc(a.xs, (uint32_t)a.T * (uint32_t)(KB * gpb));
     const rsrc_t rws = make_rsrc(a.ws, MX ? (uint32_t)KB * (uint32_t)n16s * 64u : (uint32_t)KB * (uint32_t)nbs);
-    constexpr uint32_t kOut = 0x80000000u;   // past every descriptor's end
-    uint32_t aoff[MF], xoff[MF], boff[NF], soff[NF];
+    uint32_t xoff[MF], xsoff[MF], wfrag[NF];
 #pragma unroll
     for (int i = 0; i < MF; ++i) {
-        const uint32_t row = (uint32_t)min(m0 + i * 16 + r16, a.T - 1);
-        aoff[i] = row * (uint32_t)a.K + (MX ? 16 * G : 32 * G);
-        xoff[i] = row * (uint32_t)(KB * gpb) + (MX ? G : 0);
+        const uint32_t row = (uint32_t)min(m0 + i * 16 + r16, a.T - 1);   // (rows past the end: not stored)
+        xoff[i] = row * (uint32_t)a.K + (MX ? 16 * G : 32 * G);
+        xsoff[i] = row * (uint32_t)(KB * gpb) + (MX ? G : 0);
     }
 #pragma unroll
-    for (int j = 0; j < NF; ++j) {
-        const uint32_t n16 = (uint32_t)min(n0 + j, n16s - 1);
-        boff[j] = n16 * (uint32_t)KB * kFragBytes + 16 * lane;
-        soff[j] = MX ? n16 * (uint32_t)KB * 64 + lane : n16 / 8;
-    }
-    v8i A[PF][MF], B[PF][NF];
-    int sa[PF][MF], sb[PF][NF];
-    auto load = [&](int p, int kb) __attribute__((always_inline)) {
-        const bool in = kb < KB;
-        const uint32_t k = (uint32_t)kb;
+    for (int j = 0; j < NF; ++j)
+        wfrag[j] = __builtin_amdgcn_readfirstlane((uint32_t)min(n0 + j, n16s - 1));
+    const uint32_t l16 = 16 * lane;
+    v8i X[PF][MF], W[PF][NF];
+    uint8_t sx[PF][MF], sw[PF][NF];   // widened at their use: done at the load, that waits for it
+    auto load = [&](int p, int blk) __attribute__((always_inline)) {
+        const uint32_t kb = (uint32_t)min(blk, KB - 1);   // (past the end the last block again, unused)
 #pragma unroll
         for (int j = 0; j < NF; ++j) {
-            const uint32_t o = in ? boff[j] + k * kFragBytes : kOut;
-            const v4i_t lo = __builtin_amdgcn_raw_buffer_load_b128(rw, o, 0, MOE_WLOAD_AUX);
-            const v4i_t hi = __builtin_amdgcn_raw_buffer_load_b128(rw, o + 1024, 0, MOE_WLOAD_AUX);
-            B[p][j] = v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-            sb[p][j] = __builtin_amdgcn_raw_buffer_load_b8(rws, in ? soff[j] + (MX ? k * 64 : k * nbs) : kOut, 0, 0);
+            const uint32_t f = (wfrag[j] * (uint32_t)KB + kb);
+            const v4i_t lo = __builtin_amdgcn_raw_buffer_load_b128(rw, l16, f * kFragBytes, MF > 2 ? 0 : MOE_WLOAD_AUX);
+            const v4i_t hi = __builtin_amdgcn_raw_buffer_load_b128(rw, l16 + 1024, f * kFragBytes, MF > 2 ? 0 : MOE_WLOAD_AUX);
+            W[p][j] = v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            sw[p][j] = MX ? __builtin_amdgcn_raw_buffer_load_b8(rws, lane, f * 64, 0)
+                          : __builtin_amdgcn_raw_buffer_load_b8(rws, 0, kb * nbs + wfrag[j] / 8, 0);
         }
 #pragma unroll
         for (int i = 0; i < MF; ++i) {
-            const uint32_t o = in ? aoff[i] + k * kGroup : kOut;
-            const v4i_t lo = __builtin_amdgcn_raw_buffer_load_b128(ra, o, 0, 0);
-            const v4i_t hi = __builtin_amdgcn_raw_buffer_load_b128(ra, o + (MX ? 64 : 16), 0, 0);
-            A[p][i] = v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-            sa[p][i] = __builtin_amdgcn_raw_buffer_load_b8(rxs, in ? xoff[i] + k * gpb : kOut, 0, 0);
+            const v4i_t lo = __builtin_amdgcn_raw_buffer_load_b128(rx, xoff[i], kb * kGroup, 0);
+            const v4i_t hi = __builtin_amdgcn_raw_buffer_load_b128(rx, xoff[i] + (MX ? 64 : 16), kb * kGroup, 0);
+            X[p][i] = v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            sx[p][i] = __builtin_amdgcn_raw_buffer_load_b8(rxs, xsoff[i], kb * gpb, 0);
         }
     };
     v4f acc[MF][NF];
@@ -95,18 +121,30 @@ __global__ __launch_bounds__(64 * WK) void k_linear_stream(LinArgs a) {
     for (int i = 0; i < MF; ++i)
 #pragma unroll
         for (int j = 0; j < NF; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    auto products = [&](int p) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < MF; ++i)
+#pragma unroll
+            for (int j = 0; j < NF; ++j) acc[i][j] = mfma_fp8(W[p][j], X[p][i], acc[i][j], sw[p][j], sx[p][i]);
+    };
+    const int nk = KB > wv ? (KB - wv + WK - 1) / WK : 0;   // blocks wv, wv + WK, ... of this wave
 #pragma unroll
     for (int p = 0; p < PF; ++p) load(p, wv + p * WK);
-    for (int kb = wv; kb < KB; kb += WK * PF) {
+    int i0 = 0;
+    for (; i0 + PF <= nk; i0 += PF) {
 #pragma unroll
         for (int p = 0; p < PF; ++p) {
-#pragma unroll
-            for (int i = 0; i < MF; ++i)
-#pragma unroll
-                for (int j = 0; j < NF; ++j) acc[i][j] = mfma_fp8(A[p][i], B[p][j], acc[i][j], sa[p][i], sb[p][j]);
-            load(p, kb + (p + PF) * WK);
+            products(p);
+            // (kept in this order: hoisted over the products, the loads take registers of their own, and
+            // the copies back wait for all of them)
+            __builtin_amdgcn_sched_barrier(0);
+            load(p, wv + (i0 + p + PF) * WK);
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
+#pragma unroll
+    for (int p = 0; p < PF; ++p)
+        if (i0 + p < nk) products(p);
 #pragma unroll
     for (int i = 0; i < MF; ++i)
 #pragma unroll
@@ -116,28 +154,423 @@ __global__ __launch_bounds__(64 * WK) void k_linear_stream(LinArgs a) {
         v4f v = s_acc[0][q][lane];
 #pragma unroll
         for (int w = 1; w < WK; ++w) v += s_acc[w][q][lane];
-        const int i = q / NF, j = q - i * NF, col = (n0 + j) * 16 + r16, row = m0 + i * 16 + 4 * G;
-        if (n0 + j < n16s) {
-            const float b = a.bias ? a.bias[col] : 0.f;
+        const int i = q / NF, j = q - i * NF, col = (n0 + j) * 16 + 4 * G, row = m0 + i * 16 + r16;
+        if (n0 + j < n16s && row < a.T) put4(a, row, col, v);
+    }
+}
+
+// ----------------------------------------------------------------------------------------
+// Tiled kernel for many rows.  Workgroup of WM x WN waves, each 16 MI rows x 16 NJ columns.  The
+// instruction's first operand is the weights and its second the activations, so a lane of the
+// accumulator holds row l % 16 of a fragment and four consecutive columns, 4 (l / 16) ...: the
+// epilogue then works on whole vectors of a row, without LDS.
+//   * Activations: every row fragment is read by WN waves, so they go through LDS, three stages of
+//     one K block, filled by LDS-DMA two blocks ahead.  A row's 16-byte chunks stand at
+//     slot ^ (row % 8), where chunk c has slot c (32-element scales) or c / 2 + 4 (c % 2): a lane
+//     needs slots l / 16 and l / 16 + 4 in both cases, without bank conflicts.
+//   * Weights: a fragment is read by WM waves only, and its packed order is the operand's, so it goes
+//     straight to registers one block ahead: staging it too would make the LDS the bound (two waves
+//     per SIMD read 24 KB of operands per 32 instructions otherwise).
+//   * The first row fragments of block kb + 1 are read during block kb, so that matrix instructions
+//     follow the barrier at once.
+__device__ __forceinline__ v4i_t make_srd(const void* base, uint32_t bytes) {
+    const uint64_t b = reinterpret_cast<uint64_t>(base);
+    v4i_t r;
+    r[0] = (int)__builtin_amdgcn_readfirstlane((uint32_t)b);
+    r[1] = (int)(__builtin_amdgcn_readfirstlane((uint32_t)(b >> 32)) & 0xFFFFu);   // stride 0
+    r[2] = (int)__builtin_amdgcn_readfirstlane(bytes);
+    r[3] = 0x00020000;
+    return r;
+}
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+    return (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void*)p);
+}
+// Bytes from the buffer at voff + soff into LDS at base + (16 or 4) * lane.  The compiler does not
+// see these loads: their end is awaited by wait_all and a barrier before the LDS is read.
+__device__ __forceinline__ void dma16(const v4i_t& srd, uint32_t base, uint32_t voff, uint32_t soff) {
+    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :
+                 : "s"(base), "v"(voff), "s"(srd), "s"(soff)
+                 : "memory", "m0");
+}
+__device__ __forceinline__ void dma4(const v4i_t& srd, uint32_t base, uint32_t voff, uint32_t soff) {
+    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+                 :
+                 : "s"(base), "v"(voff), "s"(srd), "s"(soff)
+                 : "memory", "m0");
+}
+__device__ __forceinline__ void wait_all() { asm volatile("s_waitcnt vmcnt(0)" : : : "memory"); }
+
+// The product with the weights' scale in byte 0 of sw and the rows' in byte bx of sx (bx is a constant
+// after unrolling).
+__device__ __forceinline__ v4f mfma_wx(v8i w, v8i x, v4f acc, int sw, int sx, int bx) {
+    switch (bx) {
+        case 0: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, acc, 0, 0, 0, sw, 0, sx);
+        case 1: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, acc, 0, 0, 0, sw, 1, sx);
+        case 2: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, acc, 0, 0, 0, sw, 2, sx);
+        default: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, acc, 0, 0, 0, sw, 3, sx);
+    }
+}
+
+// 4 x 4 transpose between the registers r[0..3] and the four groups of 16 lanes: r[i] of group g
+// becomes what r[g] of group i was.
+__device__ __forceinline__ void transpose_groups(uint32_t (&r)[4]) {
+    auto swap32 = [](uint32_t& a, uint32_t& b) {
+        auto v = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+        a = v[0];
+        b = v[1];
+    };
+    auto swap16 = [](uint32_t& a, uint32_t& b) {
+        auto v = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+        a = v[0];
+        b = v[1];
+    };
+    swap32(r[0], r[2]);
+    swap32(r[1], r[3]);
+    swap16(r[0], r[1]);
+    swap16(r[2], r[3]);
+}
+
+__device__ __forceinline__ void store16(v4u_t* d, v4u_t v, int nt) {
+    if (nt) __builtin_nontemporal_store(v, d);
+    else *d = v;
+}
+
+// Epilogue of a wave's 64 columns col0 .. (of which those below N exist; N is a multiple of 16).
+// acc[mi][j]: columns col0 + 16 j + 4 G .. +3 of row row0 + 16 mi.
+//   bf16: the four groups of 16 lanes are transposed against the four column fragments, so that lane
+//   group G holds the 16 columns of fragment G, 32 bytes: residual and output move as 16-byte vectors.
+//   float32: a lane's four columns are 16 bytes already.
+// The residual of all rows is requested before the first one is used.
+template <int MI>
+__device__ __forceinline__ void tile_residual(const LinArgs& a, uint4 (&q)[MI][2], int row0, int col0) {
+    const int G = (threadIdx.x & 63) >> 4;
+    const bool on = col0 + 16 * G < a.N;
+    if (a.out_bf16 && a.res) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                if (row + r < a.T) put(a, row + r, col, v[r], b);
+        for (int mi = 0; mi < MI; ++mi) {
+            q[mi][0] = q[mi][1] = make_uint4(0, 0, 0, 0);
+            if (on && row0 + 16 * mi < a.T) {
+                const uint4* s = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.res) +
+                                                                (row0 + 16 * mi) * a.ldr + col0 + 16 * G);
+                q[mi][0] = s[0];
+                q[mi][1] = s[1];
+            }
+        }
+    }
+}
+template <int MI, int ACT>
+__device__ __forceinline__ void tile_epilogue(const LinArgs& a, v4f (&acc)[MI][4], const v4f (&b)[4], uint4 (&q)[MI][2],
+                                              int row0, int col0) {
+    const int G = (threadIdx.x & 63) >> 4;
+    const bool bf = a.out_bf16, on = col0 + 16 * G < a.N;
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) {
+        const int64_t row = row0 + 16 * mi;
+        const bool live = row < a.T;
+        v4f (&v)[4] = acc[mi];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[j][i] = act_fn(v[j][i] + b[j][i], ACT);
+        if (bf) {
+            uint32_t lo[4], hi[4];
+            if (a.res) {
+                lo[0] = q[mi][0].x, hi[0] = q[mi][0].y, lo[1] = q[mi][0].z, hi[1] = q[mi][0].w;
+                lo[2] = q[mi][1].x, hi[2] = q[mi][1].y, lo[3] = q[mi][1].z, hi[3] = q[mi][1].w;
+                transpose_groups(lo);
+                transpose_groups(hi);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    v[j][0] += __uint_as_float(lo[j] << 16);
+                    v[j][1] += __uint_as_float(lo[j] & 0xFFFF0000u);
+                    v[j][2] += __uint_as_float(hi[j] << 16);
+                    v[j][3] += __uint_as_float(hi[j] & 0xFFFF0000u);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                lo[j] = pack_bf16(v[j][0], v[j][1]);
+                hi[j] = pack_bf16(v[j][2], v[j][3]);
+            }
+            transpose_groups(lo);
+            transpose_groups(hi);
+            if (on && live) {
+                v4u_t* d = reinterpret_cast<v4u_t*>(reinterpret_cast<uint16_t*>(a.y) + row * a.ldy + col0 + 16 * G);
+                store16(d, v4u_t{lo[0], hi[0], lo[1], hi[1]}, a.nt);
+                store16(d + 1, v4u_t{lo[2], hi[2], lo[3], hi[3]}, a.nt);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int col = col0 + 16 * j + 4 * G;
+                if (live && col < a.N) {
+                    if (a.res) v[j] += *reinterpret_cast<const v4f*>(reinterpret_cast<const float*>(a.res) + row * a.ldr + col);
+                    store16(reinterpret_cast<v4u_t*>(reinterpret_cast<float*>(a.y) + row * a.ldy + col),
+                            __builtin_bit_cast(v4u_t, v[j]), a.nt);
+                }
+            }
         }
     }
 }
 
+template <bool MX, int MI, int NJ, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_tile(LinArgs a, int tiles_m, int tiles_n) {
+    static_assert(NJ == 4, "the epilogue takes 64 columns");
+    constexpr int NW = WM * WN, ROWS = 16 * MI * WM, NTH = 64 * NW, DMA = ROWS * 8 / NTH;
+    constexpr int STAGE = ROWS * kGroup, SCST = MX ? ROWS * 4 : 0;
+    static_assert(ROWS * 8 % NTH == 0 && (!MX || ROWS % 64 == 0), "whole copies");
+    extern __shared__ __align__(16) uint8_t smem[];
+    uint8_t* s_a = smem;                       // [3][ROWS][128]
+    uint8_t* s_x = smem + 3 * STAGE;           // MX: [3][WM][16][MI] dwords; else [KB][WM][16][MI] bytes
+    const int KB = a.K / kGroup, nbs = (a.N + kGroup - 1) / kGroup;
+    constexpr int COLS = 16 * NJ * WN, NBW = (COLS + 127) / 128;
+    uint8_t* s_w = s_x + KB * ROWS;            // (128-element scales) [KB][column blocks of the tile]
+    float* s_bias = reinterpret_cast<float*>(MX ? s_x + 3 * SCST : s_w + (KB * NBW + 15) / 16 * 16);   // [COLS]
+
+    // Work order: workgroup L runs on XCD L % 8; XCD x takes a contiguous share of the list, which walks
+    // the row tiles in groups of 8 with the column tile outside, so that one XCD's workgroups share both
+    // operands through its L2.
+    int tm, tn;
+    {
+        const int total = tiles_m * tiles_n, per = (total + 7) / 8, L = blockIdx.x;
+        const int w = (L & 7) * per + (L >> 3);
+        if ((L >> 3) >= per || w >= total) return;
+        const int sb = w / (8 * tiles_n), r = w - sb * 8 * tiles_n, g = min(8, tiles_m - sb * 8);
+        tn = r / g;
+        tm = sb * 8 + r - tn * g;
+    }
+    // Two workgroups share a CU.  The one that was dealt second runs ahead at equal work, so that their
+    // epilogues (memory) and K loops (matrix cores) fall apart: 262 -> 258 us at 16384 x 4096 x 4096.
+    if (MI > 4 && ((blockIdx.x >> 8) & 1)) __builtin_amdgcn_s_setprio(1);
+    const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wv / WN, wn = wv % WN, r16 = lane & 15, G = lane >> 4, x8 = r16 & 7;
+    const int m0 = tm * ROWS, n0 = tn * COLS, n16s = a.N / 16;
+    constexpr int gpb = MX ? 4 : 1;
+
+    const v4i_t ra = make_srd(a.xq, (uint32_t)a.T * (uint32_t)a.K);
+    const v4i_t rs = make_srd(a.xs, (uint32_t)a.T * (uint32_t)(KB * gpb));
+    const rsrc_t rw = make_rsrc(a.w, (uint32_t)a.K * (uint32_t)a.N);
+    const rsrc_t rws = make_rsrc(a.ws, MX ? (uint32_t)KB * (uint32_t)n16s * 64u : (uint32_t)KB * (uint32_t)nbs);
+
+    // copy i of wave wv: rows 8 (wv + NW i) .. +7; lane l brings one chunk of row + l / 8 to slot l % 8
+    uint32_t aoff[DMA];
+#pragma unroll
+    for (int i = 0; i < DMA; ++i) {
+        const int row = min(m0 + 8 * (wv + NW * i) + (lane >> 3), a.T - 1), slot = (lane & 7) ^ (lane >> 3);
+        const int chunk = MX ? slot : (slot < 4 ? 2 * slot : 2 * slot - 7);
+        aoff[i] = (uint32_t)row * (uint32_t)a.K + 16 * chunk;
+    }
+    const uint32_t lds_w = lds_addr(s_a) + wv * 1024;
+    uint32_t xoff = 0, lds_x = 0;   // MX: the row scales' dwords (waves past ROWS / 64 copy the last 64 again)
+    if constexpr (MX) {
+        const int pos = min(wv, ROWS / 64 - 1) * 64 + lane;   // [wm][row % 16][fragment]
+        const int row = min(m0 + pos / (16 * MI) * (16 * MI) + (pos % MI) * 16 + (pos / MI) % 16, a.T - 1);
+        xoff = (uint32_t)row * (uint32_t)(KB * 4);
+        lds_x = lds_addr(s_x) + min(wv, ROWS / 64 - 1) * 256;
+    }
+    auto issue = [&](int kb, int st) __attribute__((always_inline)) {
+        const uint32_t base = __builtin_amdgcn_readfirstlane(lds_w + st * STAGE);
+#pragma unroll
+        for (int i = 0; i < DMA; ++i) dma16(ra, base + i * NW * 1024, aoff[i], kb * kGroup);
+        if constexpr (MX) {
+            dma4(rs, __builtin_amdgcn_readfirstlane(lds_x + st * SCST), xoff, kb * 4);
+        }
+    };
+    // weights: fragment j of the wave, the operand's packed order (fragments past the last column: the
+    // last one again, for columns that are not stored)
+    uint32_t wfrag[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+        wfrag[j] = __builtin_amdgcn_readfirstlane((uint32_t)min(n0 / 16 + wn * NJ + j, n16s - 1) * (uint32_t)KB);
+    const uint32_t l16 = 16 * lane;
+    struct Wt {
+        v8i w[NJ];
+        uint8_t s[NJ];
+    };
+    auto load_w = [&](int kb, Wt& W) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const uint32_t f = wfrag[j] + (uint32_t)kb;
+            const v4i_t lo = __builtin_amdgcn_raw_buffer_load_b128(rw, l16, f * kFragBytes, 0);
+            const v4i_t hi = __builtin_amdgcn_raw_buffer_load_b128(rw, l16 + 1024, f * kFragBytes, 0);
+            W.w[j] = v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            if constexpr (MX) W.s[j] = __builtin_amdgcn_raw_buffer_load_b8(rws, lane, f * 64, 0);
+        }
+    };
+    // Everything loaded so far has arrived; stating it as a use keeps the compiler from waiting again
+    // behind newer loads.
+    auto arrived = [&](Wt& W) __attribute__((always_inline)) {
+        wait_all();
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            asm volatile("" : "+v"(W.w[j]));
+        }
+    };
+    Wt W0, W1;
+    issue(0, 0);
+    issue(min(1, KB - 1), 1);
+    load_w(0, W0);
+    for (int i = tid; i < COLS; i += NTH) s_bias[i] = a.bias && n0 + i < a.N ? a.bias[n0 + i] : 0.f;
+    if constexpr (!MX) {   // scale tables of all K blocks: 8 threads per row of xs
+        const int c = tid & 7;
+        auto pos = [&](int q) { return (q / (16 * MI)) * 16 * MI + (q % 16) * MI + (q / 16) % MI; };
+        if (KB % 4 == 0 && (reinterpret_cast<uintptr_t>(a.xs) & 3) == 0) {
+            for (int k4 = c; k4 < KB / 4; k4 += 8) {
+                uint32_t v[ROWS * 8 / NTH];
+#pragma unroll
+                for (int i = 0; i < ROWS * 8 / NTH; ++i)
+                    v[i] = reinterpret_cast<const uint32_t*>(a.xs)[(int64_t)min(m0 + (tid >> 3) + i * (NTH / 8), a.T - 1) * (KB / 4) + k4];
+#pragma unroll
+                for (int i = 0; i < ROWS * 8 / NTH; ++i)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        s_x[(4 * k4 + k) * ROWS + pos((tid >> 3) + i * (NTH / 8))] = (uint8_t)(v[i] >> (8 * k));
+            }
+        } else {
+            for (int q = tid >> 3; q < ROWS; q += NTH / 8)
+                for (int kb = c; kb < KB; kb += 8)
+                    s_x[kb * ROWS + pos(q)] = a.xs[(int64_t)min(m0 + q, a.T - 1) * KB + kb];
+        }
+        for (int kb = tid; kb < KB; kb += NTH)
+#pragma unroll
+            for (int i = 0; i < NBW; ++i) s_w[kb * NBW + i] = a.ws[(int64_t)kb * nbs + min(n0 / kGroup + i, nbs - 1)];
+    }
+
+    v4f acc[MI][NJ];
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    auto frag = [&](int st, int mi) __attribute__((always_inline)) {
+        const uint8_t* rowp = s_a + st * STAGE + ((wm * MI + mi) * 16 + r16) * kGroup;
+        const uint4 lo = *reinterpret_cast<const uint4*>(rowp + ((G ^ x8) << 4));
+        const uint4 hi = *reinterpret_cast<const uint4*>(rowp + (((G + 4) ^ x8) << 4));
+        return v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+    };
+    // The residual: with registers to spare it is requested before the K loop, else behind it.
+    const int col0 = n0 + wn * NJ * 16, row0 = m0 + wm * MI * 16 + r16;
+    uint4 res[MI][2];
+    if constexpr (MI <= 4) tile_residual<MI>(a, res, row0, col0);
+    arrived(W0);
+    __syncthreads();
+    // Row fragments are taken P at a time, the next P being read meanwhile: 2, or 1 with 32-element
+    // scales, whose eight weight-scale registers leave no room for more (2 spilled 26 registers).
+    constexpr int P = MX ? 1 : 2;
+    v8i xa[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) xa[i] = frag(0, i);
+    int st = 0;
+    // One K block: on entry block kb is in its stage and W, its first row fragments in xa, and block
+    // kb + 1's copies have been issued before the last wait.
+    auto step = [&](int kb, Wt& W, Wt& N) __attribute__((always_inline)) {
+        const int s1 = st == 2 ? 0 : st + 1, s2 = s1 == 2 ? 0 : s1 + 1;
+        // (past the end the last block again, unused: the loop has no branches)
+        load_w(min(kb + 1, KB - 1), N);
+        issue(min(kb + 2, KB - 1), s2);
+        int sx[(MI + 3) / 4], sw = 0;   // 128-element scales: byte mi % 4 of sx[mi / 4]
+        if constexpr (!MX) {
+            const int* p = reinterpret_cast<const int*>(s_x + kb * ROWS + (wm * 16 + r16) * MI);
+#pragma unroll
+            for (int i = 0; i < MI / 4; ++i) sx[i] = p[i];
+            sw = s_w[kb * NBW + (wn * NJ * 16) / 128];
+        }
+        const uint32_t* mxs = reinterpret_cast<const uint32_t*>(s_x + st * SCST) + (wm * 16 + r16) * MI;
+#pragma unroll
+        for (int p = 0; p < MI; p += P) {
+            v8i xn[P];
+            int s[P];
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                s[i] = MX ? (int)(mxs[p + i] >> (8 * G)) : sx[p / 4];   // MX: byte G of the row's four
+                xn[i] = p + P < MI ? frag(st, p + P + i) : frag(s1, i);
+            }
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+                    acc[p + i][j] = mfma_wx(W.w[j], xa[i], acc[p + i][j], MX ? W.s[j] : sw, s[i], MX ? 0 : (p + i) & 3);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < P; ++i) xa[i] = xn[i];
+        }
+        arrived(N);
+        __syncthreads();
+        st = s1;
+    };
+    int kb = 0;
+    for (; kb + 2 <= KB; kb += 2) {
+        step(kb, W0, W1);
+        step(kb + 1, W1, W0);
+    }
+    if (kb < KB) step(kb, W0, W1);
+
+    if constexpr (MI > 4) tile_residual<MI>(a, res, row0, col0);
+    v4f bias[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) bias[j] = *reinterpret_cast<const v4f*>(s_bias + wn * NJ * 16 + 16 * j + 4 * G);
+    auto out = [&](auto A) __attribute__((always_inline)) {
+        tile_epilogue<MI, decltype(A)::value>(a, acc, bias, res, row0, col0);
+    };
+    switch (a.act) {
+        case MOE_ACT_RELU: out(std::integral_constant<int, MOE_ACT_RELU>{}); break;
+        case MOE_ACT_SILU: out(std::integral_constant<int, MOE_ACT_SILU>{}); break;
+        case MOE_ACT_GELU: out(std::integral_constant<int, MOE_ACT_GELU>{}); break;
+        case MOE_ACT_GELU_TANH: out(std::integral_constant<int, MOE_ACT_GELU_TANH>{}); break;
+        default: out(std::integral_constant<int, MOE_ACT_NONE>{});
+    }
+}
+
+template <bool MX, int MI, int NJ, int WM, int WN>
+static hipError_t run_tile_t(const LinArgs& a, hipStream_t st) {
+    constexpr int ROWS = 16 * MI * WM, COLS = 16 * NJ * WN;
+    const int tm = (int)ceil_div(a.T, ROWS), tn = (int)ceil_div(a.N, COLS), KB = a.K / kGroup;
+    const size_t lds = 3 * ROWS * kGroup + COLS * 4 +
+                       (MX ? 3 * ROWS * 4 : (size_t)KB * ROWS + (KB * ((COLS + 127) / 128) + 15) / 16 * 16);
+    auto kern = k_linear_tile<MX, MI, NJ, WM, WN>;
+    if (lds > 64 * 1024) {
+        const hipError_t e =
+            hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+        if (e != hipSuccess) return e;
+    }
+    const int64_t total = (int64_t)tm * tn;
+    hipLaunchKernelGGL(kern, dim3((unsigned)(ceil_div(total, 8) * 8)), dim3(64 * WM * WN), lds, st, a, tm, tn);
+    return hipGetLastError();
+}
+template <int MI, int NJ, int WM, int WN>
+static hipError_t run_tile(const LinArgs& a, hipStream_t st) {
+    return a.mx ? run_tile_t<true, MI, NJ, WM, WN>(a, st) : run_tile_t<false, MI, NJ, WM, WN>(a, st);
+}
+
 template <int MF, int NF, int WK, int PF>
-static void run_stream(const LinArgs& a, hipStream_t st) {
+static hipError_t run_stream(const LinArgs& a, hipStream_t st) {
     const dim3 grid((unsigned)ceil_div(a.N, 16 * NF), (unsigned)ceil_div(a.T, 16 * MF));
     if (a.mx) hipLaunchKernelGGL((k_linear_stream<true, MF, NF, WK, PF>), grid, dim3(64 * WK), 0, st, a);
     else hipLaunchKernelGGL((k_linear_stream<false, MF, NF, WK, PF>), grid, dim3(64 * WK), 0, st, a);
+    return hipGetLastError();
 }
 
-hipError_t launch_linear(const LinArgs& a, hipStream_t st) {
-    if (a.T <= 16) run_stream<1, 1, 8, 8>(a, st);
-    else if (a.T <= 32) run_stream<2, 1, 8, 4>(a, st);
-    else run_stream<4, 4, 4, 2>(a, st);
-    return hipGetLastError();
+// Variant by the number of workgroups that a tile size makes.  The stream kernel takes the smallest
+// tile that does not make more of them than there are CUs, 256 (below that a larger tile only
+// lengthens the one round: 32 x 4096 x 512 takes 6.7 us on 16 x 16 tiles and 11.7 on 32 x 32; above it
+// the operands are read again by every tile: 64 x 7168 x 7168 takes 20.7 us on 64 x 32 tiles, 224 of
+// them, and 37 on 16 x 32); no tile is taller than the rows need.  Beyond that the tiled kernel, two
+// of whose workgroups share a CU, by the same rule with 512 (192 x 7168 x 7168: 34 us, stream 45;
+// 384 x 2816 x 2816: 18.2, stream 22.8; 4096 x 4096 x 4096: 128 x 256 tiles 64, 64 x 128 tiles 88).
+hipError_t launch_linear(const LinArgs& args, hipStream_t st) {
+    LinArgs a = args;
+    // Outputs larger than the L2s together leave past them: they would evict the operands that the
+    // running tiles share (16384 x 4096 x 4096 in bf16: 238 -> 224 us).
+    a.nt = (int64_t)a.T * a.N * (a.out_bf16 ? 2 : 4) >= (32 << 20);
+    auto fits = [&](int rows, int cols, int64_t most) { return ceil_div(a.T, rows) * ceil_div(a.N, cols) <= most; };
+    if (fits(16, 16, 256)) return run_stream<1, 1, 4, 4>(a, st);
+    if (fits(16, 32, 256) || a.T <= 16) return run_stream<1, 2, 4, 4>(a, st);
+    if (fits(32, 32, 256) || a.T <= 32) return run_stream<2, 2, 4, 4>(a, st);
+    if (fits(64, 32, 256) || a.T <= 64) return run_stream<4, 2, 4, 3>(a, st);
+    if (fits(64, 64, 256)) return run_stream<4, 4, 4, 2>(a, st);
+    if (fits(64, 128, 512)) return run_tile<4, 4, 1, 2>(a, st);
+    if (fits(64, 256, 512)) return run_tile<4, 4, 1, 4>(a, st);
+    return run_tile<8, 4, 1, 4>(a, st);
 }
 
 }  // namespace moe

@@ -78,6 +78,7 @@ struct LinArgs {
     void* y;
     int64_t ldy;
     int act, out_bf16, mx;
+    int nt = 0;           // outputs past the caches (set by launch_linear)
 };
 hipError_t launch_linear(const LinArgs& a, hipStream_t st);
 

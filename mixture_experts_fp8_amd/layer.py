@@ -15,7 +15,7 @@ from typing import Optional
 import torch
 
 from . import binding as B
-from .binding import RouteParams, _check, _need, _ptr, _stream, lib, workspace
+from .binding import RouteParams, _check, _need, _ptr, lib, workspace
 
 MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH = range(5)
 ACTIVATIONS = {"none": MOE_ACT_NONE, "relu": MOE_ACT_RELU, "silu": MOE_ACT_SILU, "gelu": MOE_ACT_GELU,
@@ -60,6 +60,13 @@ class CombineBackwardArgs(ctypes.Structure):
                 ("stream", _vp)]
 
 
+# The current device and a device's current stream as plain integers, without building a Stream object
+# per call (a decode-sized call takes less time on the GPU than that takes on the host).
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 class _Call:
     """An operator's argument struct, its buffers and their device."""
 
@@ -73,10 +80,11 @@ class _Call:
         self._keep, self._dev = (tensors, keep), dev.index
 
     def _run(self, stream: Optional[int]) -> None:
-        if torch.cuda.current_device() != self._dev:   # the tensors' device, on its own current stream
-            with torch.cuda.device(self._dev):
+        dev = self._dev
+        if _current_device() != dev:   # run on the tensors' device, on its own current stream
+            with torch.cuda.device(dev):
                 return self._run(stream)
-        self.args.stream = _stream() if stream is None else stream
+        self.args.stream = _raw_stream(dev) if stream is None else stream
         rc = self._fn(self._ref)
         if rc:
             _check(rc)
