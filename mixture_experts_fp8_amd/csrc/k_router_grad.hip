@@ -59,6 +59,10 @@ struct Seqs {
     }
 };
 
+// exp(x) by the base-2 instruction: off by |x| 2^-24 and a unit in the last place, of which a softmax
+// sees its row's spread of logits.
+__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+
 // Softmax numerators of a row: v -> exp(v - max); returns their sum (0 only where every logit is
 // -infinity) and the shift.  NaN logits make the sum NaN.
 template <int L, int Q>
@@ -71,65 +75,94 @@ __device__ __forceinline__ float softmax_row(float (&v)[4 * Q], float& shift) {
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < 4 * Q; ++i) {
-        v[i] = expf(v[i] - shift);
+        v[i] = exp_fast(v[i] - shift);
         s += v[i];
     }
     return rsum<L>(s);
 }
 
+// Sums over a workgroup's threads, in wave order; s: one float per wave.
+template <int NW>
+__device__ __forceinline__ float block_sum(float v, float* s) {
+    v = wave_sum(v);
+    __syncthreads();   // (an earlier sum has been read)
+    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) v += s[i];
+    return v;
+}
+
+// losses from the sums over the sequences (bal: sum_s sum_e c P / T_s; z: sum of squared log-sums)
+__device__ __forceinline__ void put_losses(const BalanceArgs& a, float bal, float z, int live, int valid) {
+    bal = live ? a.ca * bal * ((float)a.E / (float)a.k) / (float)live : 0.f;
+    z = valid ? a.cz * z / (float)valid : 0.f;
+    a.losses[0] = bal + z;
+    a.losses[1] = bal;
+    a.losses[2] = z;
+}
+
 // ----------------------------------------------------------------------------------------
-// Sums of probabilities, counts and squared log-sums of each (workgroup, sequence) part.
-template <int L, int Q, bool VEC>
-__global__ __launch_bounds__(256) void k_balance_rows(BalanceArgs a, BalancePlan p) {
-    constexpr int NG = 256 / L, N = 4 * Q;
+// Sums of probabilities, counts and squared log-sums of each (workgroup, sequence) part, into the
+// part's slot.  ONE: a single workgroup holds all rows and writes the results itself, which saves the
+// second launch and its latency (64 x 8: 10 -> 4 us).
+constexpr int kRowsThreads = 512;
+template <int L, int Q, bool VEC, bool ONE>
+__global__ __launch_bounds__(kRowsThreads) void k_balance_rows(BalanceArgs a, BalancePlan p) {
+    constexpr int NT = kRowsThreads, NG = NT / L, N = 4 * Q;
     __shared__ __align__(16) float s_p[NG][L * N];
     __shared__ int s_hit[L * N];
-    __shared__ float s_z[NG];
+    __shared__ float s_z[NG], s_w[NT / 64];
     const int tid = threadIdx.x, g = tid / L, sub = tid % L, b = blockIdx.x;
-    if (b == 0 && tid == 0) *reinterpret_cast<int*>(a.ws + p.done) = 0;   // the second kernel's ticket
-    float* probs = reinterpret_cast<float*>(a.ws + p.probs);
-    int* hits = reinterpret_cast<int*>(a.ws + p.hits);
-    float* zs = reinterpret_cast<float*>(a.ws + p.z);
+    if (!ONE && b == 0 && tid == 0) *reinterpret_cast<int*>(a.ws + p.done) = 0;   // the second kernel's ticket
     const Seqs sq{a.off, a.S, a.T};
     const int lo = b * p.chunk, hi = min(a.T, lo + p.chunk);
-    for (int s = sq.find(lo); s < a.S && sq.begin(s) < hi; ++s) {
+    float bal = 0.f, ztot = 0.f;
+    int live = 0, valid = 0;
+    for (int s = ONE ? 0 : sq.find(lo); s < a.S && (ONE || sq.begin(s) < hi); ++s) {
         const int r0 = max(sq.begin(s), lo), r1 = min(sq.end(s), hi);
-        if (r0 >= r1) continue;
-        for (int e = tid; e < a.E; e += 256) s_hit[e] = 0;
+        if (r0 >= r1 && !ONE) continue;
+        float acc[N], z = 0.f, v[N];
+        if (r0 + g < r1) load_row<L, Q, VEC>(a.logits + (int64_t)(r0 + g) * a.E, a.E, sub, -INFINITY, v);
+        for (int e = tid; e < a.E; e += NT) s_hit[e] = 0;
         __syncthreads();
-        for (int64_t i = (int64_t)r0 * a.k + tid; i < (int64_t)r1 * a.k; i += 256) {
+        for (int64_t i = (int64_t)r0 * a.k + tid; i < (int64_t)r1 * a.k; i += NT) {
             const int id = a.ids[i];
             if (id >= 0 && id < a.E) atomicAdd(&s_hit[id], 1);
         }
-        float acc[N], z = 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) acc[i] = 0.f;
         for (int r = r0 + g; r < r1; r += NG) {
-            float v[N];
-            load_row<L, Q, VEC>(a.logits + (int64_t)r * a.E, a.E, sub, -INFINITY, v);
-            float num[N], shift;
+            float num[N], shift, nx[N];
+            if (r + NG < r1) load_row<L, Q, VEC>(a.logits + (int64_t)(r + NG) * a.E, a.E, sub, -INFINITY, nx);
+            float tot = 0.f;
             if (a.scoring == MOE_SCORING_SIGMOID) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) num[i] = 1.0f / (1.0f + expf(-v[i]));
+                for (int i = 0; i < N; ++i) {
+                    num[i] = __builtin_amdgcn_rcpf(1.0f + exp_fast(-v[i]));
+                    tot += num[i];
+                }
+                tot = rsum<L>(tot);
             }
-            const float sum = softmax_row<L, Q>(v, shift);
-            if (sum != 0.f) {
-                const float lse = shift + logf(sum);
-                z = fmaf(lse, lse, z);
-            }
-            float tot = sum;
-            if (a.scoring == MOE_SCORING_SIGMOID) {
-                float t = 0.f;
+            if (a.scoring != MOE_SCORING_SIGMOID || a.cz != 0.f) {
+                const float sum = softmax_row<L, Q>(v, shift);
+                if (sum != 0.f) {
+                    const float lse = shift + logf(sum);
+                    z = fmaf(lse, lse, z);
+                }
+                if (a.scoring != MOE_SCORING_SIGMOID) {
+                    tot = sum;
 #pragma unroll
-                for (int i = 0; i < N; ++i) t += num[i];
-                tot = rsum<L>(t);
-            } else {
-#pragma unroll
-                for (int i = 0; i < N; ++i) num[i] = v[i];
+                    for (int i = 0; i < N; ++i) num[i] = v[i];
+                }
             }
             const float inv = tot != 0.f ? 1.0f / tot : 0.f;
 #pragma unroll
-            for (int i = 0; i < N; ++i) acc[i] = fmaf(num[i], inv, acc[i]);
+            for (int i = 0; i < N; ++i) {
+                acc[i] = fmaf(num[i], inv, acc[i]);
+                v[i] = nx[i];
+            }
         }
 #pragma unroll
         for (int i = 0; i < Q; ++i)
@@ -137,36 +170,50 @@ __global__ __launch_bounds__(256) void k_balance_rows(BalanceArgs a, BalancePlan
                 make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
         if (sub == 0) s_z[g] = z;
         __syncthreads();
-        const int64_t slot = (int64_t)(b + s) * a.E;
-        for (int e = tid; e < a.E; e += 256) {
-            float v = 0.f;
+        const int len = r1 - r0;
+        float dot = 0.f;
+        for (int e = tid; e < a.E; e += NT) {
+            float t = 0.f;
 #pragma unroll
-            for (int i = 0; i < NG; ++i) v += s_p[i][e];
-            probs[slot + e] = v;
-            hits[slot + e] = s_hit[e];
+            for (int i = 0; i < NG; ++i) t += s_p[i][e];
+            if constexpr (ONE) {
+                const float mean = len > 0 ? t / (float)len : 0.f;
+                a.counts[(int64_t)s * a.E + e] = len > 0 ? s_hit[e] : 0;
+                if (a.mean_probs) a.mean_probs[(int64_t)s * a.E + e] = mean;
+                if (len > 0) dot = fmaf(mean, (float)s_hit[e] / (float)len, dot);
+            } else {
+                const int64_t slot = (int64_t)(b + s) * p.stride;
+                reinterpret_cast<float*>(a.ws + p.probs)[slot + e] = t;
+                reinterpret_cast<int*>(a.ws + p.hits)[slot + e] = s_hit[e];
+            }
         }
+        float t = 0.f;
         if (tid == 0) {
-            float v = 0.f;
 #pragma unroll
-            for (int i = 0; i < NG; ++i) v += s_z[i];
-            zs[b + s] = v;
+            for (int i = 0; i < NG; ++i) t += s_z[i];
+            if constexpr (!ONE) reinterpret_cast<float*>(a.ws + p.z)[b + s] = t;
+        }
+        if constexpr (ONE) {
+            bal += block_sum<NT / 64>(dot, s_w);
+            ztot += t;
+            live += len > 0;
+            valid += max(len, 0);
         }
         __syncthreads();
     }
+    if (ONE && tid == 0) put_losses(a, bal, ztot, live, valid);
 }
 
-// Workgroup (sequence, 64 experts): the parts' sums in row order -> counts, mean probabilities and
-// the sequence's share of the losses; the last workgroup to finish adds the shares in order.
-__global__ __launch_bounds__(1024) void k_balance_reduce(BalanceArgs a, BalancePlan p) {
-    constexpr int NG = 1024 / kBalanceCols;
-    __shared__ float s_p[NG][kBalanceCols];
-    __shared__ int s_h[NG][kBalanceCols];
-    __shared__ float s_w[2][16];
-    __shared__ int s_n[2][16];
-    __shared__ int s_last;
-    const int tid = threadIdx.x, c = tid & (kBalanceCols - 1), g = tid / kBalanceCols;
-    const int ncp = (int)ceil_div(a.E, kBalanceCols);
-    const int s = blockIdx.x / ncp, cp = blockIdx.x - s * ncp, e = cp * kBalanceCols + c;
+// One workgroup per sequence: its parts' sums in row order -> counts, mean probabilities and the
+// sequence's share of the losses.  A thread takes four experts of every NG-th part; with several
+// sequences the last workgroup to finish adds the shares in sequence order.
+__global__ __launch_bounds__(1024) void k_balance_reduce(BalanceArgs a, BalancePlan p, int c4) {
+    __shared__ __align__(16) float4 s_p[1024];
+    __shared__ __align__(16) int4 s_h[1024];
+    __shared__ float s_w[16];
+    __shared__ int s_n[2][16], s_last;
+    const int tid = threadIdx.x, NG = 1024 / c4, c = tid & (c4 - 1), g = tid / c4;   // c4: a power of two >= E / 4
+    const int s = blockIdx.x, e0 = 4 * c;
     const Seqs sq{a.off, a.S, a.T};
     const int t0 = sq.begin(s), t1 = sq.end(s);
     const float* probs = reinterpret_cast<const float*>(a.ws + p.probs);
@@ -174,84 +221,81 @@ __global__ __launch_bounds__(1024) void k_balance_reduce(BalanceArgs a, BalanceP
     const float* zs = reinterpret_cast<const float*>(a.ws + p.z);
     float* seq = reinterpret_cast<float*>(a.ws + p.seq);
     const int b0 = t0 / p.chunk, b1 = t1 > t0 ? (t1 - 1) / p.chunk + 1 : b0;
-    float v = 0.f;
-    int n = 0;
-    if (e < a.E)
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    int4 n = make_int4(0, 0, 0, 0);
+    if (e0 < a.E) {
+#pragma unroll 4
         for (int b = b0 + g; b < b1; b += NG) {
-            v += probs[(int64_t)(b + s) * a.E + e];
-            n += hits[(int64_t)(b + s) * a.E + e];
+            const int64_t o = (int64_t)(b + s) * p.stride + e0;   // (rows of `stride` = E rounded up to 4)
+            const float4 x = *reinterpret_cast<const float4*>(probs + o);
+            const int4 h = *reinterpret_cast<const int4*>(hits + o);
+            v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+            n.x += h.x, n.y += h.y, n.z += h.z, n.w += h.w;
         }
-    s_p[g][c] = v;
-    s_h[g][c] = n;
+    }
+    float z = 0.f;
+    for (int b = b0 + tid; b < b1; b += 1024) z += zs[b + s];
+    s_p[tid] = v;
+    s_h[tid] = n;
     __syncthreads();
-    if (tid < 64) {
-        v = 0.f;
-        n = 0;
-#pragma unroll
+    const float len = (float)(t1 - t0);
+    float dot = 0.f;
+    for (int e = tid; e < a.E; e += 1024) {
+        float t = 0.f;
+        int m = 0;
+#pragma unroll 8
         for (int i = 0; i < NG; ++i) {
-            v += s_p[i][c];
-            n += s_h[i][c];
+            t += reinterpret_cast<const float*>(s_p)[4 * i * c4 + e];
+            m += reinterpret_cast<const int*>(s_h)[4 * i * c4 + e];
         }
-        const float len = (float)(t1 - t0), mean = t1 > t0 ? v / len : 0.f;
-        if (e < a.E) {
-            a.counts[(int64_t)s * a.E + e] = n;
-            if (a.mean_probs) a.mean_probs[(int64_t)s * a.E + e] = mean;
-        }
-        const float dot = wave_sum(t1 > t0 && e < a.E ? mean * ((float)n / len) : 0.f);
-        float z = 0.f;
-        if (cp == 0)
-            for (int b = b0 + c; b < b1; b += 64) z += zs[b + s];
-        z = wave_sum(z);
-        if (c == 0) {
-            __hip_atomic_store(&seq[2 * blockIdx.x], dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            __hip_atomic_store(&seq[2 * blockIdx.x + 1], z, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            __threadfence();
-            s_last = __hip_atomic_fetch_add(reinterpret_cast<int*>(a.ws + p.done), 1, __ATOMIC_ACQ_REL,
-                                            __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
-        }
+        const float mean = t1 > t0 ? t / len : 0.f;
+        a.counts[(int64_t)s * a.E + e] = m;
+        if (a.mean_probs) a.mean_probs[(int64_t)s * a.E + e] = mean;
+        if (t1 > t0) dot = fmaf(mean, (float)m / len, dot);
+    }
+    dot = block_sum<16>(dot, s_w);
+    z = block_sum<16>(z, s_w);
+    if (a.S == 1) {
+        if (tid == 0) put_losses(a, dot, z, t1 > t0, max(t1 - t0, 0));
+        return;
+    }
+    if (tid == 0) {
+        __hip_atomic_store(&seq[2 * s], dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(&seq[2 * s + 1], z, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        s_last = __hip_atomic_fetch_add(reinterpret_cast<int*>(a.ws + p.done), 1, __ATOMIC_ACQ_REL,
+                                        __HIP_MEMORY_SCOPE_AGENT) == a.S - 1;
     }
     __syncthreads();
     if (!s_last) return;
-    __threadfence();
-    float bal = 0.f, z = 0.f;
+    float bal = 0.f;
+    z = 0.f;
     int live = 0, valid = 0;
-    for (int i = tid; i < (int)gridDim.x; i += 1024) {
+    for (int i = tid; i < a.S; i += 1024) {
         bal += __hip_atomic_load(&seq[2 * i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         z += __hip_atomic_load(&seq[2 * i + 1], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const int l = sq.end(i) - sq.begin(i);
+        live += l > 0;
+        valid += l;
     }
-    for (int i = tid; i < a.S; i += 1024) {
-        const int len = sq.end(i) - sq.begin(i);
-        live += len > 0;
-        valid += len;
-    }
-    bal = wave_sum(bal);
-    z = wave_sum(z);
+    bal = block_sum<16>(bal, s_w);
+    z = block_sum<16>(z, s_w);
 #pragma unroll
     for (int o = 32; o; o >>= 1) {
         live += __shfl_xor(live, o);
         valid += __shfl_xor(valid, o);
     }
     if ((tid & 63) == 0) {
-        s_w[0][tid >> 6] = bal;
-        s_w[1][tid >> 6] = z;
         s_n[0][tid >> 6] = live;
         s_n[1][tid >> 6] = valid;
     }
     __syncthreads();
     if (tid == 0) {
-        bal = z = 0.f;
         live = valid = 0;
         for (int i = 0; i < 16; ++i) {
-            bal += s_w[0][i];
-            z += s_w[1][i];
             live += s_n[0][i];
             valid += s_n[1][i];
         }
-        bal = live ? a.ca * bal * ((float)a.E / (float)a.k) / (float)live : 0.f;
-        z = valid ? a.cz * z / (float)valid : 0.f;
-        a.losses[0] = bal + z;
-        a.losses[1] = bal;
-        a.losses[2] = z;
+        put_losses(a, bal, z, live, valid);
     }
 }
 
@@ -269,12 +313,22 @@ static bool vec4(const void* p, int E) { return E % 4 == 0 && (uintptr_t)p % 16 
 
 hipError_t launch_balance_loss(const BalanceArgs& a, hipStream_t st) {
     const BalancePlan p = balance_plan(a.T, a.E, a.S);
-#define MOE_CALL(L, Q, V) hipLaunchKernelGGL((k_balance_rows<L, Q, V>), dim3(p.nblocks), dim3(256), 0, st, a, p)
-    MOE_ROW_DISPATCH(a.E, vec4(a.logits, a.E), MOE_CALL);
+    const bool v = vec4(a.logits, a.E);
+    if (p.nblocks == 1) {
+#define MOE_CALL(L, Q, V) hipLaunchKernelGGL((k_balance_rows<L, Q, V, true>), dim3(1), dim3(kRowsThreads), 0, st, a, p)
+        MOE_ROW_DISPATCH(a.E, v, MOE_CALL);
+#undef MOE_CALL
+        return hipGetLastError();
+    }
+#define MOE_CALL(L, Q, V) \
+    hipLaunchKernelGGL((k_balance_rows<L, Q, V, false>), dim3(p.nblocks), dim3(kRowsThreads), 0, st, a, p)
+    MOE_ROW_DISPATCH(a.E, v, MOE_CALL);
 #undef MOE_CALL
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k_balance_reduce, dim3((unsigned)(a.S * ceil_div(a.E, kBalanceCols))), dim3(1024), 0, st, a, p);
+    int c4 = 1;
+    while (4 * c4 < a.E) c4 *= 2;
+    hipLaunchKernelGGL(k_balance_reduce, dim3(a.S), dim3(1024), 0, st, a, p, c4);
     return hipGetLastError();
 }
 
@@ -289,11 +343,16 @@ hipError_t launch_balance_loss(const BalanceArgs& a, hipStream_t st) {
 //            over the chosen (softmax renormalised; sigmoid with a factor 1 - s):
 //                      rsf q (D - m sum q D),  q = score / sum m score
 constexpr int kSeqLds = 1024;   // sequence boundaries held in LDS
+
+// Orders the LDS accesses of a wave's own lanes (a row's lanes are in one wave).
+__device__ __forceinline__ void wave_lds_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
+
 template <int L, int Q, bool VEC>
 __global__ __launch_bounds__(256) void k_route_bwd(RouteBwdArgs a) {
     constexpr int NG = 256 / L, N = 4 * Q;
     __shared__ int s_off[kSeqLds + 1];
     __shared__ int s_n[2][4];
+    __shared__ __align__(16) float s_d[NG][L * N], s_m[NG][L * N];
     const int tid = threadIdx.x, g = tid / L, sub = tid % L;
     const int64_t t = (int64_t)blockIdx.x * NG + g;
     const Seqs sq{a.off, a.S, a.T};
@@ -331,17 +390,25 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouteBwdArgs a) {
         const bool sig = a.scoring == MOE_SCORING_SIGMOID;
         float l[N], v[N], sc[N], om[N], shift;   // om: 1 - s for the sigmoid, 1 for softmax
         load_row<L, Q, VEC>(a.logits + t * a.E, a.E, sub, -INFINITY, l);
+        int id0 = -1, c[N];     // everything else the row needs is requested now as well
+        float dw0 = 0.f;
+        if (a.dw && sub < a.k) {
+            id0 = a.ids[t * a.k + sub];
+            dw0 = a.dw[t * a.k + sub];
+        }
+        if (a.counts) load_row<L, Q, VEC>(a.counts + (int64_t)s * a.E, a.E, sub, 0, c);
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] = l[i];
-        const float sum = softmax_row<L, Q>(v, shift);
+        float sum = 0.f;
+        if (!sig || a.cz != 0.f) sum = softmax_row<L, Q>(v, shift);
         const float inv = sum != 0.f ? 1.0f / sum : 0.f;
         float pinv = inv;
         if (sig) {
             float z = 0.f;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const float ex = expf(-l[i]);
-                sc[i] = 1.0f / (1.0f + ex);
+                const float ex = exp_fast(-l[i]);
+                sc[i] = __builtin_amdgcn_rcpf(1.0f + ex);
                 om[i] = ex < INFINITY ? ex * sc[i] : 1.0f - sc[i];
                 z += sc[i];
             }
@@ -357,8 +424,6 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouteBwdArgs a) {
         if (a.counts) {
             const float len = (float)(t1 - t0);
             const float cu = a.ca / (float)live * ((float)a.E / (float)a.k) / len / len;
-            int c[N];
-            load_row<L, Q, VEC>(a.counts + (int64_t)s * a.E, a.E, sub, 0, c);
             float pu = 0.f;
 #pragma unroll
             for (int i = 0; i < N; ++i) pu = fmaf(sc[i] * pinv, cu * (float)c[i], pu);
@@ -372,18 +437,43 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouteBwdArgs a) {
             for (int i = 0; i < N; ++i) d[i] = fmaf(cz, v[i], d[i]);
         }
         if (a.dw) {
+            // D and m through the row's LDS lines: lane j adds up the slots that chose the same expert as
+            // slot j, in slot order, and all of them store that sum (comparing every expert with every
+            // slot instead took 640 instructions of a row's 1100 at 256 experts and 8 slots)
             float D[N], m[N];
+            float* dl = s_d[g];
+            float* ml = s_m[g];
 #pragma unroll
-            for (int i = 0; i < N; ++i) D[i] = m[i] = 0.f;
-            for (int j = 0; j < a.k; ++j) {
-                const int id = a.ids[t * a.k + j];
-                const float w = a.dw[t * a.k + j];
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const bool hit = id == 4 * (sub + L * (i / 4)) + (i & 3);
-                    D[i] += hit ? w : 0.f;
-                    m[i] += hit ? 1.f : 0.f;
+            for (int i = 0; i < Q; ++i) {
+                *reinterpret_cast<float4*>(dl + 4 * (sub + L * i)) = make_float4(0.f, 0.f, 0.f, 0.f);
+                *reinterpret_cast<float4*>(ml + 4 * (sub + L * i)) = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            wave_lds_fence();
+            for (int j0 = 0; j0 < a.k; j0 += L) {
+                const int id = j0 == 0 ? id0 : j0 + sub < a.k ? a.ids[t * a.k + j0 + sub] : -1;
+                const float w = j0 == 0 ? dw0 : j0 + sub < a.k ? a.dw[t * a.k + j0 + sub] : 0.f;
+                const bool in = id >= 0 && id < a.E;
+                float sum = in ? dl[id] : 0.f, cnt = in ? ml[id] : 0.f;   // (slots of earlier rounds)
+                wave_lds_fence();
+                const int n = min(L, a.k - j0);
+                for (int j = 0; j < n; ++j) {
+                    const bool same = __shfl(id, j, L) == id;
+                    const float wj = __shfl(w, j, L);
+                    sum += same ? wj : 0.f;
+                    cnt += same ? 1.f : 0.f;
                 }
+                if (in) {
+                    dl[id] = sum;
+                    ml[id] = cnt;
+                }
+                wave_lds_fence();
+            }
+#pragma unroll
+            for (int i = 0; i < Q; ++i) {
+                const float4 x = *reinterpret_cast<const float4*>(dl + 4 * (sub + L * i));
+                const float4 y = *reinterpret_cast<const float4*>(ml + 4 * (sub + L * i));
+                D[4 * i] = x.x, D[4 * i + 1] = x.y, D[4 * i + 2] = x.z, D[4 * i + 3] = x.w;
+                m[4 * i] = y.x, m[4 * i + 1] = y.y, m[4 * i + 2] = y.z, m[4 * i + 3] = y.w;
             }
             if (!sig && !a.renorm) {
                 float pd = 0.f;
@@ -402,7 +492,7 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouteBwdArgs a) {
                 }
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    q[i] = m[i] > 0.f ? (sig ? sc[i] : expf(l[i] - mx)) : 0.f;
+                    q[i] = m[i] > 0.f ? (sig ? sc[i] : exp_fast(l[i] - mx)) : 0.f;
                     z = fmaf(m[i], q[i], z);
                     qd = fmaf(q[i], D[i], qd);
                 }

@@ -13,21 +13,26 @@ int norm_bwd_parts(int T, int H) {
 }
 size_t norm_bwd_ws_bytes(int T, int H) { return (size_t)norm_bwd_parts(T, H) * H * 4; }
 
+// Up to 128 rows one workgroup does everything; beyond that 32 rows each (one for every 16 lanes of a
+// workgroup), more from 8192 rows on, where 256 workgroups fill the chip and more parts would only
+// lengthen the second kernel.
 BalancePlan balance_plan(int T, int E, int S) {
     BalancePlan p;
-    p.chunk = std::max(64, (int)cdiv(T, 256));
+    p.chunk = T <= 128 ? 128 : std::max(32, (int)cdiv(T, 256));
     p.nblocks = (int)cdiv(T, p.chunk);
     p.nslots = p.nblocks + S;
+    p.stride = (E + 3) / 4 * 4;
     size_t o = 0;
     auto take = [&](size_t n) {
         const size_t r = o;
         o += align256(n);
         return r;
     };
-    p.probs = take((size_t)p.nslots * E * 4);
-    p.hits = take((size_t)p.nslots * E * 4);
-    p.z = take((size_t)p.nslots * 4);
-    p.seq = take((size_t)S * cdiv(E, kBalanceCols) * 8);
+    const size_t rows = p.nblocks > 1 ? p.nslots : 0;
+    p.probs = take(rows * p.stride * 4);
+    p.hits = take(rows * p.stride * 4);
+    p.z = take(rows * 4);
+    p.seq = take((size_t)S * 8);
     p.done = take(4);
     p.end = o;
     return p;

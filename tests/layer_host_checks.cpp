@@ -36,9 +36,11 @@ static void balance_slots() {
         const BalancePlan p = balance_plan(T, E, S);
         CHECK((int64_t)p.nblocks * p.chunk >= T && (int64_t)(p.nblocks - 1) * p.chunk < T);
         const size_t o[] = {p.probs, p.hits, p.z, p.seq, p.done, p.end};
-        for (int i = 0; i + 1 < 6; ++i) CHECK(o[i] < o[i + 1] && o[i] % 256 == 0);
-        CHECK(p.hits - p.probs >= (size_t)p.nslots * E * 4 && p.z - p.hits >= (size_t)p.nslots * E * 4);
-        CHECK(p.seq - p.z >= (size_t)p.nslots * 4 && p.done - p.seq >= (size_t)S * cdiv(E, kBalanceCols) * 8);
+        for (int i = 0; i + 1 < 6; ++i) CHECK(o[i] <= o[i + 1] && o[i] % 256 == 0);
+        CHECK(p.stride >= E && p.stride % 4 == 0 && p.done - p.seq >= (size_t)S * 8 && p.end - p.done >= 4);
+        if (p.nblocks == 1) continue;   // no parts
+        CHECK(p.hits - p.probs >= (size_t)p.nslots * p.stride * 4 && p.z - p.hits >= (size_t)p.nslots * p.stride * 4);
+        CHECK(p.seq - p.z >= (size_t)p.nslots * 4);
         std::set<int> seen;
         for (int b = 0; b < p.nblocks; ++b)
             for (int s = 0; s < S; ++s)

@@ -350,9 +350,10 @@ def _check_router(l, lf, ids, idn, dw, dwf, k, scoring, renorm, rsf, offsets):
     fin = lf[np.isfinite(lf)]
     R = float(fin.max() - fin.min()) if fin.size else 0.0
     # a probability: exponent R u off, exp and division a few u, sum of E terms (chain <= 16 + 6);
-    # sums over rows: chain <= chunk / 4 + 16 and <= 256 / 16 + 16 of the parts
+    # sums over rows: a part's rows over 8 groups of lanes or more (chain <= T / 256 / 8 + 32), then at
+    # most 256 parts one by one
     c_row = R + 40
-    c_sum = c_row + max(64, len(lf) / 256) + 64
+    c_sum = c_row + len(lf) / 2048 + 32 + 256
     within(host(out["mean_probs"]), mean, c_sum * U * mean + 1e-37, "mean_probs")
     lse = max(1.0, np.abs(fin).max() if fin.size else 1.0)
     got = host(out["losses"])
