@@ -9,21 +9,58 @@
 
 namespace moe {
 
+// Lane exchange of both halves of a double by the DPP control word of dpp_f32.
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, (uint64_t)dpp_u32<CTRL>((uint32_t)(u >> 32)) << 32 | dpp_u32<CTRL>((uint32_t)u));
+}
+__device__ __forceinline__ double lane_f64(double v, int lane) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double wave_sum(double v) {
+    v += dpp_f64<0xB1>(v);
+    v += dpp_f64<0x4E>(v);
+    v += dpp_f64<0x124>(v);
+    v += dpp_f64<0x128>(v);
+    return (lane_f64(v, 0) + lane_f64(v, 16)) + (lane_f64(v, 32) + lane_f64(v, 48));
+}
+
 // Sum over the G threads of a row: a wave's sum, then (G > 64) the waves' sums through LDS in wave
-// order.  s: G / 64 floats of the row, not in use by a slower wave of an earlier call (the callers
-// alternate two of them).
+// order.  s: G / 64 doubles, used once.
 template <int G>
-__device__ __forceinline__ float row_sum(float v, float* s) {
+__device__ __forceinline__ double row_sum(double v, double* s) {
     v = wave_sum(v);
     if constexpr (G > 64) {
-        const int wv = (threadIdx.x % G) >> 6;
-        if ((threadIdx.x & 63) == 0) s[wv] = v;
+        if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
         __syncthreads();
-        v = 0.f;
+        v = 0.0;
 #pragma unroll
         for (int i = 0; i < G / 64; ++i) v += s[i];
     }
     return v;
+}
+
+// 1 / sqrt(x) to double precision: the instruction's estimate (about 2^-26 off) and one Newton step,
+// which would make NaN of the infinity and the zero that the ends of the range give.
+__device__ __forceinline__ double rsqrt_f64(double x) {
+    const double r = __builtin_amdgcn_rsq(x);
+    const double n = r * fma(-0.5 * x * r, r, 1.5);
+    return x > 0.0 && x < __builtin_inf() ? n : r;
+}
+
+// A double as a float that rounds to the same bf16: rounded to odd (towards zero, the last bit set where
+// anything was cut off).  Rounded to nearest it could land on the middle of two bf16 values and be
+// rounded the other way then, which happens to one value in 2^17.
+__device__ __forceinline__ float round_odd(double d) {
+    const float f = (float)d;
+    const double r = d - (double)f;
+    uint32_t u = __float_as_uint(f);
+    if (r != 0.0) u = (u - ((r > 0.0) != (d > 0.0) ? 1u : 0u)) | 1u;
+    return __uint_as_float(u);
 }
 
 // E4M3 codes of 8 values in each of LANES consecutive lanes sharing one scale (LANES * 8 columns):
@@ -47,11 +84,13 @@ __device__ __forceinline__ uint2 group_codes(const float (&f)[8], int& e) {
 }
 
 // G threads per row, VPT vectors of 8 columns per thread (G * VPT >= H / 8); a workgroup holds
-// max(1, 256 / G) rows.
+// max(1, 256 / G) rows.  The row's sum, its root and the two products are formed in double, which the
+// memory hides: y is then the definition's value rounded once, and the codes, which a value beside a
+// border would otherwise tip, are the definition's codes.
 template <int G, int VPT>
 __global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_rmsnorm(NormArgs a) {
     constexpr int RPB = G < 256 ? 256 / G : 1;
-    __shared__ float s_sum[RPB][G / 64];
+    __shared__ double s_sum[G / 64];
     const int sub = threadIdx.x % G, nv = a.H >> 3;
     const int64_t t = (int64_t)blockIdx.x * RPB + threadIdx.x / G;
     if (RPB > 1 && t >= a.T) return;   // (RPB > 1 only with G = 64: no barrier follows)
@@ -81,7 +120,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_rmsnorm(NormArgs a) {
             w1[i] = *reinterpret_cast<const float4*>(a.w + v * 8 + 4);
         }
     }
-    float ss = 0.f;
+    double ss = 0.0;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         float f[8];
@@ -95,7 +134,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_rmsnorm(NormArgs a) {
             unpack8(vx[i], f);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
+        for (int j = 0; j < 8; ++j) ss = fma((double)f[j], (double)f[j], ss);
     }
     if (a.h) {
 #pragma unroll
@@ -105,8 +144,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_rmsnorm(NormArgs a) {
         }
     }
     if (!a.y && !a.yq) return;   // (uniform)
-    ss = row_sum<G>(ss, s_sum[threadIdx.x / G]);
-    const float r = 1.0f / sqrtf(ss / (float)a.H + a.eps);
+    const double r = rsqrt_f64(fma(row_sum<G>(ss, s_sum), a.inv_h, (double)a.eps));
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int v = sub + i * G;
@@ -114,7 +152,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_rmsnorm(NormArgs a) {
         unpack8(vx[i], f);
         const float w[8] = {w0[i].x, w0[i].y, w0[i].z, w0[i].w, w1[i].x, w1[i].y, w1[i].z, w1[i].w};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = f[j] * r * w[j];
+        for (int j = 0; j < 8; ++j) f[j] = round_odd((double)f[j] * r * (double)w[j]);
         const uint4 o = pack8(f);
         if (v < nv) {   // a scale's lanes are all in or all out: H is a multiple of its columns
             if (a.y) *reinterpret_cast<uint4*>(a.y + t * a.H + v * 8) = o;
@@ -144,7 +182,7 @@ hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t st) {
     if (nv <= 64) run_norm<64, 1>(a, st);
     else if (nv <= 256) run_norm<256, 1>(a, st);
     else if (nv <= 512) run_norm<512, 1>(a, st);
-    else if (nv <= 1024) run_norm<1024, 1>(a, st);
+    else if (nv <= 1024) run_norm<512, 2>(a, st);   // 4096 x 7168 with residual and codes: 50.5 us, 1024 threads 51.4
     else if (nv <= 2048) run_norm<1024, 2>(a, st);
     else run_norm<1024, 4>(a, st);
     return hipGetLastError();
@@ -169,20 +207,30 @@ __global__ __launch_bounds__(G) void k_add_rmsnorm_bwd(NormBwdArgs a) {
             w[i][j] = v < nv ? a.w[v * 8 + j] : 0.f;
         }
     }
-    int par = 0;
-    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, par ^= 1) {
-        uint4 vh[VPT], vd[VPT], vr[VPT];
+    struct Row {
+        uint4 h[VPT], d[VPT], r[VPT];
+    };
+    auto load = [&](int64_t t, Row& x) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = sub + i * G;
             const int64_t o = t * a.H + v * 8;
-            vh[i] = vd[i] = vr[i] = make_uint4(0, 0, 0, 0);
+            x.h[i] = x.d[i] = x.r[i] = make_uint4(0, 0, 0, 0);
             if (v < nv) {
-                vh[i] = *reinterpret_cast<const uint4*>(a.h + o);
-                vd[i] = *reinterpret_cast<const uint4*>(a.dy + o);
-                if (a.dh) vr[i] = *reinterpret_cast<const uint4*>(a.dh + o);
+                x.h[i] = *reinterpret_cast<const uint4*>(a.h + o);
+                x.d[i] = *reinterpret_cast<const uint4*>(a.dy + o);
+                if (a.dh) x.r[i] = *reinterpret_cast<const uint4*>(a.dh + o);
             }
         }
+    };
+    int par = 0;
+    Row nx;
+    load(blockIdx.x, nx);
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, par ^= 1) {
+        uint4 vh[VPT], vd[VPT], vr[VPT];
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) vh[i] = nx.h[i], vd[i] = nx.d[i], vr[i] = nx.r[i];
+        if (t + gridDim.x < a.T) load(t + gridDim.x, nx);   // in flight over this row's sums
         // sum h^2 and sum g h in one exchange: mean(g xhat) = r sum(g h) / H
         float ss = 0.f, gh = 0.f;
 #pragma unroll
@@ -242,21 +290,27 @@ __global__ __launch_bounds__(G) void k_add_rmsnorm_bwd(NormBwdArgs a) {
     }
 }
 
-// dweight[c] = sum of the partial rows, in order: 32 columns per workgroup, 32 row groups whose
+// dweight[c] = sum of the partial rows: 32 columns per workgroup as 8 vectors of 4, 32 row groups, whose
 // sums are then added in order through LDS.
-__global__ __launch_bounds__(1024) void k_norm_dw(const float* __restrict__ part, int np, int H, float* __restrict__ dw) {
-    __shared__ float s[32][33];
-    const int c = threadIdx.x & 31, g = threadIdx.x >> 5, col = blockIdx.x * 32 + c;
-    float v = 0.f;
-    if (col < H)
-        for (int p = g; p < np; p += 32) v += part[(int64_t)p * H + col];
-    s[g][c] = v;
+__global__ __launch_bounds__(256) void k_norm_dw(const float* __restrict__ part, int np, int H, float* __restrict__ dw) {
+    __shared__ __align__(16) float s[32][32];
+    const int c = threadIdx.x & 7, g = threadIdx.x >> 3, col = blockIdx.x * 32 + 4 * c;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (col < H) {   // (H is a multiple of 8)
+#pragma unroll 16
+        for (int p = g; p < np; p += 32) {
+            const float4 x = *reinterpret_cast<const float4*>(part + (int64_t)p * H + col);
+            v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+        }
+    }
+    *reinterpret_cast<float4*>(&s[g][4 * c]) = v;
     __syncthreads();
-    if (g == 0 && col < H) {
-        v = 0.f;
+    const int o = blockIdx.x * 32 + threadIdx.x;
+    if (threadIdx.x < 32 && o < H) {
+        float t = 0.f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v += s[i][c];
-        dw[col] = v;
+        for (int i = 0; i < 32; ++i) t += s[i][threadIdx.x];
+        dw[o] = t;
     }
 }
 
@@ -270,12 +324,12 @@ hipError_t launch_add_rmsnorm_backward(const NormBwdArgs& a, hipStream_t st) {
     if (nv <= 64) run_norm_bwd<64, 1>(a, grid, st);
     else if (nv <= 256) run_norm_bwd<256, 1>(a, grid, st);
     else if (nv <= 512) run_norm_bwd<512, 1>(a, grid, st);
-    else if (nv <= 1024) run_norm_bwd<1024, 1>(a, grid, st);
+    else if (nv <= 1024) run_norm_bwd<512, 2>(a, grid, st);
     else if (nv <= 2048) run_norm_bwd<1024, 2>(a, grid, st);
     else run_norm_bwd<1024, 4>(a, grid, st);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.dw) return e;
-    hipLaunchKernelGGL(k_norm_dw, dim3((unsigned)ceil_div(a.H, 32)), dim3(1024), 0, st, a.part, grid, a.H, a.dw);
+    hipLaunchKernelGGL(k_norm_dw, dim3((unsigned)ceil_div(a.H, 32)), dim3(256), 0, st, a.part, grid, a.H, a.dw);
     return hipGetLastError();
 }
 

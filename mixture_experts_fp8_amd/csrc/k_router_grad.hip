@@ -530,18 +530,20 @@ hipError_t launch_route_backward(const RouteBwdArgs& a, hipStream_t st) {
 }
 
 // ----------------------------------------------------------------------------------------
-// Gradients of the combine: G threads per token walk its columns 8 at a time; up to 8 expert rows
-// are in flight per column vector, so dy is read once for every 8 slots.  Bound by HBM: the expert
-// rows are read once and (dexpert_out) written once.
+// Gradients of the combine: G threads per token walk its columns, 16 bytes of every expert row at a
+// time (8 bf16 or 4 float32 columns); up to 8 expert rows are in flight per vector, so dy is read once
+// for every 8 slots.  Bound by HBM: the expert rows are read once and (dexpert_out) written once, both
+// past the caches.
 typedef unsigned v4u_t __attribute__((ext_vector_type(4)));
 template <bool BF16, int G, bool DOUT>
 __global__ __launch_bounds__(256) void k_combine_bwd(CombineBwdArgs a) {
-    constexpr int RPB = 256 / G;
-    __shared__ float s_dot[4][8];
-    const int sub = threadIdx.x % G;
-    const int64_t t = (int64_t)blockIdx.x * RPB + threadIdx.x / G;
-    if (RPB > 1 && t >= a.T) return;   // (no barrier follows with G = 64)
-    const int nv = a.H >> 3;
+    constexpr int RPB = 256 / G, CW = BF16 ? 8 : 4, NW = G / 64;
+    __shared__ float s_dot[RPB][NW][8];
+    const int sub = threadIdx.x % G, r = threadIdx.x / G;
+    const int64_t tt = (int64_t)blockIdx.x * RPB + r;
+    const bool on = tt < a.T;           // (the barriers below are for every thread)
+    const int64_t t = on ? tt : a.T - 1;
+    const int nv = on ? a.H / CW : 0;
     const int64_t A = (int64_t)a.T * a.k;
     for (int j0 = 0; j0 < a.k; j0 += 8) {
         int64_t p[8];
@@ -555,53 +557,47 @@ __global__ __launch_bounds__(256) void k_combine_bwd(CombineBwdArgs a) {
             dot[u] = 0.f;
         }
         for (int v = sub; v < nv; v += G) {
-            v4u_t e[8][BF16 ? 1 : 2];
+            v4u_t e[8];
             if (a.dwt) {
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
-                    if (p[u] >= 0) {
-                        const v4u_t* src = reinterpret_cast<const v4u_t*>(
-                            reinterpret_cast<const uint8_t*>(a.eo) + (p[u] * a.H + v * 8) * (BF16 ? 2 : 4));
-                        e[u][0] = __builtin_nontemporal_load(src);
-                        if constexpr (!BF16) e[u][1] = __builtin_nontemporal_load(src + 1);
-                    } else {
-                        e[u][0] = v4u_t{0, 0, 0, 0};
-                        if constexpr (!BF16) e[u][1] = v4u_t{0, 0, 0, 0};
-                    }
+                    e[u] = v4u_t{0, 0, 0, 0};
+                    if (p[u] >= 0)
+                        e[u] = __builtin_nontemporal_load(reinterpret_cast<const v4u_t*>(a.eo) + p[u] * (a.H / CW) + v);
                 }
             }
             float d[8];
-            unpack8(*reinterpret_cast<const uint4*>(a.dy + t * a.H + v * 8), d);
+            if constexpr (BF16) {
+                unpack8(*reinterpret_cast<const uint4*>(a.dy + t * a.H + v * 8), d);
+            } else {
+                const uint2 x = *reinterpret_cast<const uint2*>(a.dy + t * a.H + v * 4);
+                d[0] = __uint_as_float(x.x << 16), d[1] = __uint_as_float(x.x & 0xFFFF0000u);
+                d[2] = __uint_as_float(x.y << 16), d[3] = __uint_as_float(x.y & 0xFFFF0000u);
+            }
             if (a.dwt) {
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
+                for (int u = 0; u < 8; ++u)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < CW; ++i) {
                         float x;
                         if constexpr (BF16)
-                            x = i & 1 ? __uint_as_float(e[u][0][i / 2] & 0xFFFF0000u) : __uint_as_float(e[u][0][i / 2] << 16);
+                            x = i & 1 ? __uint_as_float(e[u][i / 2] & 0xFFFF0000u) : __uint_as_float(e[u][i / 2] << 16);
                         else
-                            x = __uint_as_float(e[u][i / 4][i & 3]);
+                            x = __uint_as_float(e[u][i]);
                         dot[u] = fmaf(d[i], x, dot[u]);
                     }
-                }
             }
             if constexpr (DOUT) {
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
                     if (p[u] >= 0) {
-                        v4u_t* dst = reinterpret_cast<v4u_t*>(reinterpret_cast<uint8_t*>(a.deo) +
-                                                              (p[u] * a.H + v * 8) * (BF16 ? 2 : 4));
-                        if constexpr (BF16) {
-                            __builtin_nontemporal_store(v4u_t{pack_bf16(wj[u] * d[0], wj[u] * d[1]), pack_bf16(wj[u] * d[2], wj[u] * d[3]),
-                                                              pack_bf16(wj[u] * d[4], wj[u] * d[5]), pack_bf16(wj[u] * d[6], wj[u] * d[7])}, dst);
-                        } else {
+                        v4u_t o;
 #pragma unroll
-                            for (int q = 0; q < 2; ++q)
-                                __builtin_nontemporal_store(
-                                    v4u_t{__float_as_uint(wj[u] * d[4 * q]), __float_as_uint(wj[u] * d[4 * q + 1]),
-                                          __float_as_uint(wj[u] * d[4 * q + 2]), __float_as_uint(wj[u] * d[4 * q + 3])}, dst + q);
+                        for (int i = 0; i < 4; ++i) {
+                            if constexpr (BF16) o[i] = pack_bf16(wj[u] * d[2 * i], wj[u] * d[2 * i + 1]);
+                            else o[i] = __float_as_uint(wj[u] * d[i]);
                         }
+                        __builtin_nontemporal_store(o, reinterpret_cast<v4u_t*>(a.deo) + p[u] * (a.H / CW) + v);
                     }
                 }
             }
@@ -609,19 +605,23 @@ __global__ __launch_bounds__(256) void k_combine_bwd(CombineBwdArgs a) {
         if (a.dwt) {
 #pragma unroll
             for (int u = 0; u < 8; ++u) dot[u] = wave_sum(dot[u]);
-            if constexpr (G > 64) {
+            if constexpr (NW > 1) {
                 if (j0) __syncthreads();   // the previous slots' sums have been read
                 if ((sub & 63) == 0) {
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) s_dot[sub >> 6][u] = dot[u];
+                    for (int u = 0; u < 8; ++u) s_dot[r][sub >> 6][u] = dot[u];
                 }
                 __syncthreads();
 #pragma unroll
-                for (int u = 0; u < 8; ++u) dot[u] = (s_dot[0][u] + s_dot[1][u]) + (s_dot[2][u] + s_dot[3][u]);
+                for (int u = 0; u < 8; ++u) {
+                    dot[u] = s_dot[r][0][u];
+#pragma unroll
+                    for (int w = 1; w < NW; ++w) dot[u] += s_dot[r][w][u];
+                }
             }
 #pragma unroll
             for (int u = 0; u < 8; ++u)
-                if (sub == u && j0 + u < a.k) a.dwt[t * a.k + j0 + u] = p[u] >= 0 ? dot[u] : 0.f;
+                if (on && sub == u && j0 + u < a.k) a.dwt[t * a.k + j0 + u] = p[u] >= 0 ? dot[u] : 0.f;
         }
     }
 }
@@ -633,15 +633,22 @@ static void run_combine_bwd(const CombineBwdArgs& a, hipStream_t st) {
     else hipLaunchKernelGGL((k_combine_bwd<BF16, G, false>), grid, dim3(256), 0, st, a);
 }
 
+// Threads per token, by its nv vectors.  Few tokens: as many as there are vectors, one round of loads
+// (64 x 4096 bf16: 6.3 us with 256 threads, 15 with 64).  Otherwise fewer where rows are short, for more
+// rounds in flight from fewer workgroups (2047 x 768 float32: 128 threads 11.6 us, 256 14.8), and a wave
+// where dexpert_out is written too (2047 x 2816 bf16: 40 us, 128 threads 46); 256 from 512 vectors on
+// (4096 x 4096 bf16 with dexpert_out: 108 us, 64 threads 138).
+template <bool BF16>
+static void pick_combine_bwd(const CombineBwdArgs& a, hipStream_t st) {
+    const int nv = a.H / (BF16 ? 8 : 4);
+    if (nv <= 64 || (a.T >= 1024 && nv < 512 && a.deo)) run_combine_bwd<BF16, 64>(a, st);
+    else if (nv <= 128 || (a.T >= 1024 && nv < 512)) run_combine_bwd<BF16, 128>(a, st);
+    else run_combine_bwd<BF16, 256>(a, st);
+}
+
 hipError_t launch_combine_backward(const CombineBwdArgs& a, hipStream_t st) {
-    const bool wide = a.H > 1024;
-    if (a.bf16) {
-        if (wide) run_combine_bwd<true, 256>(a, st);
-        else run_combine_bwd<true, 64>(a, st);
-    } else {
-        if (wide) run_combine_bwd<false, 256>(a, st);
-        else run_combine_bwd<false, 64>(a, st);
-    }
+    if (a.bf16) pick_combine_bwd<true>(a, st);
+    else pick_combine_bwd<false>(a, st);
     return hipGetLastError();
 }
 

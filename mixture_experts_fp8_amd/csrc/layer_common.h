@@ -50,6 +50,7 @@ struct NormArgs {
     uint8_t* yq;
     uint8_t* ys;
     int group;       // columns per scale: 0 (no codes), 32 or 128
+    double inv_h;    // 1 / H
 };
 hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t st);
 

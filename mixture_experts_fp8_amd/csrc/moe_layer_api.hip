@@ -19,7 +19,7 @@ int moe_add_rmsnorm(const moe_add_rmsnorm_args* a) {
     if (int rc = moe::host::check_add_rmsnorm(a)) return rc;
     const int group = !a->yq ? 0 : a->quant == MOE_QUANT_FP8_BLOCK128 ? 128 : 32;
     const moe::NormArgs n{a->T, a->H, a->x, a->ld_x, a->residual, a->ld_residual, a->weight, a->eps,
-                          a->h, a->y, a->yq, a->ys, group};
+                          a->h, a->y, a->yq, a->ys, group, 1.0 / a->H};
     return done("moe_add_rmsnorm", moe::launch_add_rmsnorm(n, static_cast<hipStream_t>(a->stream)));
 }
 

@@ -7,10 +7,9 @@
 
 namespace moe {
 
-int norm_bwd_parts(int T, int H) {
-    (void)H;
-    return std::min(T, kNormBwdMaxParts);
-}
+// One workgroup per CU where a row takes 512 threads or more (16384 x 4096 with dweight: 97 us; 512
+// workgroups 105, 1024 115: their partial rows cost more than they hide), more of the smaller ones.
+int norm_bwd_parts(int T, int H) { return std::min(T, H <= 512 ? 2048 : H <= 2048 ? 512 : 256); }
 size_t norm_bwd_ws_bytes(int T, int H) { return (size_t)norm_bwd_parts(T, H) * H * 4; }
 
 // Up to 128 rows one workgroup does everything; beyond that 32 rows each (one for every 16 lanes of a

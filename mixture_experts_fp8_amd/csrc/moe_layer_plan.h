@@ -6,7 +6,6 @@
 namespace moe {
 
 // ---- RMS norm backward: weight-gradient partials, one row of H floats per workgroup
-constexpr int kNormBwdMaxParts = 512;
 int norm_bwd_parts(int T, int H);   // workgroups (= partial rows) of the backward kernel
 size_t norm_bwd_ws_bytes(int T, int H);
 
