@@ -9,6 +9,32 @@
 
 namespace moe {
 
+// 16- and 8-byte accesses; ST (streamed): past the caches, for matrices larger than they are.
+typedef unsigned v4u_t __attribute__((ext_vector_type(4)));
+typedef unsigned v2u_t __attribute__((ext_vector_type(2)));
+template <bool ST>
+__device__ __forceinline__ uint4 ld16(const void* p) {
+    const v4u_t* q = reinterpret_cast<const v4u_t*>(p);
+    const v4u_t v = ST ? __builtin_nontemporal_load(q) : *q;
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+template <bool ST>
+__device__ __forceinline__ void st16(void* p, uint4 v) {
+    const v4u_t x = {v.x, v.y, v.z, v.w};
+    if constexpr (ST) __builtin_nontemporal_store(x, reinterpret_cast<v4u_t*>(p));
+    else *reinterpret_cast<v4u_t*>(p) = x;
+}
+template <bool ST>
+__device__ __forceinline__ void st8(void* p, uint2 v) {
+    const v2u_t x = {v.x, v.y};
+    if constexpr (ST) __builtin_nontemporal_store(x, reinterpret_cast<v2u_t*>(p));
+    else *reinterpret_cast<v2u_t*>(p) = x;
+}
+// One of the matrices alone is larger than the L2s together, so none of them is found there by the next
+// operator (4096 x 7168 with residual and codes 55.2 -> 51.4 us, backward at 16384 x 4096 97 -> 90; at
+// 2048 x 2816, which fits, streaming costs 5%).
+static bool streamed(int T, int H) { return (int64_t)T * H * 2 >= (32 << 20); }
+
 // Lane exchange of both halves of a double by the DPP control word of dpp_f32.
 template <int CTRL>
 __device__ __forceinline__ double dpp_f64(double v) {
@@ -87,7 +113,7 @@ __device__ __forceinline__ uint2 group_codes(const float (&f)[8], int& e) {
 // max(1, 256 / G) rows.  The row's sum, its root and the two products are formed in double, which the
 // memory hides: y is then the definition's value rounded once, and the codes, which a value beside a
 // border would otherwise tip, are the definition's codes.
-template <int G, int VPT>
+template <int G, int VPT, bool ST>
 __global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_rmsnorm(NormArgs a) {
     constexpr int RPB = G < 256 ? 256 / G : 1;
     __shared__ double s_sum[G / 64];
@@ -101,14 +127,14 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_rmsnorm(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int v = sub + i * G;
-        if (v < nv) vx[i] = *reinterpret_cast<const uint4*>(xr + v * 8);
+        if (v < nv) vx[i] = ld16<ST>(xr + v * 8);
         else vx[i] = make_uint4(0, 0, 0, 0);
     }
     if (rr) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = sub + i * G;
-            if (v < nv) vr[i] = *reinterpret_cast<const uint4*>(rr + v * 8);
+            if (v < nv) vr[i] = ld16<ST>(rr + v * 8);
             else vr[i] = make_uint4(0, 0, 0, 0);
         }
     }
@@ -140,7 +166,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_rmsnorm(NormArgs a) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = sub + i * G;
-            if (v < nv) *reinterpret_cast<uint4*>(a.h + t * a.H + v * 8) = vx[i];
+            if (v < nv) st16<ST>(a.h + t * a.H + v * 8, vx[i]);
         }
     }
     if (!a.y && !a.yq) return;   // (uniform)
@@ -155,15 +181,15 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_rmsnorm(NormArgs a) {
         for (int j = 0; j < 8; ++j) f[j] = round_odd((double)f[j] * r * (double)w[j]);
         const uint4 o = pack8(f);
         if (v < nv) {   // a scale's lanes are all in or all out: H is a multiple of its columns
-            if (a.y) *reinterpret_cast<uint4*>(a.y + t * a.H + v * 8) = o;
+            if (a.y) st16<ST>(a.y + t * a.H + v * 8, o);
             if (a.yq) {
                 unpack8(o, f);
                 int e;
                 if (a.group == 128) {
-                    *reinterpret_cast<uint2*>(a.yq + t * a.H + v * 8) = group_codes<16>(f, e);
+                    st8<ST>(a.yq + t * a.H + v * 8, group_codes<16>(f, e));
                     if ((v & 15) == 0) a.ys[t * (a.H >> 7) + (v >> 4)] = (uint8_t)(e + 127);
                 } else {
-                    *reinterpret_cast<uint2*>(a.yq + t * a.H + v * 8) = group_codes<4>(f, e);
+                    st8<ST>(a.yq + t * a.H + v * 8, group_codes<4>(f, e));
                     if ((v & 3) == 0) a.ys[t * (a.H >> 5) + (v >> 2)] = (uint8_t)(e + 127);
                 }
             }
@@ -174,7 +200,9 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_rmsnorm(NormArgs a) {
 template <int G, int VPT>
 static void run_norm(const NormArgs& a, hipStream_t st) {
     constexpr int RPB = G < 256 ? 256 / G : 1;
-    hipLaunchKernelGGL((k_add_rmsnorm<G, VPT>), dim3((unsigned)ceil_div(a.T, RPB)), dim3(G < 256 ? 256 : G), 0, st, a);
+    const dim3 grid((unsigned)ceil_div(a.T, RPB)), block(G < 256 ? 256 : G);
+    if (streamed(a.T, a.H)) hipLaunchKernelGGL((k_add_rmsnorm<G, VPT, true>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((k_add_rmsnorm<G, VPT, false>), grid, block, 0, st, a);
 }
 
 hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t st) {
@@ -182,7 +210,7 @@ hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t st) {
     if (nv <= 64) run_norm<64, 1>(a, st);
     else if (nv <= 256) run_norm<256, 1>(a, st);
     else if (nv <= 512) run_norm<512, 1>(a, st);
-    else if (nv <= 1024) run_norm<512, 2>(a, st);   // 4096 x 7168 with residual and codes: 50.5 us, 1024 threads 51.4
+    else if (nv <= 1024) run_norm<512, 2>(a, st);   // (with one vector each, 1024 threads are 2% slower at 4096 x 7168)
     else if (nv <= 2048) run_norm<1024, 2>(a, st);
     else run_norm<1024, 4>(a, st);
     return hipGetLastError();
@@ -193,7 +221,7 @@ hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t st) {
 // gradient sum_t dy xhat.  A workgroup walks rows blockIdx.x, + gridDim.x, ... and keeps its
 // share of the weight gradient in registers; the workgroups' sums go to `part` and are added in
 // workgroup order by k_norm_dw.
-template <int G, int VPT>
+template <int G, int VPT, bool ST>
 __global__ __launch_bounds__(G) void k_add_rmsnorm_bwd(NormBwdArgs a) {
     __shared__ float s_sum[2][2][G / 64];
     const int sub = threadIdx.x, nv = a.H >> 3;
@@ -217,9 +245,9 @@ __global__ __launch_bounds__(G) void k_add_rmsnorm_bwd(NormBwdArgs a) {
             const int64_t o = t * a.H + v * 8;
             x.h[i] = x.d[i] = x.r[i] = make_uint4(0, 0, 0, 0);
             if (v < nv) {
-                x.h[i] = *reinterpret_cast<const uint4*>(a.h + o);
-                x.d[i] = *reinterpret_cast<const uint4*>(a.dy + o);
-                if (a.dh) x.r[i] = *reinterpret_cast<const uint4*>(a.dh + o);
+                x.h[i] = ld16<ST>(a.h + o);
+                x.d[i] = ld16<ST>(a.dy + o);
+                if (a.dh) x.r[i] = ld16<ST>(a.dh + o);
             }
         }
     };
@@ -274,7 +302,7 @@ __global__ __launch_bounds__(G) void k_add_rmsnorm_bwd(NormBwdArgs a) {
                 const float g = r * (d[j] * w[i][j] - h[j] * c);
                 e[j] = a.dh ? g + e[j] : g;
             }
-            if (v < nv) *reinterpret_cast<uint4*>(a.dx + t * a.H + v * 8) = pack8(e);
+            if (v < nv) st16<ST>(a.dx + t * a.H + v * 8, pack8(e));
         }
     }
     if (a.dw) {
@@ -316,7 +344,8 @@ __global__ __launch_bounds__(256) void k_norm_dw(const float* __restrict__ part,
 
 template <int G, int VPT>
 static void run_norm_bwd(const NormBwdArgs& a, int grid, hipStream_t st) {
-    hipLaunchKernelGGL((k_add_rmsnorm_bwd<G, VPT>), dim3(grid), dim3(G), 0, st, a);
+    if (streamed(a.T, a.H)) hipLaunchKernelGGL((k_add_rmsnorm_bwd<G, VPT, true>), dim3(grid), dim3(G), 0, st, a);
+    else hipLaunchKernelGGL((k_add_rmsnorm_bwd<G, VPT, false>), dim3(grid), dim3(G), 0, st, a);
 }
 
 hipError_t launch_add_rmsnorm_backward(const NormBwdArgs& a, hipStream_t st) {
