@@ -45,26 +45,48 @@ __device__ __forceinline__ float act_fn(float v, int act) {
     }
 }
 
-// Four consecutive columns of a row: act(v + bias) + residual, stored in y's type.
-__device__ __forceinline__ void put4(const LinArgs& a, int64_t row, int col, v4f v) {
+// Bias and residual of four consecutive columns of a row, and the finished columns from their sum:
+// act(v + bias) + residual, stored in y's type.
+struct Extra {
+    v4f bias;
+    v4u_t res;   // bf16: two words
+};
+__device__ __forceinline__ Extra load_extra(const LinArgs& a, int64_t row, int col) {
+    Extra e;
+    e.bias = v4f{0.f, 0.f, 0.f, 0.f};
+    e.res = v4u_t{0, 0, 0, 0};
     if (a.bias) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += a.bias[col + i];
+        for (int i = 0; i < 4; ++i) e.bias[i] = a.bias[col + i];   // (4-byte aligned)
     }
+    if (a.res) {
+        if (a.out_bf16) {
+            const uint2 r = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(a.res) + row * a.ldr + col);
+            e.res[0] = r.x;
+            e.res[1] = r.y;
+        } else {
+            e.res = *reinterpret_cast<const v4u_t*>(reinterpret_cast<const float*>(a.res) + row * a.ldr + col);
+        }
+    }
+    return e;
+}
+__device__ __forceinline__ void put4(const LinArgs& a, int64_t row, int col, v4f v, const Extra& e) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = act_fn(v[i], a.act);
+    for (int i = 0; i < 4; ++i) v[i] = act_fn(v[i] + e.bias[i], a.act);
     if (a.out_bf16) {
         if (a.res) {
-            const uint2 r = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(a.res) + row * a.ldr + col);
-            v[0] += __uint_as_float(r.x << 16);
-            v[1] += __uint_as_float(r.x & 0xFFFF0000u);
-            v[2] += __uint_as_float(r.y << 16);
-            v[3] += __uint_as_float(r.y & 0xFFFF0000u);
+            v[0] += __uint_as_float(e.res[0] << 16);
+            v[1] += __uint_as_float(e.res[0] & 0xFFFF0000u);
+            v[2] += __uint_as_float(e.res[1] << 16);
+            v[3] += __uint_as_float(e.res[1] & 0xFFFF0000u);
         }
         *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.y) + row * a.ldy + col) =
             make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
     } else {
-        if (a.res) v += *reinterpret_cast<const v4f*>(reinterpret_cast<const float*>(a.res) + row * a.ldr + col);
+        if (a.res) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] += __uint_as_float(e.res[i]);
+        }
         *reinterpret_cast<v4f*>(reinterpret_cast<float*>(a.y) + row * a.ldy + col) = v;
     }
 }
@@ -130,6 +152,16 @@ __global__ __launch_bounds__(64 * WK) void k_linear_stream(LinArgs a) {
     const int nk = KB > wv ? (KB - wv + WK - 1) / WK : 0;   // blocks wv, wv + WK, ... of this wave
 #pragma unroll
     for (int p = 0; p < PF; ++p) load(p, wv + p * WK);
+    // the bias and residual of the fragments that this wave will finish, fetched over the K loop
+    constexpr int QN = (MF * NF + WK - 1) / WK;
+    Extra ex[QN];
+    bool live[QN];
+#pragma unroll
+    for (int n = 0; n < QN; ++n) {
+        const int q = wv + n * WK, i = q / NF, j = q - i * NF, row = m0 + i * 16 + r16;
+        live[n] = q < MF * NF && n0 + j < n16s && row < a.T;
+        if (live[n]) ex[n] = load_extra(a, row, (n0 + j) * 16 + 4 * G);
+    }
     int i0 = 0;
     for (; i0 + PF <= nk; i0 += PF) {
 #pragma unroll
@@ -150,12 +182,15 @@ __global__ __launch_bounds__(64 * WK) void k_linear_stream(LinArgs a) {
 #pragma unroll
         for (int j = 0; j < NF; ++j) s_acc[wv][i * NF + j][lane] = acc[i][j];
     __syncthreads();
-    for (int q = wv; q < MF * NF; q += WK) {
-        v4f v = s_acc[0][q][lane];
 #pragma unroll
-        for (int w = 1; w < WK; ++w) v += s_acc[w][q][lane];
-        const int i = q / NF, j = q - i * NF, col = (n0 + j) * 16 + 4 * G, row = m0 + i * 16 + r16;
-        if (n0 + j < n16s && row < a.T) put4(a, row, col, v);
+    for (int n = 0; n < QN; ++n) {
+        const int q = wv + n * WK, i = q / NF, j = q - i * NF;
+        if (live[n]) {
+            v4f v = s_acc[0][q][lane];
+#pragma unroll
+            for (int w = 1; w < WK; ++w) v += s_acc[w][q][lane];
+            put4(a, m0 + i * 16 + r16, (n0 + j) * 16 + 4 * G, v, ex[n]);
+        }
     }
 }
 

@@ -224,7 +224,7 @@ __global__ __launch_bounds__(1024) void k_balance_reduce(BalanceArgs a, BalanceP
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     int4 n = make_int4(0, 0, 0, 0);
     if (e0 < a.E) {
-#pragma unroll 4
+#pragma unroll 8
         for (int b = b0 + g; b < b1; b += NG) {
             const int64_t o = (int64_t)(b + s) * p.stride + e0;   // (rows of `stride` = E rounded up to 4)
             const float4 x = *reinterpret_cast<const float4*>(probs + o);
