@@ -63,6 +63,11 @@ struct Seqs {
 // sees its row's spread of logits.
 __device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
 
+// Natural logarithm and reciprocal by their instructions (one unit in the last place): with IEEE
+// divisions and library logarithms the gradient of 16384 x 128 logits takes 7.6 us instead of 6.9.
+__device__ __forceinline__ float log_fast(float x) { return __builtin_amdgcn_logf(x) * 0.69314718f; }
+__device__ __forceinline__ float rcp_or_0(float x) { return x != 0.f ? __builtin_amdgcn_rcpf(x) : 0.f; }
+
 // Softmax numerators of a row: v -> exp(v - max); returns their sum (0 only where every logit is
 // -infinity) and the shift.  NaN logits make the sum NaN.
 template <int L, int Q>
@@ -108,15 +113,22 @@ __device__ __forceinline__ void put_losses(const BalanceArgs& a, float bal, floa
 // part's slot.  ONE: a single workgroup holds all rows and writes the results itself, which saves the
 // second launch and its latency (64 x 8: 10 -> 4 us).
 constexpr int kRowsThreads = 512;
+constexpr int kSeqLds = 1024;   // sequence boundaries held in LDS (a search in memory waits for every step)
 template <int L, int Q, bool VEC, bool ONE>
 __global__ __launch_bounds__(kRowsThreads) void k_balance_rows(BalanceArgs a, BalancePlan p) {
     constexpr int NT = kRowsThreads, NG = NT / L, N = 4 * Q;
     __shared__ __align__(16) float s_p[NG][L * N];
     __shared__ int s_hit[L * N];
     __shared__ float s_z[NG], s_w[NT / 64];
+    __shared__ int s_off[kSeqLds + 1];
     const int tid = threadIdx.x, g = tid / L, sub = tid % L, b = blockIdx.x;
     if (!ONE && b == 0 && tid == 0) *reinterpret_cast<int*>(a.ws + p.done) = 0;   // the second kernel's ticket
-    const Seqs sq{a.off, a.S, a.T};
+    const bool staged = a.off && a.S <= kSeqLds;
+    if (staged) {
+        for (int i = tid; i <= a.S; i += NT) s_off[i] = a.off[i];
+        __syncthreads();
+    }
+    const Seqs sq{staged ? s_off : a.off, a.S, a.T};
     const int lo = b * p.chunk, hi = min(a.T, lo + p.chunk);
     float bal = 0.f, ztot = 0.f;
     int live = 0, valid = 0;
@@ -148,7 +160,7 @@ __global__ __launch_bounds__(kRowsThreads) void k_balance_rows(BalanceArgs a, Ba
             if (a.scoring != MOE_SCORING_SIGMOID || a.cz != 0.f) {
                 const float sum = softmax_row<L, Q>(v, shift);
                 if (sum != 0.f) {
-                    const float lse = shift + logf(sum);
+                    const float lse = shift + log_fast(sum);
                     z = fmaf(lse, lse, z);
                 }
                 if (a.scoring != MOE_SCORING_SIGMOID) {
@@ -157,7 +169,7 @@ __global__ __launch_bounds__(kRowsThreads) void k_balance_rows(BalanceArgs a, Ba
                     for (int i = 0; i < N; ++i) num[i] = v[i];
                 }
             }
-            const float inv = tot != 0.f ? 1.0f / tot : 0.f;
+            const float inv = rcp_or_0(tot);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 acc[i] = fmaf(num[i], inv, acc[i]);
@@ -342,8 +354,6 @@ hipError_t launch_balance_loss(const BalanceArgs& a, hipStream_t st) {
 //   weights, softmax   rsf p (D - sum p D)
 //            over the chosen (softmax renormalised; sigmoid with a factor 1 - s):
 //                      rsf q (D - m sum q D),  q = score / sum m score
-constexpr int kSeqLds = 1024;   // sequence boundaries held in LDS
-
 // Orders the LDS accesses of a wave's own lanes (a row's lanes are in one wave).
 __device__ __forceinline__ void wave_lds_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
@@ -401,7 +411,7 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouteBwdArgs a) {
         for (int i = 0; i < N; ++i) v[i] = l[i];
         float sum = 0.f;
         if (!sig || a.cz != 0.f) sum = softmax_row<L, Q>(v, shift);
-        const float inv = sum != 0.f ? 1.0f / sum : 0.f;
+        const float inv = rcp_or_0(sum);
         float pinv = inv;
         if (sig) {
             float z = 0.f;
@@ -413,7 +423,7 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouteBwdArgs a) {
                 z += sc[i];
             }
             z = rsum<L>(z);
-            pinv = z != 0.f ? 1.0f / z : 0.f;
+            pinv = rcp_or_0(z);
         } else {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
@@ -422,17 +432,23 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouteBwdArgs a) {
             }
         }
         if (a.counts) {
-            const float len = (float)(t1 - t0);
-            const float cu = a.ca / (float)live * ((float)a.E / (float)a.k) / len / len;
+            const float rl = __builtin_amdgcn_rcpf((float)(t1 - t0));
+            const float cu = a.ca * __builtin_amdgcn_rcpf((float)live) * a.load * rl * rl;
             float pu = 0.f;
 #pragma unroll
-            for (int i = 0; i < N; ++i) pu = fmaf(sc[i] * pinv, cu * (float)c[i], pu);
-            pu = rsum<L>(pu);
+            for (int i = 0; i < N; ++i) pu = fmaf(sc[i], (float)c[i], pu);
+            pu = rsum<L>(pu) * pinv;      // sum p c
+            const float f = cu * pinv;
+            if (sig) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) d[i] = sc[i] * pinv * om[i] * (cu * (float)c[i] - pu);
+                for (int i = 0; i < N; ++i) d[i] = f * sc[i] * om[i] * ((float)c[i] - pu);
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) d[i] = f * sc[i] * ((float)c[i] - pu);
+            }
         }
         if (a.cz != 0.f && sum != 0.f) {
-            const float cz = 2.0f * a.cz / (float)valid * (shift + logf(sum)) * inv;
+            const float cz = 2.0f * a.cz * __builtin_amdgcn_rcpf((float)valid) * (shift + log_fast(sum)) * inv;
 #pragma unroll
             for (int i = 0; i < N; ++i) d[i] = fmaf(cz, v[i], d[i]);
         }
@@ -478,10 +494,11 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouteBwdArgs a) {
             if (!sig && !a.renorm) {
                 float pd = 0.f;
 #pragma unroll
-                for (int i = 0; i < N; ++i) pd = fmaf(v[i] * inv, D[i], pd);
-                pd = rsum<L>(pd);
+                for (int i = 0; i < N; ++i) pd = fmaf(v[i], D[i], pd);
+                pd = rsum<L>(pd) * inv;
+                const float f = a.rsf * inv;
 #pragma unroll
-                for (int i = 0; i < N; ++i) d[i] = fmaf(a.rsf * v[i] * inv, D[i] - pd, d[i]);
+                for (int i = 0; i < N; ++i) d[i] = fmaf(f * v[i], D[i] - pd, d[i]);
             } else {
                 float q[N], mx = -INFINITY, z = 0.f, qd = 0.f;
                 if (!sig) {   // shifted by the largest chosen logit, as the forward weights are
@@ -498,11 +515,11 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouteBwdArgs a) {
                 }
                 z = rsum<L>(z);
                 qd = rsum<L>(qd);
-                const float zi = z != 0.f ? 1.0f / z : 0.f;
+                const float zi = rcp_or_0(z);
                 qd *= zi;
+                const float f = a.rsf * zi;
 #pragma unroll
-                for (int i = 0; i < N; ++i)
-                    d[i] = fmaf(a.rsf * q[i] * zi * om[i], D[i] - m[i] * qd, d[i]);
+                for (int i = 0; i < N; ++i) d[i] = fmaf(f * q[i] * om[i], D[i] - m[i] * qd, d[i]);
             }
         }
     }

@@ -106,6 +106,7 @@ struct RouteBwdArgs {
     const int32_t* off;
     float ca, cz;
     float* dlogits;
+    float load;           // E / k
 };
 hipError_t launch_route_backward(const RouteBwdArgs& a, hipStream_t st);
 

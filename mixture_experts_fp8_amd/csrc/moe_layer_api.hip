@@ -63,7 +63,8 @@ int moe_route_backward(const moe_route_backward_args* a) {
     const moe_route_params* p = a->route;
     const moe::RouteBwdArgs b{a->T, p->num_experts, p->top_k, a->num_seqs, p->scoring, p->renormalize != 0,
                               p->routed_scaling_factor, a->router_logits, a->topk_ids, a->dtopk_weights, a->counts,
-                              a->seq_offsets, a->balance_coef, a->z_coef, a->dlogits};
+                              a->seq_offsets, a->balance_coef, a->z_coef, a->dlogits,
+                              (float)p->num_experts / (float)p->top_k};
     return done("moe_route_backward", moe::launch_route_backward(b, static_cast<hipStream_t>(a->stream)));
 }
 
