@@ -9,6 +9,7 @@
 #include "layer_common.h"
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 namespace moe {
@@ -349,6 +350,61 @@ __device__ __forceinline__ void tile_epilogue(const LinArgs& a, v4f (&acc)[MI][4
     }
 }
 
+template <int MI>
+__device__ __forceinline__ void tile_finish(const LinArgs& a, v4f (&acc)[MI][4], const v4f (&b)[4], uint4 (&q)[MI][2],
+                                            int row0, int col0) {
+    switch (a.act) {
+        case MOE_ACT_RELU: return tile_epilogue<MI, MOE_ACT_RELU>(a, acc, b, q, row0, col0);
+        case MOE_ACT_SILU: return tile_epilogue<MI, MOE_ACT_SILU>(a, acc, b, q, row0, col0);
+        case MOE_ACT_GELU: return tile_epilogue<MI, MOE_ACT_GELU>(a, acc, b, q, row0, col0);
+        case MOE_ACT_GELU_TANH: return tile_epilogue<MI, MOE_ACT_GELU_TANH>(a, acc, b, q, row0, col0);
+        default: return tile_epilogue<MI, MOE_ACT_NONE>(a, acc, b, q, row0, col0);
+    }
+}
+
+// Work order: workgroup L runs on XCD L % 8; XCD x takes a contiguous share of the list, which walks the
+// row tiles in groups of 8 with the column tile outside, so that one XCD's workgroups share both
+// operands through its L2.  False for the holes behind the last tile.
+__device__ __forceinline__ bool tile_of(int tiles_m, int tiles_n, int& tm, int& tn) {
+    const int total = tiles_m * tiles_n, per = (total + 7) / 8, L = blockIdx.x;
+    const int w = (L & 7) * per + (L >> 3);
+    if ((L >> 3) >= per || w >= total) return false;
+    const int sb = w / (8 * tiles_n), r = w - sb * 8 * tiles_n, g = min(8, tiles_m - sb * 8);
+    tn = r / g;
+    tm = sb * 8 + r - tn * g;
+    return true;
+}
+
+// 128-element scales of all K blocks: the rows' as [kb][wave row][row % 16][fragment], the weights' as
+// [kb][column block of the tile].  8 threads per row of xs.
+template <int MI, int ROWS, int NTH, int NBW>
+__device__ __forceinline__ void load_scale_tables(const LinArgs& a, uint8_t* s_x, uint8_t* s_w, int KB, int nbs, int m0,
+                                                  int n0) {
+    const int tid = threadIdx.x;
+    const int c = tid & 7;
+    auto pos = [&](int q) { return (q / (16 * MI)) * 16 * MI + (q % 16) * MI + (q / 16) % MI; };
+    if (KB % 4 == 0 && (reinterpret_cast<uintptr_t>(a.xs) & 3) == 0) {
+        for (int k4 = c; k4 < KB / 4; k4 += 8) {
+            uint32_t v[ROWS * 8 / NTH];
+#pragma unroll
+            for (int i = 0; i < ROWS * 8 / NTH; ++i)
+                v[i] = reinterpret_cast<const uint32_t*>(a.xs)[(int64_t)min(m0 + (tid >> 3) + i * (NTH / 8), a.T - 1) * (KB / 4) + k4];
+#pragma unroll
+            for (int i = 0; i < ROWS * 8 / NTH; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    s_x[(4 * k4 + k) * ROWS + pos((tid >> 3) + i * (NTH / 8))] = (uint8_t)(v[i] >> (8 * k));
+        }
+    } else {
+        for (int q = tid >> 3; q < ROWS; q += NTH / 8)
+            for (int kb = c; kb < KB; kb += 8)
+                s_x[kb * ROWS + pos(q)] = a.xs[(int64_t)min(m0 + q, a.T - 1) * KB + kb];
+    }
+    for (int kb = tid; kb < KB; kb += NTH)
+#pragma unroll
+        for (int i = 0; i < NBW; ++i) s_w[kb * NBW + i] = a.ws[(int64_t)kb * nbs + min(n0 / kGroup + i, nbs - 1)];
+}
+
 template <bool MX, int MI, int NJ, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_tile(LinArgs a, int tiles_m, int tiles_n) {
     static_assert(NJ == 4, "the epilogue takes 64 columns");
@@ -363,18 +419,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_tile(LinArgs a, int 
     uint8_t* s_w = s_x + KB * ROWS;            // (128-element scales) [KB][column blocks of the tile]
     float* s_bias = reinterpret_cast<float*>(MX ? s_x + 3 * SCST : s_w + (KB * NBW + 15) / 16 * 16);   // [COLS]
 
-    // Work order: workgroup L runs on XCD L % 8; XCD x takes a contiguous share of the list, which walks
-    // the row tiles in groups of 8 with the column tile outside, so that one XCD's workgroups share both
-    // operands through its L2.
     int tm, tn;
-    {
-        const int total = tiles_m * tiles_n, per = (total + 7) / 8, L = blockIdx.x;
-        const int w = (L & 7) * per + (L >> 3);
-        if ((L >> 3) >= per || w >= total) return;
-        const int sb = w / (8 * tiles_n), r = w - sb * 8 * tiles_n, g = min(8, tiles_m - sb * 8);
-        tn = r / g;
-        tm = sb * 8 + r - tn * g;
-    }
+    if (!tile_of(tiles_m, tiles_n, tm, tn)) return;
     // Two workgroups share a CU.  The one that was dealt second runs ahead at equal work, so that their
     // epilogues (memory) and K loops (matrix cores) fall apart: 262 -> 258 us at 16384 x 4096 x 4096.
     if (MI > 4 && ((blockIdx.x >> 8) & 1)) __builtin_amdgcn_s_setprio(1);
@@ -447,30 +493,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_tile(LinArgs a, int 
     issue(min(1, KB - 1), 1);
     load_w(0, W0);
     for (int i = tid; i < COLS; i += NTH) s_bias[i] = a.bias && n0 + i < a.N ? a.bias[n0 + i] : 0.f;
-    if constexpr (!MX) {   // scale tables of all K blocks: 8 threads per row of xs
-        const int c = tid & 7;
-        auto pos = [&](int q) { return (q / (16 * MI)) * 16 * MI + (q % 16) * MI + (q / 16) % MI; };
-        if (KB % 4 == 0 && (reinterpret_cast<uintptr_t>(a.xs) & 3) == 0) {
-            for (int k4 = c; k4 < KB / 4; k4 += 8) {
-                uint32_t v[ROWS * 8 / NTH];
-#pragma unroll
-                for (int i = 0; i < ROWS * 8 / NTH; ++i)
-                    v[i] = reinterpret_cast<const uint32_t*>(a.xs)[(int64_t)min(m0 + (tid >> 3) + i * (NTH / 8), a.T - 1) * (KB / 4) + k4];
-#pragma unroll
-                for (int i = 0; i < ROWS * 8 / NTH; ++i)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        s_x[(4 * k4 + k) * ROWS + pos((tid >> 3) + i * (NTH / 8))] = (uint8_t)(v[i] >> (8 * k));
-            }
-        } else {
-            for (int q = tid >> 3; q < ROWS; q += NTH / 8)
-                for (int kb = c; kb < KB; kb += 8)
-                    s_x[kb * ROWS + pos(q)] = a.xs[(int64_t)min(m0 + q, a.T - 1) * KB + kb];
-        }
-        for (int kb = tid; kb < KB; kb += NTH)
-#pragma unroll
-            for (int i = 0; i < NBW; ++i) s_w[kb * NBW + i] = a.ws[(int64_t)kb * nbs + min(n0 / kGroup + i, nbs - 1)];
-    }
+    if constexpr (!MX) load_scale_tables<MI, ROWS, NTH, NBW>(a, s_x, s_w, KB, nbs, m0, n0);
 
     v4f acc[MI][NJ];
 #pragma unroll
@@ -544,16 +567,27 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_tile(LinArgs a, int 
     v4f bias[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) bias[j] = *reinterpret_cast<const v4f*>(s_bias + wn * NJ * 16 + 16 * j + 4 * G);
-    auto out = [&](auto A) __attribute__((always_inline)) {
-        tile_epilogue<MI, decltype(A)::value>(a, acc, bias, res, row0, col0);
-    };
-    switch (a.act) {
-        case MOE_ACT_RELU: out(std::integral_constant<int, MOE_ACT_RELU>{}); break;
-        case MOE_ACT_SILU: out(std::integral_constant<int, MOE_ACT_SILU>{}); break;
-        case MOE_ACT_GELU: out(std::integral_constant<int, MOE_ACT_GELU>{}); break;
-        case MOE_ACT_GELU_TANH: out(std::integral_constant<int, MOE_ACT_GELU_TANH>{}); break;
-        default: out(std::integral_constant<int, MOE_ACT_NONE>{});
+    tile_finish<MI>(a, acc, bias, res, row0, col0);
+}
+
+// Launches a tiled kernel.  More than 64 KB of LDS has to be asked for, once per kernel and device.
+constexpr int kLdsBytes = 160 * 1024;
+template <auto Kern>
+static hipError_t launch_tiles(const LinArgs& a, int tm, int tn, int threads, size_t lds, hipStream_t st) {
+    if (lds > 64 * 1024) {
+        static std::atomic<uint64_t> asked{0};   // a bit per device
+        int dev = 0;
+        hipError_t e = hipGetDevice(&dev);
+        if (e != hipSuccess) return e;
+        const uint64_t bit = 1ull << (dev & 63);
+        if (dev > 63 || !(asked.load(std::memory_order_relaxed) & bit)) {
+            e = hipFuncSetAttribute(reinterpret_cast<const void*>(Kern), hipFuncAttributeMaxDynamicSharedMemorySize, kLdsBytes);
+            if (e != hipSuccess) return e;
+            asked.fetch_or(bit, std::memory_order_relaxed);
+        }
     }
+    hipLaunchKernelGGL(Kern, dim3((unsigned)(ceil_div((int64_t)tm * tn, 8) * 8)), dim3(threads), lds, st, a, tm, tn);
+    return hipGetLastError();
 }
 
 template <bool MX, int MI, int NJ, int WM, int WN>
@@ -562,19 +596,185 @@ static hipError_t run_tile_t(const LinArgs& a, hipStream_t st) {
     const int tm = (int)ceil_div(a.T, ROWS), tn = (int)ceil_div(a.N, COLS), KB = a.K / kGroup;
     const size_t lds = 3 * ROWS * kGroup + COLS * 4 +
                        (MX ? 3 * ROWS * 4 : (size_t)KB * ROWS + (KB * ((COLS + 127) / 128) + 15) / 16 * 16);
-    auto kern = k_linear_tile<MX, MI, NJ, WM, WN>;
-    if (lds > 64 * 1024) {
-        const hipError_t e =
-            hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-        if (e != hipSuccess) return e;
-    }
-    const int64_t total = (int64_t)tm * tn;
-    hipLaunchKernelGGL(kern, dim3((unsigned)(ceil_div(total, 8) * 8)), dim3(64 * WM * WN), lds, st, a, tm, tn);
-    return hipGetLastError();
+    return launch_tiles<k_linear_tile<MX, MI, NJ, WM, WN>>(a, tm, tn, 64 * WM * WN, lds, st);
 }
 template <int MI, int NJ, int WM, int WN>
 static hipError_t run_tile(const LinArgs& a, hipStream_t st) {
     return a.mx ? run_tile_t<true, MI, NJ, WM, WN>(a, st) : run_tile_t<false, MI, NJ, WM, WN>(a, st);
+}
+
+// ----------------------------------------------------------------------------------------
+// The same product where there are too few tiles to hide a K block's latency behind another workgroup:
+// both operands go through LDS, so that the copies are this kernel's only outstanding loads and their
+// number can be waited for.  S stages hold S - 2 K blocks on their way while block kb's products run
+// and block kb + 1's operands are read.  (A second set of waves, each taking every other K block, is slower: 512 x 4096 x 4096
+// 17.6 us instead of 15.6.)
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+    asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+
+template <bool MX, int MI, int NJ, int WM, int WN, int S>
+__global__ __launch_bounds__(64 * WM * WN, 1) void k_linear_deep(LinArgs a, int tiles_m, int tiles_n) {
+    constexpr int NW = WM * WN, ROWS = 16 * MI * WM, COLS = 16 * NJ * WN, NTH = 64 * NW;
+    constexpr int DX = ROWS / 8 / NW, DW = COLS / 8 / NW;            // 1 KB copies of a wave and block
+    constexpr int XB = ROWS * kGroup, WB = COLS * kGroup;
+    constexpr int XS = MX ? ROWS * 4 : 0, WS = MX ? COLS * 4 : 0;    // MX: scales of a block
+    constexpr int DS = MX ? (ROWS + COLS) / 64 / NW + ((ROWS + COLS) / 64 % NW != 0) : 0;   // 256-byte copies
+    constexpr int STAGE = XB + WB + XS + WS, OPS = DX + DW + DS;
+    static_assert(ROWS / 8 % NW == 0 && COLS / 8 % NW == 0 && ROWS % 64 == 0 && COLS % 64 == 0 && S >= 3, "whole copies");
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int KB = a.K / kGroup, nbs = (a.N + kGroup - 1) / kGroup;
+    constexpr int NBW = (COLS + 127) / 128, gpb = MX ? 4 : 1;
+    uint8_t* s_x = smem + S * STAGE;            // (128-element scales) [KB][WM][16][MI] bytes
+    uint8_t* s_w = s_x + KB * ROWS;             // (128-element scales) [KB][column blocks of the tile]
+    float* s_bias = reinterpret_cast<float*>(MX ? s_x : s_w + (KB * NBW + 15) / 16 * 16);   // [COLS]
+    int tm, tn;
+    if (!tile_of(tiles_m, tiles_n, tm, tn)) return;
+    const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wv / WN, wn = wv % WN, r16 = lane & 15, G = lane >> 4, x8 = r16 & 7;
+    const int m0 = tm * ROWS, n0 = tn * COLS, n16s = a.N / 16;
+    const v4i_t rx = make_srd(a.xq, (uint32_t)a.T * (uint32_t)a.K);
+    const v4i_t rw = make_srd(a.w, (uint32_t)a.K * (uint32_t)a.N);
+    const v4i_t rxs = make_srd(a.xs, (uint32_t)a.T * (uint32_t)(KB * gpb));
+    const v4i_t rws = make_srd(a.ws, MX ? (uint32_t)KB * (uint32_t)n16s * 64u : (uint32_t)KB * (uint32_t)nbs);
+
+    uint4 res[MI][2];
+    const int col0 = n0 + wn * NJ * 16, row0 = m0 + wm * MI * 16 + r16;
+    tile_residual<MI>(a, res, row0, col0);
+
+    uint32_t xoff[DX], wsrc[DW];   // rows as in k_linear_tile; weights: copy i of the wave, half a fragment
+#pragma unroll
+    for (int i = 0; i < DX; ++i) {
+        const int row = min(m0 + 8 * (wv + NW * i) + (lane >> 3), a.T - 1), slot = (lane & 7) ^ (lane >> 3);
+        const int chunk = MX ? slot : (slot < 4 ? 2 * slot : 2 * slot - 7);
+        xoff[i] = (uint32_t)row * (uint32_t)a.K + 16 * chunk;
+    }
+#pragma unroll
+    for (int i = 0; i < DW; ++i) {
+        const int g = wv + NW * i;
+        wsrc[i] = __builtin_amdgcn_readfirstlane((uint32_t)min(n0 / 16 + (g >> 1), n16s - 1) * (uint32_t)KB * kFragBytes + (g & 1) * 1024);
+    }
+    const uint32_t l16 = 16 * lane, lds0 = lds_addr(smem);
+    uint32_t soff[DS ? DS : 1], sdst[DS ? DS : 1];
+    bool srow[DS ? DS : 1];
+    if constexpr (MX) {   // the rows' dwords [wm][row % 16][fragment], then the column fragments' 64 bytes each
+#pragma unroll
+        for (int i = 0; i < DS; ++i) {
+            const int c = min(wv + NW * i, (ROWS + COLS) / 64 - 1);   // (past the last: the last again)
+            srow[i] = c < ROWS / 64;
+            if (srow[i]) {
+                const int pos = c * 64 + lane;
+                const int row = min(m0 + pos / (16 * MI) * (16 * MI) + (pos % MI) * 16 + (pos / MI) % 16, a.T - 1);
+                soff[i] = (uint32_t)row * (uint32_t)(KB * 4);
+            } else {
+                const int q = (c - ROWS / 64) * 64 + lane;            // dword q of the tile's fragments
+                soff[i] = (uint32_t)min(n0 / 16 + q / 16, n16s - 1) * (uint32_t)KB * 64 + (q % 16) * 4;
+            }
+            sdst[i] = XB + WB + c * 256;
+        }
+    }
+    auto issue = [&](int blk, int st) __attribute__((always_inline)) {
+        const int kb = min(blk, KB - 1);   // (past the end the last block again: the count per step stays)
+        const uint32_t base = __builtin_amdgcn_readfirstlane(lds0 + st * STAGE + wv * 1024);
+#pragma unroll
+        for (int i = 0; i < DX; ++i) dma16(rx, base + i * NW * 1024, xoff[i], kb * kGroup);
+#pragma unroll
+        for (int i = 0; i < DW; ++i) dma16(rw, base + XB + i * NW * 1024, l16, wsrc[i] + kb * kFragBytes);
+        if constexpr (MX) {
+#pragma unroll
+            for (int i = 0; i < DS; ++i) {
+                const uint32_t d = __builtin_amdgcn_readfirstlane(lds0 + st * STAGE + sdst[i]);
+                if (srow[i]) dma4(rxs, d, soff[i], kb * 4);
+                else dma4(rws, d, soff[i], kb * 64);
+            }
+        }
+    };
+    if constexpr (!MX) load_scale_tables<MI, ROWS, NTH, NBW>(a, s_x, s_w, KB, nbs, m0, n0);
+    for (int i = tid; i < COLS; i += NTH) s_bias[i] = a.bias && n0 + i < a.N ? a.bias[n0 + i] : 0.f;
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s) issue(s, s);
+
+    struct Ops {
+        v8i x[MI], w[NJ];
+        int sx[MI], sw[NJ];
+    };
+    auto read = [&](int blk, int st, Ops& o) __attribute__((always_inline)) {
+        const uint8_t* cur = smem + st * STAGE;
+        const int kb = min(blk, KB - 1);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            const uint8_t* rowp = cur + ((wm * MI + i) * 16 + r16) * kGroup;
+            const uint4 lo = *reinterpret_cast<const uint4*>(rowp + ((G ^ x8) << 4));
+            const uint4 hi = *reinterpret_cast<const uint4*>(rowp + (((G + 4) ^ x8) << 4));
+            o.x[i] = v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+            if constexpr (MX) o.sx[i] = (int)(reinterpret_cast<const uint32_t*>(cur + XB + WB)[(wm * 16 + r16) * MI + i] >> (8 * G));
+            else o.sx[i] = s_x[kb * ROWS + (wm * 16 + r16) * MI + i];
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const uint8_t* f = cur + XB + (wn * NJ + j) * kFragBytes + l16;
+            const uint4 lo = *reinterpret_cast<const uint4*>(f), hi = *reinterpret_cast<const uint4*>(f + 1024);
+            o.w[j] = v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+            o.sw[j] = MX ? cur[XB + WB + XS + (wn * NJ + j) * 64 + lane] : s_w[kb * NBW + (wn * NJ * 16) / 128];
+        }
+    };
+    v4f acc[MI][NJ];
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    wait_vm<(S - 2) * OPS>();
+    __syncthreads();
+    Ops A, B;
+    read(0, 0, A);
+    int st = 0;   // stage of block i
+    auto step = [&](int i, Ops& C, Ops& N) __attribute__((always_inline)) {
+        wait_vm<(S - 3) * OPS>();   // block i + 1 has landed (this wave's copies) ...
+        __syncthreads();            // ... and everyone's; block i - 1's stage has been read by all
+        issue(i + S - 1, st == 0 ? S - 1 : st - 1);
+        st = st == S - 1 ? 0 : st + 1;
+        read(i + 1, st, N);
+    };
+    auto products = [&](Ops& C) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) acc[i][j] = mfma_fp8(C.w[j], C.x[i], acc[i][j], C.sw[j], C.sx[i]);
+    };
+    int i = 0;
+    for (; i + 2 < KB; i += 2) {
+        step(i, A, B);
+        products(A);
+        step(i + 1, B, A);
+        products(B);
+    }
+    if (i + 1 < KB) {
+        step(i, A, B);
+        products(A);
+        products(B);
+    } else {
+        products(A);
+    }
+    wait_all();
+
+    v4f bias[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) bias[j] = *reinterpret_cast<const v4f*>(s_bias + wn * NJ * 16 + 16 * j + 4 * G);
+    tile_finish<MI>(a, acc, bias, res, row0, col0);
+}
+
+template <bool MX, int MI, int NJ, int WM, int WN, int S>
+static hipError_t run_deep_t(const LinArgs& a, hipStream_t st) {
+    constexpr int ROWS = 16 * MI * WM, COLS = 16 * NJ * WN;
+    const int tm = (int)ceil_div(a.T, ROWS), tn = (int)ceil_div(a.N, COLS), KB = a.K / kGroup;
+    const size_t lds = S * (ROWS + COLS) * (kGroup + (MX ? 4 : 0)) + COLS * 4 +
+                       (MX ? 0 : (size_t)KB * ROWS + (KB * ((COLS + 127) / 128) + 15) / 16 * 16);
+    return launch_tiles<k_linear_deep<MX, MI, NJ, WM, WN, S>>(a, tm, tn, 64 * WM * WN, lds, st);
+}
+template <int MI, int NJ, int WM, int WN, int S>
+static hipError_t run_deep(const LinArgs& a, hipStream_t st) {
+    return a.mx ? run_deep_t<true, MI, NJ, WM, WN, S>(a, st) : run_deep_t<false, MI, NJ, WM, WN, S>(a, st);
 }
 
 template <int MF, int NF, int WK, int PF>
@@ -585,13 +785,17 @@ static hipError_t run_stream(const LinArgs& a, hipStream_t st) {
     return hipGetLastError();
 }
 
-// Variant by the number of workgroups that a tile size makes.  The stream kernel takes the smallest
-// tile that does not make more of them than there are CUs, 256 (below that a larger tile only
-// lengthens the one round: 32 x 4096 x 512 takes 6.7 us on 16 x 16 tiles and 11.7 on 32 x 32; above it
-// the operands are read again by every tile: 64 x 7168 x 7168 takes 20.7 us on 64 x 32 tiles, 224 of
-// them, and 37 on 16 x 32); no tile is taller than the rows need.  Beyond that the tiled kernel, two
-// of whose workgroups share a CU, by the same rule with 512 (192 x 7168 x 7168: 34 us, stream 45;
-// 384 x 2816 x 2816: 18.2, stream 22.8; 4096 x 4096 x 4096: 128 x 256 tiles 64, 64 x 128 tiles 88).
+// Variant by the number of workgroups that a tile size makes, times measured with a residual.
+//   * The stream kernel takes the smallest tile that does not make more of them than there are CUs,
+//     256: below that a larger tile only lengthens the one round (32 x 4096 x 512: 6.7 us on 16 x 16
+//     tiles, 11.7 on 32 x 32), above it every tile reads the operands again (64 x 7168 x 7168: 20.7 us on
+//     64 x 32 tiles, 224 of them, 37 on 16 x 32).  No tile is taller than the rows need.
+//   * 64 x 128 tiles with deep copies while at most two workgroups share a CU, with four stages where
+//     each has one to itself (512 x 4096 x 4096: 15.8 us; k_linear_tile on the same tiles 22.2;
+//     192 x 7168 x 7168: 22.8, 64 x 64 stream tiles 47) and three, which fit twice, else
+//     (1024 x 4096 x 4096: 24.1, four stages 29.7).
+//   * k_linear_tile beyond: 64 x 256 tiles up to 512 workgroups (2047 x 4096 x 4096: 39.2; 64 x 128 deep
+//     45.6), then 128 x 256 (4096 x 4096 x 4096: 65; 64 x 256 78).
 hipError_t launch_linear(const LinArgs& args, hipStream_t st) {
     LinArgs a = args;
     // Outputs larger than the L2s together leave past them: they would evict the operands that the
@@ -602,8 +806,8 @@ hipError_t launch_linear(const LinArgs& args, hipStream_t st) {
     if (fits(16, 32, 256) || a.T <= 16) return run_stream<1, 2, 4, 4>(a, st);
     if (fits(32, 32, 256) || a.T <= 32) return run_stream<2, 2, 4, 4>(a, st);
     if (fits(64, 32, 256) || a.T <= 64) return run_stream<4, 2, 4, 3>(a, st);
-    if (fits(64, 64, 256)) return run_stream<4, 4, 4, 2>(a, st);
-    if (fits(64, 128, 512)) return run_tile<4, 4, 1, 2>(a, st);
+    if (fits(64, 128, 256)) return run_deep<2, 4, 2, 2, 4>(a, st);
+    if (fits(64, 128, 512)) return run_deep<2, 4, 2, 2, 3>(a, st);
     if (fits(64, 256, 512)) return run_tile<4, 4, 1, 4>(a, st);
     return run_tile<8, 4, 1, 4>(a, st);
 }

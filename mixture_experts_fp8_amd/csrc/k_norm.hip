@@ -218,13 +218,17 @@ hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t st) {
 
 // ----------------------------------------------------------------------------------------
 // Backward.  With xhat = h r and g = dy w:  dx = r (g - xhat mean(g xhat)) + dh, and the weight
-// gradient sum_t dy xhat.  A workgroup walks rows blockIdx.x, + gridDim.x, ... and keeps its
-// share of the weight gradient in registers; the workgroups' sums go to `part` and are added in
-// workgroup order by k_norm_dw.
+// gradient sum_t dy xhat.  A workgroup of G threads (short rows: four waves with a row each) walks rows
+// a grid apart, keeps its share of the weight gradient in registers; the workgroups' sums go to `part`
+// and are added in workgroup order by k_norm_dw.
 template <int G, int VPT, bool ST>
-__global__ __launch_bounds__(G) void k_add_rmsnorm_bwd(NormBwdArgs a) {
+__global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_rmsnorm_bwd(NormBwdArgs a) {
+    constexpr int RPB = G < 256 ? 256 / G : 1;
+    static_assert(RPB == 1 || VPT == 1, "short rows are one vector per thread");
     __shared__ float s_sum[2][2][G / 64];
-    const int sub = threadIdx.x, nv = a.H >> 3;
+    __shared__ __align__(16) float s_dw[RPB][RPB > 1 ? G * 8 : 4];
+    const int sub = threadIdx.x % G, rw = threadIdx.x / G, nv = a.H >> 3;
+    const int64_t step = (int64_t)gridDim.x * RPB;
     float dw[VPT][8], w[VPT][8];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -253,12 +257,13 @@ __global__ __launch_bounds__(G) void k_add_rmsnorm_bwd(NormBwdArgs a) {
     };
     int par = 0;
     Row nx;
-    load(blockIdx.x, nx);
-    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, par ^= 1) {
+    const int64_t first = (int64_t)blockIdx.x * RPB + rw;
+    if (first < a.T) load(first, nx);
+    for (int64_t t = first; t < a.T; t += step, par ^= 1) {
         uint4 vh[VPT], vd[VPT], vr[VPT];
 #pragma unroll
         for (int i = 0; i < VPT; ++i) vh[i] = nx.h[i], vd[i] = nx.d[i], vr[i] = nx.r[i];
-        if (t + gridDim.x < a.T) load(t + gridDim.x, nx);   // in flight over this row's sums
+        if (t + step < a.T) load(t + step, nx);   // in flight over this row's sums
         // sum h^2 and sum g h in one exchange: mean(g xhat) = r sum(g h) / H
         float ss = 0.f, gh = 0.f;
 #pragma unroll
@@ -306,6 +311,17 @@ __global__ __launch_bounds__(G) void k_add_rmsnorm_bwd(NormBwdArgs a) {
         }
     }
     if (a.dw) {
+        if constexpr (RPB > 1) {   // the waves' sums, in order
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s_dw[rw][sub * 8 + j] = dw[0][j];
+            __syncthreads();
+            if (rw) return;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+#pragma unroll
+                for (int w = 1; w < RPB; ++w) dw[0][j] += s_dw[w][sub * 8 + j];
+            }
+        }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = sub + i * G;
@@ -344,12 +360,15 @@ __global__ __launch_bounds__(256) void k_norm_dw(const float* __restrict__ part,
 
 template <int G, int VPT>
 static void run_norm_bwd(const NormBwdArgs& a, int grid, hipStream_t st) {
-    if (streamed(a.T, a.H)) hipLaunchKernelGGL((k_add_rmsnorm_bwd<G, VPT, true>), dim3(grid), dim3(G), 0, st, a);
-    else hipLaunchKernelGGL((k_add_rmsnorm_bwd<G, VPT, false>), dim3(grid), dim3(G), 0, st, a);
+    if (streamed(a.T, a.H)) hipLaunchKernelGGL((k_add_rmsnorm_bwd<G, VPT, true>), dim3(grid), dim3(G < 256 ? 256 : G), 0, st, a);
+    else hipLaunchKernelGGL((k_add_rmsnorm_bwd<G, VPT, false>), dim3(grid), dim3(G < 256 ? 256 : G), 0, st, a);
 }
 
-hipError_t launch_add_rmsnorm_backward(const NormBwdArgs& a, hipStream_t st) {
+hipError_t launch_add_rmsnorm_backward(const NormBwdArgs& args, hipStream_t st) {
+    NormBwdArgs a = args;
     const int nv = a.H / 8, grid = norm_bwd_parts(a.T, a.H);
+    const bool one = grid == 1 && !(reinterpret_cast<uintptr_t>(a.dw) & 15);   // the only part is the sum
+    if (one) a.part = a.dw;
     if (nv <= 64) run_norm_bwd<64, 1>(a, grid, st);
     else if (nv <= 256) run_norm_bwd<256, 1>(a, grid, st);
     else if (nv <= 512) run_norm_bwd<512, 1>(a, grid, st);
@@ -357,7 +376,7 @@ hipError_t launch_add_rmsnorm_backward(const NormBwdArgs& a, hipStream_t st) {
     else if (nv <= 2048) run_norm_bwd<1024, 2>(a, grid, st);
     else run_norm_bwd<1024, 4>(a, grid, st);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !a.dw) return e;
+    if (e != hipSuccess || !a.dw || one) return e;
     hipLaunchKernelGGL(k_norm_dw, dim3((unsigned)ceil_div(a.H, 32)), dim3(256), 0, st, a.part, grid, a.H, a.dw);
     return hipGetLastError();
 }

@@ -129,12 +129,21 @@ __global__ __launch_bounds__(kRowsThreads) void k_balance_rows(BalanceArgs a, Ba
         __syncthreads();
     }
     const Seqs sq{staged ? s_off : a.off, a.S, a.T};
-    const int lo = b * p.chunk, hi = min(a.T, lo + p.chunk);
+    const int lo = b * p.chunk, hi = lo + min(p.chunk, a.T - lo);
+    if constexpr (ONE) {   // what no sequence with rows overwrites below
+        for (int64_t i = tid; i < (int64_t)a.S * a.E; i += NT) {
+            a.counts[i] = 0;
+            if (a.mean_probs) a.mean_probs[i] = 0.f;
+        }
+        __syncthreads();
+    }
     float bal = 0.f, ztot = 0.f;
-    int live = 0, valid = 0;
-    for (int s = ONE ? 0 : sq.find(lo); s < a.S && (ONE || sq.begin(s) < hi); ++s) {
-        const int r0 = max(sq.begin(s), lo), r1 = min(sq.end(s), hi);
-        if (r0 >= r1 && !ONE) continue;
+    int live = 0, valid = 0, s, r1;
+    // from row to row over the sequences that have rows here (empty ones are stepped over by the search)
+    for (int r0 = max(lo, sq.begin(0)); r0 < hi; r0 = r1) {
+        s = sq.find(r0);
+        r1 = min(sq.end(s), hi);
+        if (r1 <= r0) break;   // behind the last sequence
         float acc[N], z = 0.f, v[N];
         if (r0 + g < r1) load_row<L, Q, VEC>(a.logits + (int64_t)(r0 + g) * a.E, a.E, sub, -INFINITY, v);
         for (int e = tid; e < a.E; e += NT) s_hit[e] = 0;
@@ -189,10 +198,10 @@ __global__ __launch_bounds__(kRowsThreads) void k_balance_rows(BalanceArgs a, Ba
 #pragma unroll
             for (int i = 0; i < NG; ++i) t += s_p[i][e];
             if constexpr (ONE) {
-                const float mean = len > 0 ? t / (float)len : 0.f;
-                a.counts[(int64_t)s * a.E + e] = len > 0 ? s_hit[e] : 0;
+                const float mean = t / (float)len;
+                a.counts[(int64_t)s * a.E + e] = s_hit[e];
                 if (a.mean_probs) a.mean_probs[(int64_t)s * a.E + e] = mean;
-                if (len > 0) dot = fmaf(mean, (float)s_hit[e] / (float)len, dot);
+                dot = fmaf(mean, (float)s_hit[e] / (float)len, dot);
             } else {
                 const int64_t slot = (int64_t)(b + s) * p.stride;
                 reinterpret_cast<float*>(a.ws + p.probs)[slot + e] = t;
@@ -208,8 +217,8 @@ __global__ __launch_bounds__(kRowsThreads) void k_balance_rows(BalanceArgs a, Ba
         if constexpr (ONE) {
             bal += block_sum<NT / 64>(dot, s_w);
             ztot += t;
-            live += len > 0;
-            valid += max(len, 0);
+            live += 1;
+            valid += len;
         }
         __syncthreads();
     }
@@ -326,7 +335,7 @@ static bool vec4(const void* p, int E) { return E % 4 == 0 && (uintptr_t)p % 16 
 hipError_t launch_balance_loss(const BalanceArgs& a, hipStream_t st) {
     const BalancePlan p = balance_plan(a.T, a.E, a.S);
     const bool v = vec4(a.logits, a.E);
-    if (p.nblocks == 1) {
+    if (p.one) {
 #define MOE_CALL(L, Q, V) hipLaunchKernelGGL((k_balance_rows<L, Q, V, true>), dim3(1), dim3(kRowsThreads), 0, st, a, p)
         MOE_ROW_DISPATCH(a.E, v, MOE_CALL);
 #undef MOE_CALL
@@ -338,7 +347,7 @@ hipError_t launch_balance_loss(const BalanceArgs& a, hipStream_t st) {
 #undef MOE_CALL
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    int c4 = 1;
+    int c4 = 32;   // (fewer columns would leave more than 32 row groups to add up one by one)
     while (4 * c4 < a.E) c4 *= 2;
     hipLaunchKernelGGL(k_balance_reduce, dim3(a.S), dim3(1024), 0, st, a, p, c4);
     return hipGetLastError();
@@ -500,16 +509,19 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouteBwdArgs a) {
 #pragma unroll
                 for (int i = 0; i < N; ++i) d[i] = fmaf(f * v[i], D[i] - pd, d[i]);
             } else {
+                // Scores relative to the largest chosen one, as the forward weights are (softmax: by its
+                // logit), and exactly 1 there: a row with a single choice then has the gradient 0, not
+                // the rounding of D - D (which a small balance loss would be lost in).
                 float q[N], mx = -INFINITY, z = 0.f, qd = 0.f;
-                if (!sig) {   // shifted by the largest chosen logit, as the forward weights are
 #pragma unroll
-                    for (int i = 0; i < N; ++i) mx = m[i] > 0.f ? fmaxf(mx, l[i]) : mx;
-                    mx = rmax<L>(mx);
-                    if (mx == -INFINITY) mx = 0.f;
-                }
+                for (int i = 0; i < N; ++i) mx = m[i] > 0.f ? fmaxf(mx, sig ? sc[i] : l[i]) : mx;
+                mx = rmax<L>(mx);
+                if (mx == -INFINITY) mx = 0.f;
+                const float rmx = rcp_or_0(mx);
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    q[i] = m[i] > 0.f ? (sig ? sc[i] : exp_fast(l[i] - mx)) : 0.f;
+                    const float s = sig ? (sc[i] == mx && mx > 0.f ? 1.f : sc[i] * rmx) : exp_fast(l[i] - mx);
+                    q[i] = m[i] > 0.f ? s : 0.f;
                     z = fmaf(m[i], q[i], z);
                     qd = fmaf(q[i], D[i], qd);
                 }

@@ -9,15 +9,20 @@ namespace moe {
 
 // One workgroup per CU where a row takes 512 threads or more (16384 x 4096 with dweight: 97 us; 512
 // workgroups 105, 1024 115: their partial rows cost more than they hide), more of the smaller ones.
-int norm_bwd_parts(int T, int H) { return std::min(T, H <= 512 ? 2048 : H <= 2048 ? 512 : 256); }
+int norm_bwd_parts(int T, int H) {
+    return H <= 512 ? (int)std::min<int64_t>(cdiv(T, 4), 512) : std::min(T, H <= 2048 ? 512 : 256);   // (four rows at a time)
+}
 size_t norm_bwd_ws_bytes(int T, int H) { return (size_t)norm_bwd_parts(T, H) * H * 4; }
 
-// Up to 128 rows one workgroup does everything; beyond that 32 rows each (one for every 16 lanes of a
-// workgroup), more from 8192 rows on, where 256 workgroups fill the chip and more parts would only
-// lengthen the second kernel.
+// A workgroup takes 32 rows at once (8 above 256 experts) and the sequences in its rows one after the
+// other.  Up to four rounds in at most four sequences, one workgroup does everything; beyond that one
+// round each, or fewer rows where the sequences are shorter, and more rounds where that would be more than
+// 512 workgroups (256 fill the chip; more parts only lengthen the second kernel).
 BalancePlan balance_plan(int T, int E, int S) {
     BalancePlan p;
-    p.chunk = T <= 128 ? 128 : std::max(32, (int)cdiv(T, 256));
+    const int round = E <= 256 ? 32 : 8;
+    p.one = T <= 4 * round && S <= 4;
+    p.chunk = p.one ? 4 * round : std::max(std::min<int>(round, (int)cdiv(T, S)), (int)cdiv(T, S > 256 || E > 256 ? 512 : 256));
     p.nblocks = (int)cdiv(T, p.chunk);
     p.nslots = p.nblocks + S;
     p.stride = (E + 3) / 4 * 4;
@@ -27,7 +32,7 @@ BalancePlan balance_plan(int T, int E, int S) {
         o += align256(n);
         return r;
     };
-    const size_t rows = p.nblocks > 1 ? p.nslots : 0;
+    const size_t rows = p.one ? 0 : p.nslots;
     p.probs = take(rows * p.stride * 4);
     p.hits = take(rows * p.stride * 4);
     p.z = take(rows * 4);
@@ -193,6 +198,8 @@ int check_linear(const moe_linear_args* a) {
     if ((int64_t)T * K >= ((int64_t)1 << 31) || (int64_t)K * N >= ((int64_t)1 << 31))
         return fail(MOE_ERR_UNSUPPORTED, "%s: T * K (%lld) and K * N (%lld) must be below 2^31 (32-bit offsets)", op,
                     (long long)T * K, (long long)K * N);
+    if ((int64_t)T * N >= ((int64_t)1 << 40))
+        return fail(MOE_ERR_UNSUPPORTED, "%s: T * N (%lld) must be below 2^40", op, (long long)T * N);
     if (!a->xq || !a->xs || !a->w || !a->w_scale || !a->y)
         return fail(MOE_ERR_INVALID, "%s: xq, xs, w, w_scale and y must not be NULL", op);
     if (a->activation < MOE_ACT_NONE || a->activation > MOE_ACT_GELU_TANH)

@@ -12,9 +12,10 @@ size_t norm_bwd_ws_bytes(int T, int H);
 // ---- balance loss: workgroup b takes rows [b * chunk, (b + 1) * chunk); the part of sequence s
 // in it writes its sums to slot b + s (increasing along the rows, so no two parts share one).
 struct BalancePlan {
+    bool one;                                // one workgroup, one launch, no parts
     int chunk, nblocks, nslots, stride;      // stride: floats of a slot's row, E rounded up to 4
     size_t probs, hits, z, seq, done, end;   // byte offsets: float [slots][stride], int [slots][stride],
-                                             // float [slots], float [S][2], int; none with one workgroup
+                                             // float [slots], float [S][2], int
 };
 BalancePlan balance_plan(int T, int E, int S);
 

@@ -144,7 +144,7 @@ def test_add_rmsnorm_special_rows():
     assert torch.isinf(M.moe_add_rmsnorm(big, w[:8].contiguous(), 1e-6, residual=big)["h"]).all()
 
 
-NORM_BWD = [(1, 128), (1, 8), (3, 136), (5, 520), (40, 2816), (33, 4096), (4, 4104), (6, 7168), (2, 8224), (3, 16512),
+NORM_BWD = [(1, 128), (1, 8), (2, 64), (5, 512), (4999, 184), (9000, 16), (3, 136), (5, 520), (40, 2816), (33, 4096), (4, 4104), (6, 7168), (2, 8224), (3, 16512),
             (1, 32768), (513, 256), (1100, 64), (1537, 1024)]
 
 
@@ -160,7 +160,7 @@ def test_add_rmsnorm_backward(T, H, with_dh):
     # weight gradient: a workgroup's rows in turn, then the partial rows (a 32nd of them in a chain, 32
     # chains); each term carries the row factor's < 64 u
     parts = B.lib().moe_add_rmsnorm_backward_workspace_size(T, H) // (4 * H)
-    chain = -(-T // parts) + -(-parts // 32) + 32
+    chain = -(-T // parts) + 4 + -(-parts // 32) + 32
     within(host(out["dweight"]), dw, (chain + 64) * U * dwmag + 1e-38, "dweight")
     again = M.moe_add_rmsnorm_backward(dy, x, w, 1e-5, dh=r if with_dh else None)
     assert torch.equal(again["dx"], out["dx"]) and torch.equal(again["dweight"], out["dweight"])
@@ -171,6 +171,19 @@ def test_add_rmsnorm_backward(T, H, with_dh):
     if with_dh:
         got = M.MoeAddRmsNormBackward(dy, x, w, 1e-5, dh=b, dx=b)()
         assert torch.equal(b, out["dx"]) and torch.equal(got["dweight"], out["dweight"])
+
+
+def test_weight_gradient_at_any_float():
+    """dweight is 4-byte aligned: a slice of a flat gradient buffer, also where one part is the whole sum."""
+    for T, H in ((1, 4096), (3, 64), (9, 64)):
+        x, _, r, _, w, _ = _norm_inputs(T, H, 3)
+        want = M.moe_add_rmsnorm_backward(r, x, w, 1e-5)
+        flat = torch.full((H + 8,), 7.0, device="cuda")
+        call = M.MoeAddRmsNormBackward(r, x, w, 1e-5)
+        call.args.dweight = flat[3:].data_ptr()
+        call()
+        assert torch.equal(flat[3:3 + H], want["dweight"])
+        assert (flat[:3] == 7).all() and (flat[3 + H:] == 7).all()
 
 
 def test_add_rmsnorm_backward_against_differences():
@@ -247,6 +260,15 @@ LINEAR_CASES = [  # T, K, N, scheme, act, bias, residual, out
     (2047, 768, 2304, "fp8", "silu", True, False, "bf16"), (1500, 1024, 4112, "mxfp8", "silu", False, True, "bf16"),
     (2600, 1152, 2560, "fp8", "none", False, False, "f32"), (4100, 256, 2048, "fp8", "gelu_tanh", True, True, "bf16"),
     (40, 32768, 32, "fp8", "none", False, True, "bf16"), (300, 16512, 512, "mxfp8", "none", False, False, "f32"),
+    # one of each variant by its number of workgroups, with one, two and an odd number of K blocks, K blocks
+    # that are no multiple of four, and columns that end inside a tile
+    (33, 384, 4112, "mxfp8", "none", True, True, "bf16"), (16, 128, 8208, "fp8", "silu", False, False, "bf16"),
+    (1, 256, 8192, "mxfp8", "none", False, True, "f32"), (64, 256, 8336, "fp8", "relu", False, True, "bf16"),
+    (257, 128, 1936, "fp8", "none", False, False, "f32"), (200, 256, 3600, "mxfp8", "none", False, True, "bf16"),
+    (300, 32768, 1168, "fp8", "none", False, True, "bf16"), (700, 128, 4112, "fp8", "gelu", True, True, "f32"),
+    (1000, 384, 3984, "mxfp8", "silu", True, True, "bf16"), (1800, 128, 4112, "mxfp8", "none", False, False, "f32"),
+    (1750, 1664, 4240, "fp8", "gelu_tanh", True, True, "bf16"), (2900, 256, 6160, "mxfp8", "none", False, True, "bf16"),
+    (2850, 640, 6160, "fp8", "none", True, False, "f32"), (3000, 128, 6160, "fp8", "relu", True, True, "bf16"),
 ]
 
 
@@ -323,6 +345,10 @@ ROUTER_CASES = [  # T, E, k, scoring, renorm, rsf, offsets
     (50, 1024, 12, "softmax", False, 1.0, None), (40, 1001, 1, "softmax", True, 1.0, [0, 39]),
     (5000, 96, 4, "softmax", True, 1.0, [0, 2500, 2600, 4999]), (20000, 16, 2, "sigmoid", True, 1.0, None),
     (17, 10, 10, "softmax", True, 1.0, [0, 0, 17, 17]), (12, 8, 2, "softmax", False, 1.0, [5, 5]),
+    (33, 100, 20, "softmax", True, 1.5, None), (21, 600, 70, "sigmoid", True, 1.0, [0, 20]),     # more slots than lanes
+    (128, 32, 4, "softmax", False, 1.0, [0, 1, 1, 90, 128]), (129, 32, 4, "sigmoid", True, 1.0, [0, 1, 1, 90, 128]),
+    (90, 16, 2, "softmax", True, 1.0, sorted([0, 90] + [(37 * i) % 91 for i in range(70)])),     # many short sequences
+    (3000, 8, 1, "sigmoid", True, 1.0, sorted([0, 2990] + [(1231 * i) % 2991 for i in range(1500)])),
 ]
 CA, CZ = 0.37, 0.011
 
@@ -413,6 +439,15 @@ def test_router_masked_experts_dropped_and_repeated_ids():
         a[4, 0] = E
         a[5, 2] = int(idn[5, 0])                  # the same expert twice, and in every slot
         a[6, :] = 11
+    # more slots than a row has lanes, with repeats on both sides of that
+    l2, lf2, ids2, idn2, dw2, dwf2 = _router_inputs(9, 40, 33, 9)
+    for a in (idn2, ids2):
+        a[0, 20] = int(idn2[0, 1])
+        a[0, 32] = int(idn2[0, 1])
+        a[1, :] = 7
+        a[2, 16:] = -1
+    for scoring, renorm in (("softmax", False), ("softmax", True), ("sigmoid", True)):
+        _check_router(l2, lf2, ids2, idn2, dw2, dwf2, 33, scoring, renorm, 0.7, None)
     for scoring, renorm in (("softmax", False), ("softmax", True), ("sigmoid", True)):
         _, d = _check_router(l, lf, ids, idn, dw, dwf, k, scoring, renorm, 1.3, [0, 20, 38])
         assert torch.isfinite(d).all() and (d[7] == 0).all()
@@ -446,6 +481,14 @@ def test_route_backward_against_differences():
         # differences: 1e-10 truncation and 1e-11 rounding of values of order 1
         _, mag = OL.route_backward(lf, idn, k, scoring, renorm, 1.7, dwf, counts, CA, CZ, [0, 2, 5])
         within(host(d), num, 1e-8 + (4 * (np.ptp(lf) + 40) + 64) * U * mag + 1e-6 * CZ)
+
+
+def test_single_choice_has_no_weight_gradient():
+    # one expert per token, normalised over the chosen: its weight is constant
+    for scoring in ("softmax", "sigmoid"):
+        l, lf, ids, idn, dw, dwf = _router_inputs(500, 12, 1, 5)
+        assert (M.moe_route_backward(_params(12, 1, scoring, True, 1.9), l, ids, dw, None, None, 0.0, 0.0) == 0).all()
+        _check_router(l, lf, ids, idn, dw, dwf, 1, scoring, True, 1.9, None)
 
 
 def test_balance_counts_are_the_routers():
@@ -572,6 +615,28 @@ def _all_calls(c):
     outs = [lin.y, norm.h, norm.y, norm.yq, norm.ys, loss.losses, loss.counts, loss.mean_probs, comb.out["dweights"],
             comb.out["d_expert_out"], route.dlogits, nb.out["dx"], nb.out["dweight"]]
     return calls, outs, (logits, dw, c)
+
+
+@pytest.mark.parametrize("T,N", [(100, 512), (300, 1024), (700, 4096), (2000, 4096), (3000, 6144)])
+def test_linear_variants_in_a_graph(T, N):
+    """First call under capture (nothing is set up before it), then replays against eager calls."""
+    xq, xs, w, _, _ = _linear_inputs(T, 384, N, "fp8", 6)
+    res, _ = bf16(rng(18, T, N).standard_normal((T, N)))
+    f = M.MoeLinear(xq, xs, w, residual=res)
+    g = M.MoeLinear(xq, xs, w, residual=res)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            f()
+    for _ in range(3):
+        res.mul_(-1.5)
+        f.y.zero_()
+        graph.replay()
+        want = g()
+        torch.cuda.synchronize()
+        assert torch.equal(f.y, want)
 
 
 def test_graph_replays_match_eager_calls():

@@ -58,7 +58,7 @@ NBWD = dict(T=4, H=256, dy=at(0), h=at(1), weight=at(2), eps=1e-6, dh=at(3), dx=
     (dict(T=-1), B.MOE_ERR_INVALID, "T (-1)"), (dict(H=12), B.MOE_ERR_UNSUPPORTED, "multiple of 8"),
     (dict(dx=None), B.MOE_ERR_INVALID, "dx"), (dict(dh=at(3, 8)), B.MOE_ERR_UNSUPPORTED, "aligned"),
     (dict(dweight=at(5, 2)), B.MOE_ERR_INVALID, "dweight"), (dict(workspace=None), B.MOE_ERR_WORKSPACE, "workspace"),
-    (dict(workspace_bytes=4095), B.MOE_ERR_WORKSPACE, "need 4096"), (dict(workspace=at(6, 64)), B.MOE_ERR_INVALID, "256-byte"),
+    (dict(workspace_bytes=1023), B.MOE_ERR_WORKSPACE, "need 1024"), (dict(workspace=at(6, 64)), B.MOE_ERR_INVALID, "256-byte"),
     (dict(dx=at(1)), B.MOE_ERR_INVALID, "dx must not overlap h"), (dict(dx=at(0, 512)), B.MOE_ERR_INVALID, "dx must not overlap dy"),
     (dict(dweight=at(2)), B.MOE_ERR_INVALID, "dweight must not overlap weight"),
     (dict(workspace=at(4)), B.MOE_ERR_INVALID, "dx and workspace"),
@@ -154,7 +154,8 @@ def test_null_args(name):
 
 def test_workspace_sizes():
     L_ = M.lib()
-    assert L_.moe_add_rmsnorm_backward_workspace_size(4, 256) == 4 * 256 * 4
+    assert L_.moe_add_rmsnorm_backward_workspace_size(5, 256) == 2 * 256 * 4   # four rows per workgroup
+    assert L_.moe_add_rmsnorm_backward_workspace_size(5, 1024) == 5 * 1024 * 4
     assert L_.moe_add_rmsnorm_backward_workspace_size(0, 256) == 0
     assert L_.moe_balance_loss_workspace_size(0, 8, 1) == 0
     small, large = (L_.moe_balance_loss_workspace_size(T, 128, 3) for T in (64, 16384))
