@@ -224,20 +224,24 @@ hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t st) {
 template <int G, int VPT, bool ST>
 __global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_rmsnorm_bwd(NormBwdArgs a) {
     constexpr int RPB = G < 256 ? 256 / G : 1;
-    static_assert(RPB == 1 || VPT == 1, "short rows are one vector per thread");
-    __shared__ float s_sum[2][2][G / 64];
-    __shared__ __align__(16) float s_dw[RPB][RPB > 1 ? G * 8 : 4];
-    const int sub = threadIdx.x % G, rw = threadIdx.x / G, nv = a.H >> 3;
+    constexpr bool AHEAD = VPT <= 4;   // else the registers hold no second row and no weights
+    __shared__ double s_sum[2][2][G / 64];
+    __shared__ __align__(16) float s_dw[RPB][RPB > 1 ? VPT * G * 8 : 4];
+    const int sub = RPB > 1 ? threadIdx.x % G : threadIdx.x, rw = RPB > 1 ? threadIdx.x / G : 0, nv = a.H >> 3;
     const int64_t step = (int64_t)gridDim.x * RPB;
-    float dw[VPT][8], w[VPT][8];
+    float dw[VPT][8], wk[AHEAD ? VPT : 1][8];
+    auto weights = [&](int i, float (&w)[8]) __attribute__((always_inline)) {
+        const int v = sub + i * G;
+        const float* p = a.w;
+        if constexpr (!AHEAD) asm volatile("" : "+s"(p));   // read again each time, not kept
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = v < nv ? p[v * 8 + j] : 0.f;
+    };
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int v = sub + i * G;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            dw[i][j] = 0.f;
-            w[i][j] = v < nv ? a.w[v * 8 + j] : 0.f;
-        }
+        for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
+        if constexpr (AHEAD) weights(i, wk[i]);
     }
     struct Row {
         uint4 h[VPT], d[VPT], r[VPT];
@@ -245,37 +249,40 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_rmsnorm_bwd(NormBwdAr
     auto load = [&](int64_t t, Row& x) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int v = sub + i * G;
-            const int64_t o = t * a.H + v * 8;
+            const uint32_t v = sub + i * G;
+            const int64_t o = t * a.H;
             x.h[i] = x.d[i] = x.r[i] = make_uint4(0, 0, 0, 0);
-            if (v < nv) {
-                x.h[i] = ld16<ST>(a.h + o);
-                x.d[i] = ld16<ST>(a.dy + o);
-                if (a.dh) x.r[i] = ld16<ST>(a.dh + o);
+            if (v < (uint32_t)nv) {   // (a row's base, the same for all of its threads, and 32-bit offsets)
+                x.h[i] = ld16<ST>(a.h + o + v * 8);
+                x.d[i] = ld16<ST>(a.dy + o + v * 8);
+                if (a.dh) x.r[i] = ld16<ST>(a.dh + o + v * 8);
             }
         }
     };
     int par = 0;
     Row nx;
     const int64_t first = (int64_t)blockIdx.x * RPB + rw;
-    if (first < a.T) load(first, nx);
+    if (AHEAD && first < a.T) load(first, nx);
     for (int64_t t = first; t < a.T; t += step, par ^= 1) {
+        if (!AHEAD) load(t, nx);
         uint4 vh[VPT], vd[VPT], vr[VPT];
 #pragma unroll
         for (int i = 0; i < VPT; ++i) vh[i] = nx.h[i], vd[i] = nx.d[i], vr[i] = nx.r[i];
-        if (t + step < a.T) load(t + step, nx);   // in flight over this row's sums
+        if (AHEAD && t + step < a.T) load(t + step, nx);   // in flight over this row's sums
         // sum h^2 and sum g h in one exchange: mean(g xhat) = r sum(g h) / H
-        float ss = 0.f, gh = 0.f;
+        double ss = 0.0, gh = 0.0;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            float h[8], d[8];
+            float h[8], d[8], wt[8];
             unpack8(vh[i], h);
             unpack8(vd[i], d);
+            if constexpr (!AHEAD) weights(i, wt);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                ss = fmaf(h[j], h[j], ss);
-                gh = fmaf(d[j] * w[i][j], h[j], gh);
+                ss = fma((double)h[j], (double)h[j], ss);
+                gh = fma((double)(d[j] * (AHEAD ? wk[AHEAD ? i : 0][j] : wt[j])), (double)h[j], gh);
             }
+            if constexpr (VPT > 2) __builtin_amdgcn_sched_barrier(0);   // one vector's values at a time
         }
         ss = wave_sum(ss);
         gh = wave_sum(gh);
@@ -285,42 +292,53 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_rmsnorm_bwd(NormBwdAr
                 s_sum[par][1][sub >> 6] = gh;
             }
             __syncthreads();
-            ss = gh = 0.f;
+            ss = gh = 0.0;
 #pragma unroll
             for (int i = 0; i < G / 64; ++i) {
                 ss += s_sum[par][0][i];
                 gh += s_sum[par][1][i];
             }
         }
-        const float r = 1.0f / sqrtf(ss / (float)a.H + a.eps);
-        const float c = gh / (float)a.H * r * r;     // xhat mean(g xhat) = h c
+        const double rd = rsqrt_f64(fma(ss, a.inv_h, (double)a.eps));
+        const float r = (float)rd, m = (float)(gh * a.inv_h * rd);   // m = mean(g xhat)
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = sub + i * G;
-            float h[8], d[8], e[8];
+            float h[8], d[8], e[8], wt[8];
+            if constexpr (VPT > 2) {   // unpacked again: kept, the values of the first pass would fill the registers
+                asm volatile("" : "+v"(vh[i].x), "+v"(vh[i].y), "+v"(vh[i].z), "+v"(vh[i].w));
+                asm volatile("" : "+v"(vd[i].x), "+v"(vd[i].y), "+v"(vd[i].z), "+v"(vd[i].w));
+            }
             unpack8(vh[i], h);
             unpack8(vd[i], d);
             unpack8(vr[i], e);
+            if constexpr (!AHEAD) weights(i, wt);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                dw[i][j] = fmaf(d[j], h[j] * r, dw[i][j]);
-                const float g = r * (d[j] * w[i][j] - h[j] * c);
+                const float x = (float)((double)h[j] * rd);
+                dw[i][j] = fmaf(d[j], x, dw[i][j]);
+                const float g = r * (d[j] * (AHEAD ? wk[AHEAD ? i : 0][j] : wt[j]) - x * m);
                 e[j] = a.dh ? g + e[j] : g;
             }
             if (v < nv) st16<ST>(a.dx + t * a.H + v * 8, pack8(e));
+            if constexpr (VPT > 2) __builtin_amdgcn_sched_barrier(0);
         }
     }
     if (a.dw) {
         if constexpr (RPB > 1) {   // the waves' sums, in order
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s_dw[rw][sub * 8 + j] = dw[0][j];
+            for (int i = 0; i < VPT; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s_dw[rw][(sub + i * G) * 8 + j] = dw[i][j];
             __syncthreads();
             if (rw) return;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int i = 0; i < VPT; ++i)
 #pragma unroll
-                for (int w = 1; w < RPB; ++w) dw[0][j] += s_dw[w][sub * 8 + j];
-            }
+                for (int j = 0; j < 8; ++j) {
+#pragma unroll
+                    for (int w = 1; w < RPB; ++w) dw[i][j] += s_dw[w][(sub + i * G) * 8 + j];
+                }
         }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
@@ -370,11 +388,12 @@ hipError_t launch_add_rmsnorm_backward(const NormBwdArgs& args, hipStream_t st) 
     const bool one = grid == 1 && !(reinterpret_cast<uintptr_t>(a.dw) & 15);   // the only part is the sum
     if (one) a.part = a.dw;
     if (nv <= 64) run_norm_bwd<64, 1>(a, grid, st);
+    else if (nv <= 128) run_norm_bwd<64, 2>(a, grid, st);
     else if (nv <= 256) run_norm_bwd<256, 1>(a, grid, st);
     else if (nv <= 512) run_norm_bwd<512, 1>(a, grid, st);
     else if (nv <= 1024) run_norm_bwd<512, 2>(a, grid, st);
-    else if (nv <= 2048) run_norm_bwd<1024, 2>(a, grid, st);
-    else run_norm_bwd<1024, 4>(a, grid, st);
+    else if (nv <= 2048) run_norm_bwd<512, 4>(a, grid, st);
+    else run_norm_bwd<512, 8>(a, grid, st);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.dw || one) return e;
     hipLaunchKernelGGL(k_norm_dw, dim3((unsigned)ceil_div(a.H, 32)), dim3(256), 0, st, a.part, grid, a.H, a.dw);

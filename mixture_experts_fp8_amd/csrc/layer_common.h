@@ -63,7 +63,8 @@ struct NormBwdArgs {
     const uint16_t* dh;   // or NULL
     uint16_t* dx;
     float* dw;            // or NULL
-    float* part;          // workspace: [norm_bwd_parts(T)][H], used with dw
+    float* part;          // workspace: [norm_bwd_parts(T, H)][H], used with dw
+    double inv_h;         // 1 / H
 };
 hipError_t launch_add_rmsnorm_backward(const NormBwdArgs& a, hipStream_t st);
 

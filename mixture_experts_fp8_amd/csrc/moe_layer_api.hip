@@ -30,7 +30,7 @@ size_t moe_add_rmsnorm_backward_workspace_size(int32_t T, int32_t H) {
 int moe_add_rmsnorm_backward(const moe_add_rmsnorm_backward_args* a) {
     if (int rc = moe::host::check_add_rmsnorm_backward(a)) return rc;
     const moe::NormBwdArgs n{a->T, a->H, a->dy, a->h, a->weight, a->eps, a->dh, a->dx, a->dweight,
-                             static_cast<float*>(a->workspace)};
+                             static_cast<float*>(a->workspace), 1.0 / a->H};
     return done("moe_add_rmsnorm_backward", moe::launch_add_rmsnorm_backward(n, static_cast<hipStream_t>(a->stream)));
 }
 

@@ -10,7 +10,7 @@ namespace moe {
 // One workgroup per CU where a row takes 512 threads or more (16384 x 4096 with dweight: 97 us; 512
 // workgroups 105, 1024 115: their partial rows cost more than they hide), more of the smaller ones.
 int norm_bwd_parts(int T, int H) {
-    return H <= 512 ? (int)std::min<int64_t>(cdiv(T, 4), 512) : std::min(T, H <= 2048 ? 512 : 256);   // (four rows at a time)
+    return H <= 1024 ? (int)std::min<int64_t>(cdiv(T, 4), 512) : std::min(T, H <= 2048 ? 512 : 256);   // (four rows at a time)
 }
 size_t norm_bwd_ws_bytes(int T, int H) { return (size_t)norm_bwd_parts(T, H) * H * 4; }
 
@@ -225,8 +225,16 @@ int check_linear(const moe_linear_args* a) {
                         {"w_scale", a->w_scale, mx ? (uint64_t)K * N / 32 : (uint64_t)(K / 128) * cdiv(N, 128)},
                         {"bias", a->bias, (uint64_t)N * 4},
                         {"residual", a->residual, a->residual ? span2(T, N, a->ld_residual, size) : 0}};
-    for (int i = 0; i < 6; ++i)
-        if (int rc = check_io(op, y, in[i], i == 5 && a->ld_residual == a->ld_y)) return rc;
+    for (int i = 0; i < 5; ++i)
+        if (int rc = check_io(op, y, in[i])) return rc;
+    // y and residual may be columns side by side in the rows of one matrix: their spans meet, they do not
+    if (a->residual && a->ld_residual == a->ld_y) {
+        const uint64_t row = (uint64_t)a->ld_y * size, used = (uint64_t)N * size;
+        const uint64_t d = ((uintptr_t)a->y > (uintptr_t)a->residual ? (uintptr_t)a->y - (uintptr_t)a->residual
+                                                                     : (uintptr_t)a->residual - (uintptr_t)a->y) % row;
+        if (a->y != a->residual && d >= used && row - d >= used) return MOE_OK;
+    }
+    if (int rc = check_io(op, y, in[5], a->ld_residual == a->ld_y)) return rc;
     return MOE_OK;
 }
 

@@ -100,7 +100,7 @@ def _rows(t: torch.Tensor, name: str, dtype, shape) -> int:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if shape[1] > 1 and t.stride(1) != 1:
         raise ValueError(f"{name}: its last dimension must be contiguous")
-    return t.stride(0) if shape[0] > 1 else max(t.stride(0), shape[1])
+    return t.stride(0) if shape[0] > 1 else shape[1]
 
 
 def _quant_group(quant: int) -> int:
@@ -217,11 +217,14 @@ class LinearWeights:
     def from_float(w: torch.Tensor, quant: int = B.MOE_QUANT_FP8_BLOCK128,
                    bias: Optional[torch.Tensor] = None) -> "LinearWeights":
         """float32 [K, N] -> quantised and packed."""
+        N = w.shape[1]
         if quant == B.MOE_QUANT_MXFP8:
             q, s = B.moe_quant_weight_mx(w[None], B.MOE_WFMT_E4M3)
         else:
+            if N % 128:   # a block that ends behind column N is quantised as if zeros followed
+                w = torch.cat([w, w.new_zeros(w.shape[0], -N % 128)], 1)
             q, s = B.moe_quant_weight_blocks(w[None])
-        return LinearWeights.from_logical(q[0], s[0], quant, bias)
+        return LinearWeights.from_logical(q[0][:, :N].contiguous(), s[0], quant, bias)
 
 
 class MoeLinear(_Call):
@@ -239,7 +242,18 @@ class MoeLinear(_Call):
         _need(xs, "xs", torch.uint8, (T, K // _quant_group(w.quant)))
         if activation not in ACTIVATIONS:
             raise ValueError(f"activation: expected one of {sorted(ACTIVATIONS)}, got {activation!r}")
-        dt = {torch.float32: B.MOE_DTYPE_F32, torch.bfloat16: B.MOE_DTYPE_BF16}[out_dtype]
+        if out_dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"out_dtype: expected float32 or bfloat16, got {out_dtype}")
+        dt = B.MOE_DTYPE_F32 if out_dtype == torch.float32 else B.MOE_DTYPE_BF16
+        # (the packed sizes; shapes that the packing refuses are refused by the call)
+        sizes = {"w": K * N, "w_scale": K * N // 32 if w.quant == B.MOE_QUANT_MXFP8 else K // 128 * -(-N // 128)}
+        for name, n in sizes.items():
+            t = getattr(w, name)
+            _need(t, name, torch.uint8)
+            if t.numel() != n:
+                raise ValueError(f"{name}: expected {n} elements, got {t.numel()}")
+        if w.bias is not None:
+            _need(w.bias, "bias", torch.float32, (N,))
         ldr = _rows(residual, "residual", out_dtype, (T, N)) if residual is not None else N
         if y is None:   # (rows 8 elements apart: N is a multiple of 16)
             y = torch.empty(T, N, dtype=out_dtype, device=xq.device)
@@ -288,6 +302,7 @@ class MoeBalanceLoss(_Call):
 
     def __init__(self, params: RouteParams, router_logits: torch.Tensor, topk_ids: torch.Tensor,
                  seq_offsets: Optional[torch.Tensor] = None, balance_coef: float = 1e-2, z_coef: float = 0.0):
+        params = RouteParams.from_buffer_copy(params)   # as they were when the buffers were checked against them
         S = _router_inputs(params, router_logits, topk_ids, seq_offsets)
         T, E, dev = router_logits.shape[0], params.num_experts, router_logits.device
         self.losses = torch.empty(3, dtype=torch.float32, device=dev)
@@ -322,6 +337,7 @@ class MoeRouteBackward(_Call):
                  dweights: Optional[torch.Tensor] = None, counts: Optional[torch.Tensor] = None,
                  seq_offsets: Optional[torch.Tensor] = None, balance_coef: float = 1e-2, z_coef: float = 0.0,
                  dlogits: Optional[torch.Tensor] = None):
+        params = RouteParams.from_buffer_copy(params)   # as they were when the buffers were checked against them
         S = _router_inputs(params, router_logits, topk_ids, seq_offsets)
         T, E = router_logits.shape
         if dweights is not None:

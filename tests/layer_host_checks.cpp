@@ -79,6 +79,22 @@ int main() {
         a.out_dtype = MOE_DTYPE_F32;
         a.workspace = at<void>(64), a.workspace_bytes = (size_t)1 << 40;
         CHECK(host::check_linear(&a) == MOE_OK);
+        // columns of one matrix: side by side, then one element group too close on either side
+        a.T = 100, a.K = 128, a.N = 64, a.ld_y = a.ld_residual = 160, a.out_dtype = MOE_DTYPE_BF16;
+        char* m = static_cast<char*>(a.y);
+        a.residual = m + 64 * 2;
+        CHECK(host::check_linear(&a) == MOE_OK);
+        a.residual = m + 96 * 2;
+        CHECK(host::check_linear(&a) == MOE_OK);
+        a.residual = m - 64 * 2;
+        CHECK(host::check_linear(&a) == MOE_OK);
+        for (int c : {56, 104, -56, 8, 160}) {
+            a.residual = m + c * 2;
+            CHECK(host::check_linear(&a) == MOE_ERR_INVALID);
+        }
+        a.residual = m;
+        CHECK(host::check_linear(&a) == MOE_OK);
+        a.residual = nullptr, a.K = 32768, a.N = 65520, a.ld_y = 65520, a.out_dtype = MOE_DTYPE_F32;
         a.T = 65536;
         CHECK(host::check_linear(&a) == MOE_ERR_UNSUPPORTED);
         a.T = a.N = a.ld_y = 1 << 20, a.K = 128;

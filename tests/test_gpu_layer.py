@@ -5,6 +5,8 @@ n terms whose longest chain of additions has c of them is off by at most (c + 2)
 of the terms' magnitudes; each test names its chains.  Matrix-core sums follow the repository's
 accumulation model (oracle.moe.ACC_ERR times the Euclidean norm of the products).
 """
+import dataclasses
+
 import numpy as np
 import pytest
 import torch
@@ -145,7 +147,7 @@ def test_add_rmsnorm_special_rows():
 
 
 NORM_BWD = [(1, 128), (1, 8), (2, 64), (5, 512), (4999, 184), (9000, 16), (3, 136), (5, 520), (40, 2816), (33, 4096), (4, 4104), (6, 7168), (2, 8224), (3, 16512),
-            (1, 32768), (513, 256), (1100, 64), (1537, 1024)]
+            (1, 32768), (513, 256), (1100, 64), (1537, 1024), (7, 600), (2100, 968), (300, 16400), (290, 10000)]
 
 
 @pytest.mark.parametrize("T,H", NORM_BWD)
@@ -171,6 +173,33 @@ def test_add_rmsnorm_backward(T, H, with_dh):
     if with_dh:
         got = M.MoeAddRmsNormBackward(dy, x, w, 1e-5, dh=b, dx=b)()
         assert torch.equal(b, out["dx"]) and torch.equal(got["dweight"], out["dweight"])
+
+
+@pytest.mark.parametrize("H", [64, 1024, 2048, 9000, 20000])
+def test_add_rmsnorm_backward_over_the_range(H):
+    """Rows whose squares leave float32 on either side (eps 0), and rows that are infinite, NaN or zero."""
+    g = rng(11, H)
+    h = g.standard_normal((9, H)) * np.array([1e-36, 1e-30, 1e-20, 1, 1e20, 1e30, 1e37, 1, 1])[:, None]
+    dy = g.standard_normal((9, H)) * np.array([1e-30, 1e-20, 1, 1, 1e15, 1e25, 1e30, 1, 1])[:, None]
+    h, hf = bf16(h)
+    dy, dyf = bf16(dy)
+    w, wf = f32(1 + 0.1 * g.standard_normal(H))
+    out = M.moe_add_rmsnorm_backward(dy, h, w, 0.0)
+    dx, _, mag, _ = OL.rmsnorm_backward(dyf, hf, wf, 0.0)
+    within(host(out["dx"]), dx, UB * np.abs(dx) + 64 * U * (1 + UB) * mag + TINY, "dx")
+    for row in range(9):     # the weight gradient, row by row: exact sums of one term
+        one = M.moe_add_rmsnorm_backward(dy[row:row + 1], h[row:row + 1], w, 0.0)
+        assert torch.equal(one["dx"], out["dx"][row:row + 1])
+        _, dw, _, dwmag = OL.rmsnorm_backward(dyf[row:row + 1], hf[row:row + 1], wf, 0.0)
+        within(host(one["dweight"]), dw, 66 * U * dwmag + 1e-38, "dweight")
+    hh = h.clone()
+    hh[0, 3], hh[1, 5], hh[2] = float("inf"), float("nan"), 0
+    got = M.moe_add_rmsnorm_backward(dy, hh, w, 1e-6, dh=dy)["dx"]
+    assert torch.isnan(got[0]).all() and torch.isnan(got[1]).all()
+    # a zero row: r = 1000, no xhat
+    ref = 1000.0 * dyf[2] * wf + dyf[2]
+    within(host(got[2]), ref, UB * np.abs(ref) + 64 * U * (1000 * np.abs(dyf[2] * wf) + np.abs(dyf[2])))
+    assert torch.equal(got[3:], M.moe_add_rmsnorm_backward(dy[3:], h[3:], w, 1e-6, dh=dy[3:])["dx"])
 
 
 def test_weight_gradient_at_any_float():
@@ -322,6 +351,35 @@ def test_linear_rows_do_not_depend_on_the_batch(scheme):
     y = M.moe_linear(xq, xs, w)
     perm = torch.randperm(700, generator=torch.Generator().manual_seed(3)).to(DEV)
     assert torch.equal(M.moe_linear(xq[perm].contiguous(), xs[perm].contiguous(), w), y[perm])
+
+
+def test_linear_columns_side_by_side():
+    """y and residual as column slices of one matrix, and a single row of a wider one in place."""
+    w = M.LinearWeights.from_float(f32(rng(3).standard_normal((256, 64)))[0])
+    x, _ = bf16(rng(4).standard_normal((20, 256)))
+    xq, xs = M.moe_quant_act(x)
+    wide = M.LinearWeights.from_float(torch.cat([f32(rng(3).standard_normal((256, 64)))[0], torch.zeros(256, 64, device=DEV)], 1))
+    assert w.N == 64 and torch.equal(M.moe_linear(xq, xs, w), M.moe_linear(xq, xs, wide)[:, :64])
+    both = torch.zeros(20, 128, dtype=torch.bfloat16, device=DEV)
+    both[:, 64:] = bf16(rng(5).standard_normal((20, 64)))[0]
+    want = M.moe_linear(xq, xs, w, residual=both[:, 64:].contiguous())
+    keep = both[:, 64:].clone()
+    got = M.moe_linear(xq, xs, w, residual=both[:, 64:], y=both[:, :64])
+    assert torch.equal(got, want) and torch.equal(both[:, 64:], keep)
+    with pytest.raises(M.MoeError):
+        M.moe_linear(xq, xs, w, residual=both[:, 32:96], y=both[:, :64])
+    one = both[3:4, 64:]
+    M.moe_linear(xq[3:4], xs[3:4], w, residual=one, y=one)
+    assert torch.equal(one, want[3:4]) and torch.equal(both[4:, 64:], keep[4:]) and torch.equal(both[3:4, :64], want[3:4])
+
+
+def test_router_parameters_are_copied():
+    p = M.route_params(8, 2)
+    l, ids = torch.randn(4, 8, device=DEV), torch.zeros(4, 2, dtype=torch.int32, device=DEV)
+    call, back = M.MoeBalanceLoss(p, l, ids), M.MoeRouteBackward(p, l, ids, torch.ones(4, 2, device=DEV))
+    a, b = call()["losses"].clone(), back().clone()
+    p.top_k, p.num_experts = 8, 1024
+    assert torch.equal(call()["losses"], a) and torch.equal(back(), b)
 
 
 def test_linear_zero_rows_and_nan():
@@ -785,6 +843,14 @@ def test_binding_refuses():
         M.moe_add_rmsnorm(x, w, want_y=False)                  # nothing to compute
     xq, xs = M.moe_quant_act(x)
     lw = M.LinearWeights.from_float(torch.zeros(256, 128, device=DEV))
+    for bad in (dict(K=128), dict(N=256), dict(w_scale=lw.w_scale[:1]), dict(bias=torch.zeros(64, device=DEV))):
+        with pytest.raises(ValueError):
+            M.moe_linear(xq if "K" not in bad else xq[:, :128].contiguous(), xs if "K" not in bad else xs[:, :1].contiguous(),
+                         dataclasses.replace(lw, **bad))
+    with pytest.raises(TypeError):
+        M.moe_linear(xq, xs, dataclasses.replace(lw, w=lw.w.cpu()))
+    with pytest.raises(TypeError):
+        M.moe_linear(xq, xs, lw, out_dtype=torch.float16)
     with pytest.raises(ValueError):
         M.moe_linear(xq, xs, lw, "swish")
     with pytest.raises(ValueError):

@@ -155,7 +155,7 @@ def test_null_args(name):
 def test_workspace_sizes():
     L_ = M.lib()
     assert L_.moe_add_rmsnorm_backward_workspace_size(5, 256) == 2 * 256 * 4   # four rows per workgroup
-    assert L_.moe_add_rmsnorm_backward_workspace_size(5, 1024) == 5 * 1024 * 4
+    assert L_.moe_add_rmsnorm_backward_workspace_size(5, 2048) == 5 * 2048 * 4
     assert L_.moe_add_rmsnorm_backward_workspace_size(0, 256) == 0
     assert L_.moe_balance_loss_workspace_size(0, 8, 1) == 0
     small, large = (L_.moe_balance_loss_workspace_size(T, 128, 3) for T in (64, 16384))
