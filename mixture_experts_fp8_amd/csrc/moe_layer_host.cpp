@@ -7,10 +7,13 @@
 
 namespace moe {
 
-// One workgroup per CU where a row takes 512 threads or more (16384 x 4096 with dweight: 97 us; 512
-// workgroups 105, 1024 115: their partial rows cost more than they hide), more of the smaller ones.
+// One workgroup per CU (16384 x 4096 with dweight 91 us, 512 workgroups 99: their partial rows cost more
+// than they hide; 4096 x 1024, four rows at a time, 12.7 and 15.5), two where a thread has one vector of a
+// row and each workgroup many rows (16384 x 2048: 66 us with one, 52 with two; 1000 x 2048: 10.9 and 12.9;
+// 65536 x 512: 64 and 52).
 int norm_bwd_parts(int T, int H) {
-    return H <= 1024 ? (int)std::min<int64_t>(cdiv(T, 4), 512) : std::min(T, H <= 2048 ? 512 : 256);   // (four rows at a time)
+    if (H <= 1024) return (int)std::min<int64_t>(cdiv(T, 4), H <= 512 && T >= 32768 ? 512 : 256);
+    return std::min(T, H <= 2048 && T >= 4096 ? 512 : 256);
 }
 size_t norm_bwd_ws_bytes(int T, int H) { return (size_t)norm_bwd_parts(T, H) * H * 4; }
 
