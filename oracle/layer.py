@@ -168,8 +168,13 @@ def route_backward(logits, ids, k, scoring, renorm, rsf, dweights=None, counts=N
                 d[a:b] += rsf * raw * (D - (raw * D).sum(axis=1, keepdims=True))
                 mag[a:b] += abs(rsf) * raw * (D_abs + (raw * D_abs).sum(axis=1, keepdims=True))
             else:
-                tot = (m * raw).sum(axis=1, keepdims=True)
-                q = np.divide(np.where(m > 0, raw, 0.0), tot, out=np.zeros_like(raw), where=tot != 0)
+                got = np.where(m > 0, raw, 0.0)
+                if scoring == "softmax":   # a softmax over the chosen: theirs may all be 0 beside a far larger logit
+                    sel = np.where(m > 0, np.asarray(logits[a:b], dtype=np.float64), -np.inf)
+                    top = sel.max(axis=1, keepdims=True)
+                    got = np.exp(sel - np.where(np.isneginf(top), 0.0, top))
+                tot = (m * got).sum(axis=1, keepdims=True)
+                q = np.divide(got, tot, out=np.zeros_like(got), where=tot != 0)
                 d[a:b] += rsf * q * om * (D - m * (q * D).sum(axis=1, keepdims=True))
                 mag[a:b] += abs(rsf) * q * om * (D_abs + m * (q * D_abs).sum(axis=1, keepdims=True))
     return d, mag

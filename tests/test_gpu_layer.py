@@ -517,6 +517,30 @@ def test_router_masked_experts_dropped_and_repeated_ids():
     assert bad == [11, 12]
 
 
+def test_router_logits_at_the_ends_of_float32():
+    """Masks of the type's lowest value, and logits whose exponentials or sigmoids leave float32."""
+    T, E, k = 24, 16, 3
+    l, lf, ids, idn, dw, dwf = _router_inputs(T, E, k, 12)
+    low = float(np.finfo(np.float32).min)
+    for a in (l, lf):
+        a[:, 12:] = low
+        a[3] = low                                # a row whose mask leaves nothing
+        a[5, 2] = -low                            # one expert takes it all
+        a[6] = 200.0
+        a[7, :6] = -60.0
+    for scoring, renorm in (("softmax", False), ("softmax", True), ("sigmoid", True)):
+        p = _params(E, k, scoring, renorm, 1.0)
+        out = M.moe_balance_loss(p, l, ids, None, CA, 0.0)
+        losses, counts, mean = OL.balance_loss(lf, idn, k, scoring, CA, 0.0)
+        # exponents up to 400 where they are not 0 or 1: < 400 u, then as in _check_router
+        within(host(out["mean_probs"]), mean, 800 * U * mean + 1e-37, "mean_probs")
+        within(host(out["losses"]), losses, 900 * U * np.abs(losses) + 1e-37, "losses")
+        d = M.moe_route_backward(p, l, ids, dw, out["counts"], None, CA, 0.0)
+        ref, mag = OL.route_backward(lf, idn, k, scoring, renorm, 1.0, dwf, counts, CA, 0.0)
+        within(host(d), ref, 4000 * U * mag + 1e-37, "dlogits")
+        assert torch.isfinite(d).all() and (scoring != "sigmoid" or (d[3] == 0).all())
+
+
 def test_route_backward_against_differences():
     T, E, k = 5, 12, 3
     l, lf, ids, idn, dw, dwf = _router_inputs(T, E, k, 3)
