@@ -612,8 +612,7 @@ static hipError_t run_tile(const LinArgs& a, hipStream_t st) {
 // both operands go through LDS, so that the copies are this kernel's only outstanding loads and their
 // number can be waited for.  S stages hold S - 2 K blocks on their way while block kb's products run
 // and block kb + 1's operands are read.  512 x 4096 x 4096: 15.6 us, one tile per CU, bound by the chain copy,
-// LDS read, product of its 32 K blocks.  (A second set of waves, each taking every other K block, is slower: 512 x 4096 x 4096
-// 17.6 us instead of 15.6.)
+// LDS read, product of its 32 K blocks.  (With a second set of waves for every other K block: 17.6 us.)
 template <int N>
 __device__ __forceinline__ void wait_vm() {
     asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
