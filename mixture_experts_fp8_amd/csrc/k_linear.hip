@@ -768,12 +768,16 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_linear_deep(LinArgs a, int 
     tile_finish<MI>(a, acc, bias, res, row0, col0);
 }
 
+// LDS of a deep tile: stages, bias, the 128-element scales of all K blocks.
+static size_t deep_lds(bool mx, int rows, int cols, int stages, int KB) {
+    return (size_t)stages * (rows + cols) * (kGroup + (mx ? 4 : 0)) + cols * 4 +
+           (mx ? 0 : (size_t)KB * rows + (KB * ((cols + 127) / 128) + 15) / 16 * 16);
+}
 template <bool MX, int MI, int NJ, int WM, int WN, int S>
 static hipError_t run_deep_t(const LinArgs& a, hipStream_t st) {
     constexpr int ROWS = 16 * MI * WM, COLS = 16 * NJ * WN;
-    const int tm = (int)ceil_div(a.T, ROWS), tn = (int)ceil_div(a.N, COLS), KB = a.K / kGroup;
-    const size_t lds = S * (ROWS + COLS) * (kGroup + (MX ? 4 : 0)) + COLS * 4 +
-                       (MX ? 0 : (size_t)KB * ROWS + (KB * ((COLS + 127) / 128) + 15) / 16 * 16);
+    const int tm = (int)ceil_div(a.T, ROWS), tn = (int)ceil_div(a.N, COLS);
+    const size_t lds = deep_lds(MX, ROWS, COLS, S, a.K / kGroup);
     return launch_tiles<k_linear_deep<MX, MI, NJ, WM, WN, S>>(a, tm, tn, 64 * WM * WN, lds, st);
 }
 template <int MI, int NJ, int WM, int WN, int S>
@@ -798,8 +802,12 @@ static hipError_t run_stream(const LinArgs& a, hipStream_t st) {
 //     each has one to itself (512 x 4096 x 4096: 15.8 us; k_linear_tile on the same tiles 22.2;
 //     192 x 7168 x 7168: 22.8, 64 x 64 stream tiles 47) and three, which fit twice, else
 //     (1024 x 4096 x 4096: 24.1, four stages 29.7).
-//   * k_linear_tile beyond: 64 x 256 tiles up to 512 workgroups (2047 x 4096 x 4096: 39.2; 64 x 128 deep
-//     45.6), then 128 x 256 (4096 x 4096 x 4096: 65; 64 x 256 78).
+//   * Then 128 x 256 tiles.  While each has a CU to itself, deep copies with eight waves (2048 x 4096 x 4096:
+//     36.7 us, MXFP8 43.9; k_linear_tile on 64 x 256 tiles 37.9 and 50.7, deep 64 x 128 tiles 44.6 and 48.9),
+//     but with 128-element scales 64 x 256 k_linear_tile if they leave more than a few CUs idle (1300 x 2048 x
+//     4096, 176 tiles: 18.7 and 19.2; MXFP8 23.1 and 22.5), or from K = 15232 on, where the scales of all K
+//     blocks do not fit beside the stages.
+//   * k_linear_tile beyond, two workgroups per CU (4096 x 4096 x 4096: 63 us; deep 78, 64 x 256 tiles 77).
 hipError_t launch_linear(const LinArgs& args, hipStream_t st) {
     LinArgs a = args;
     // Outputs larger than the L2s together leave past them: they would evict the operands that the
@@ -812,7 +820,11 @@ hipError_t launch_linear(const LinArgs& args, hipStream_t st) {
     if (fits(64, 32, 256) || a.T <= 64) return run_stream<4, 2, 4, 3>(a, st);
     if (fits(64, 128, 256)) return run_deep<2, 4, 2, 2, 4>(a, st);
     if (fits(64, 128, 512)) return run_deep<2, 4, 2, 2, 3>(a, st);
-    if (fits(64, 256, 512)) return run_tile<4, 4, 1, 4>(a, st);
+    if (fits(128, 256, 256)) {
+        if ((a.mx || !fits(128, 256, 208)) && deep_lds(a.mx, 128, 256, 3, a.K / kGroup) <= kLdsBytes)
+            return run_deep<4, 4, 2, 4, 3>(a, st);
+        return run_tile<4, 4, 1, 4>(a, st);
+    }
     return run_tile<8, 4, 1, 4>(a, st);
 }
 

@@ -298,6 +298,9 @@ LINEAR_CASES = [  # T, K, N, scheme, act, bias, residual, out
     (1000, 384, 3984, "mxfp8", "silu", True, True, "bf16"), (1800, 128, 4112, "mxfp8", "none", False, False, "f32"),
     (1750, 1664, 4240, "fp8", "gelu_tanh", True, True, "bf16"), (2900, 256, 6160, "mxfp8", "none", False, True, "bf16"),
     (2850, 640, 6160, "fp8", "none", True, False, "f32"), (3000, 128, 6160, "fp8", "relu", True, True, "bf16"),
+    (1100, 512, 4112, "mxfp8", "gelu", True, True, "bf16"), (1900, 384, 2832, "fp8", "none", True, True, "f32"),
+    (1900, 640, 3856, "fp8", "silu", True, False, "bf16"),
+    (900, 15104, 7184, "fp8", "none", False, True, "bf16"), (900, 15232, 7184, "fp8", "none", True, False, "bf16"),
 ]
 
 
