@@ -93,77 +93,63 @@ __device__ __forceinline__ void put4(const LinArgs& a, int64_t row, int col, v4f
 }
 
 // Operands straight from memory into registers, no LDS in the K loop: workgroup (column tile of
-// 16 NF, row tile of 16 MF), whose WK waves take the K blocks in turn and add their sums through
+// 16 NF, row tile of 16), whose WK waves take the K blocks in turn and add their sums through
 // LDS in wave order.  PF K blocks are in flight per wave.  Bound by the weight stream: 1 x 7168 x 7168 takes
 // 10.0 us, 5.1 TB/s; a small product (32 x 2816 x 2816 with gelu, 6.0 us) by one wave's chain of loads.
-template <bool MX, int MF, int NF, int WK, int PF>
+template <bool MX, int NF, int WK, int PF>
 __global__ __launch_bounds__(64 * WK) void k_linear_stream(LinArgs a) {
-    __shared__ __align__(16) v4f s_acc[WK][MF * NF][64];
+    __shared__ __align__(16) v4f s_acc[WK][NF][64];
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r16 = lane & 15, G = lane >> 4, KB = a.K / kGroup;
-    const int n0 = blockIdx.x * NF, m0 = blockIdx.y * MF * 16, n16s = a.N / 16;
+    const int n0 = blockIdx.x * NF, m0 = blockIdx.y * 16, n16s = a.N / 16;
     constexpr int gpb = MX ? 4 : 1;   // row scales per K block
     const int nbs = (a.N + kGroup - 1) / kGroup;
     const rsrc_t rx = make_rsrc(a.xq, (uint32_t)a.T * (uint32_t)a.K);
     const rsrc_t rw = make_rsrc(a.w, (uint32_t)a.K * (uint32_t)a.N);
     const rsrc_t rxs = make_rsrc(a.xs, (uint32_t)a.T * (uint32_t)(KB * gpb));
     const rsrc_t rws = make_rsrc(a.ws, MX ? (uint32_t)KB * (uint32_t)n16s * 64u : (uint32_t)KB * (uint32_t)nbs);
-    uint32_t xoff[MF], xsoff[MF], wfrag[NF];
-#pragma unroll
-    for (int i = 0; i < MF; ++i) {
-        const uint32_t row = (uint32_t)min(m0 + i * 16 + r16, a.T - 1);   // (rows past the end: not stored)
-        xoff[i] = row * (uint32_t)a.K + (MX ? 16 * G : 32 * G);
-        xsoff[i] = row * (uint32_t)(KB * gpb) + (MX ? G : 0);
-    }
+    const uint32_t xrow = (uint32_t)min(m0 + r16, a.T - 1);   // (rows past the end: not stored)
+    const uint32_t xoff = xrow * (uint32_t)a.K + (MX ? 16 * G : 32 * G);
+    const uint32_t xsoff = xrow * (uint32_t)(KB * gpb) + (MX ? G : 0);
+    uint32_t wfrag[NF];
 #pragma unroll
     for (int j = 0; j < NF; ++j)
         wfrag[j] = __builtin_amdgcn_readfirstlane((uint32_t)min(n0 + j, n16s - 1));
     const uint32_t l16 = 16 * lane;
-    v8i X[PF][MF], W[PF][NF];
-    uint8_t sx[PF][MF], sw[PF][NF];   // widened at their use: done at the load, that waits for it
+    v8i X[PF], W[PF][NF];
+    uint8_t sx[PF], sw[PF][NF];   // widened at their use: done at the load, that waits for it
     auto load = [&](int p, int blk) __attribute__((always_inline)) {
         const uint32_t kb = (uint32_t)min(blk, KB - 1);   // (past the end the last block again, unused)
 #pragma unroll
         for (int j = 0; j < NF; ++j) {
             const uint32_t f = (wfrag[j] * (uint32_t)KB + kb);
-            const v4i_t lo = __builtin_amdgcn_raw_buffer_load_b128(rw, l16, f * kFragBytes, MF > 2 ? 0 : MOE_WLOAD_AUX);
-            const v4i_t hi = __builtin_amdgcn_raw_buffer_load_b128(rw, l16 + 1024, f * kFragBytes, MF > 2 ? 0 : MOE_WLOAD_AUX);
+            const v4i_t lo = __builtin_amdgcn_raw_buffer_load_b128(rw, l16, f * kFragBytes, MOE_WLOAD_AUX);
+            const v4i_t hi = __builtin_amdgcn_raw_buffer_load_b128(rw, l16 + 1024, f * kFragBytes, MOE_WLOAD_AUX);
             W[p][j] = v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
             sw[p][j] = MX ? __builtin_amdgcn_raw_buffer_load_b8(rws, lane, f * 64, 0)
                           : __builtin_amdgcn_raw_buffer_load_b8(rws, 0, kb * nbs + wfrag[j] / 8, 0);
         }
-#pragma unroll
-        for (int i = 0; i < MF; ++i) {
-            const v4i_t lo = __builtin_amdgcn_raw_buffer_load_b128(rx, xoff[i], kb * kGroup, 0);
-            const v4i_t hi = __builtin_amdgcn_raw_buffer_load_b128(rx, xoff[i] + (MX ? 64 : 16), kb * kGroup, 0);
-            X[p][i] = v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-            sx[p][i] = __builtin_amdgcn_raw_buffer_load_b8(rxs, xsoff[i], kb * gpb, 0);
-        }
+        const v4i_t lo = __builtin_amdgcn_raw_buffer_load_b128(rx, xoff, kb * kGroup, 0);
+        const v4i_t hi = __builtin_amdgcn_raw_buffer_load_b128(rx, xoff + (MX ? 64 : 16), kb * kGroup, 0);
+        X[p] = v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        sx[p] = __builtin_amdgcn_raw_buffer_load_b8(rxs, xsoff, kb * gpb, 0);
     };
-    v4f acc[MF][NF];
+    v4f acc[NF];
 #pragma unroll
-    for (int i = 0; i < MF; ++i)
-#pragma unroll
-        for (int j = 0; j < NF; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < NF; ++j) acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
     auto products = [&](int p) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < MF; ++i)
-#pragma unroll
-            for (int j = 0; j < NF; ++j) acc[i][j] = mfma_fp8(W[p][j], X[p][i], acc[i][j], sw[p][j], sx[p][i]);
+        for (int j = 0; j < NF; ++j) acc[j] = mfma_fp8(W[p][j], X[p], acc[j], sw[p][j], sx[p]);
     };
     const int nk = KB > wv ? (KB - wv + WK - 1) / WK : 0;   // blocks wv, wv + WK, ... of this wave
 #pragma unroll
     for (int p = 0; p < PF; ++p) load(p, wv + p * WK);
-    // the bias and residual of the fragments that this wave will finish, fetched over the K loop
-    constexpr int QN = (MF * NF + WK - 1) / WK;
-    Extra ex[QN];
-    bool live[QN];
-#pragma unroll
-    for (int n = 0; n < QN; ++n) {
-        const int q = wv + n * WK, i = q / NF, j = q - i * NF, row = m0 + i * 16 + r16;
-        live[n] = q < MF * NF && n0 + j < n16s && row < a.T;
-        if (live[n]) ex[n] = load_extra(a, row, (n0 + j) * 16 + 4 * G);
-    }
+    // wave j finishes fragment j; its bias and residual are fetched over the K loop
+    static_assert(NF <= WK, "a wave per fragment");
+    const int row = m0 + r16, col = (n0 + wv) * 16 + 4 * G;
+    const bool live = wv < NF && n0 + wv < n16s && row < a.T;
+    Extra ex;
+    if (live) ex = load_extra(a, row, col);
     int i0 = 0;
     for (; i0 + PF <= nk; i0 += PF) {
 #pragma unroll
@@ -180,20 +166,13 @@ __global__ __launch_bounds__(64 * WK) void k_linear_stream(LinArgs a) {
     for (int p = 0; p < PF; ++p)
         if (i0 + p < nk) products(p);
 #pragma unroll
-    for (int i = 0; i < MF; ++i)
-#pragma unroll
-        for (int j = 0; j < NF; ++j) s_acc[wv][i * NF + j][lane] = acc[i][j];
+    for (int j = 0; j < NF; ++j) s_acc[wv][j][lane] = acc[j];
     __syncthreads();
+    if (!live) return;
+    v4f v = s_acc[0][wv][lane];
 #pragma unroll
-    for (int n = 0; n < QN; ++n) {
-        const int q = wv + n * WK, i = q / NF, j = q - i * NF;
-        if (live[n]) {
-            v4f v = s_acc[0][q][lane];
-#pragma unroll
-            for (int w = 1; w < WK; ++w) v += s_acc[w][q][lane];
-            put4(a, m0 + i * 16 + r16, (n0 + j) * 16 + 4 * G, v, ex[n]);
-        }
-    }
+    for (int w = 1; w < WK; ++w) v += s_acc[w][wv][lane];
+    put4(a, row, col, v, ex);
 }
 
 // ----------------------------------------------------------------------------------------
@@ -611,16 +590,18 @@ static hipError_t run_tile(const LinArgs& a, hipStream_t st) {
 // The same product where there are too few tiles to hide a K block's latency behind another workgroup:
 // both operands go through LDS, so that the copies are this kernel's only outstanding loads and their
 // number can be waited for.  S stages hold S - 2 K blocks on their way while block kb's products run
-// and block kb + 1's operands are read.  512 x 4096 x 4096: 15.6 us, one tile per CU, bound by the chain copy,
-// LDS read, product of its 32 K blocks.  (With a second set of waves for every other K block: 17.6 us.)
+// and block kb + 1's operands are read.  KS = 2: a second set of waves, with stages of its own, takes
+// every other K block and hands its sums over through LDS at the end.  Bound by the chain wait, LDS read,
+// product of a set's K blocks, about 0.27 us each (64 x 7168 x 7168: 14.1 us for 28, 3.9 TB/s of weights;
+// 512 x 4096 x 4096: 15.6 us), and by LDS reads on larger tiles (2048 x 4096 x 4096: 36.6 us, 1.9 PFLOP/s).
 template <int N>
 __device__ __forceinline__ void wait_vm() {
     asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
 }
 
-template <bool MX, int MI, int NJ, int WM, int WN, int S>
-__global__ __launch_bounds__(64 * WM * WN, 1) void k_linear_deep(LinArgs a, int tiles_m, int tiles_n) {
-    constexpr int NW = WM * WN, ROWS = 16 * MI * WM, COLS = 16 * NJ * WN, NTH = 64 * NW;
+template <bool MX, int MI, int NJ, int WM, int WN, int S, int KS>
+__global__ __launch_bounds__(64 * WM * WN * KS, 1) void k_linear_deep(LinArgs a, int tiles_m, int tiles_n) {
+    constexpr int NW = WM * WN, ROWS = 16 * MI * WM, COLS = 16 * NJ * WN, NTH = 64 * NW * KS;
     constexpr int DX = ROWS / 8 / NW, DW = COLS / 8 / NW;            // 1 KB copies of a wave and block
     constexpr int XB = ROWS * kGroup, WB = COLS * kGroup;
     constexpr int XS = MX ? ROWS * 4 : 0, WS = MX ? COLS * 4 : 0;    // MX: scales of a block
@@ -630,14 +611,16 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_linear_deep(LinArgs a, int 
     extern __shared__ __align__(16) uint8_t smem[];
     const int KB = a.K / kGroup, nbs = (a.N + kGroup - 1) / kGroup;
     constexpr int NBW = (COLS + 127) / 128, gpb = MX ? 4 : 1;
-    uint8_t* s_x = smem + S * STAGE;            // (128-element scales) [KB][WM][16][MI] bytes
+    uint8_t* s_x = smem + KS * S * STAGE;            // (128-element scales) [KB][WM][16][MI] bytes
     uint8_t* s_w = s_x + KB * ROWS;             // (128-element scales) [KB][column blocks of the tile]
     float* s_bias = reinterpret_cast<float*>(MX ? s_x : s_w + (KB * NBW + 15) / 16 * 16);   // [COLS]
     int tm, tn;
     if (!tile_of(tiles_m, tiles_n, tm, tn)) return;
-    const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int tid = threadIdx.x, lane = tid & 63, w0 = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int ks = w0 / NW, wv = w0 % NW;       // set of waves, wave of the set
     const int wm = wv / WN, wn = wv % WN, r16 = lane & 15, G = lane >> 4, x8 = r16 & 7;
     const int m0 = tm * ROWS, n0 = tn * COLS, n16s = a.N / 16;
+    uint8_t* ring = smem + ks * S * STAGE;
     const v4i_t rx = make_srd(a.xq, (uint32_t)a.T * (uint32_t)a.K);
     const v4i_t rw = make_srd(a.w, (uint32_t)a.K * (uint32_t)a.N);
     const v4i_t rxs = make_srd(a.xs, (uint32_t)a.T * (uint32_t)(KB * gpb));
@@ -645,7 +628,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_linear_deep(LinArgs a, int 
 
     uint4 res[MI][2];
     const int col0 = n0 + wn * NJ * 16, row0 = m0 + wm * MI * 16 + r16;
-    tile_residual<MI>(a, res, row0, col0);
+    if (ks == 0) tile_residual<MI>(a, res, row0, col0);
 
     uint32_t xoff[DX], wsrc[DW];   // rows as in k_linear_tile; weights: copy i of the wave, half a fragment
 #pragma unroll
@@ -659,7 +642,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_linear_deep(LinArgs a, int 
         const int g = wv + NW * i;
         wsrc[i] = __builtin_amdgcn_readfirstlane((uint32_t)min(n0 / 16 + (g >> 1), n16s - 1) * (uint32_t)KB * kFragBytes + (g & 1) * 1024);
     }
-    const uint32_t l16 = 16 * lane, lds0 = lds_addr(smem);
+    const uint32_t l16 = 16 * lane, lds0 = lds_addr(ring);
     uint32_t soff[DS ? DS : 1], sdst[DS ? DS : 1];
     bool srow[DS ? DS : 1];
     if constexpr (MX) {   // the rows' dwords [wm][row % 16][fragment], then the column fragments' 64 bytes each
@@ -678,8 +661,8 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_linear_deep(LinArgs a, int 
             sdst[i] = XB + WB + c * 256;
         }
     }
-    auto issue = [&](int blk, int st) __attribute__((always_inline)) {
-        const int kb = min(blk, KB - 1);   // (past the end the last block again: the count per step stays)
+    auto issue = [&](int blk, int st) __attribute__((always_inline)) {   // the set's block: K block blk KS + ks
+        const int kb = min(blk * KS + ks, KB - 1);   // (past the end the last block again: the count per step stays)
         const uint32_t base = __builtin_amdgcn_readfirstlane(lds0 + st * STAGE + wv * 1024);
 #pragma unroll
         for (int i = 0; i < DX; ++i) dma16(rx, base + i * NW * 1024, xoff[i], kb * kGroup);
@@ -704,8 +687,8 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_linear_deep(LinArgs a, int 
         int sx[MI], sw[NJ];
     };
     auto read = [&](int blk, int st, Ops& o) __attribute__((always_inline)) {
-        const uint8_t* cur = smem + st * STAGE;
-        const int kb = min(blk, KB - 1);
+        const uint8_t* cur = ring + st * STAGE;
+        const int kb = min(blk * KS + ks, KB - 1);
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
             const uint8_t* rowp = cur + ((wm * MI + i) * 16 + r16) * kGroup;
@@ -746,21 +729,36 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_linear_deep(LinArgs a, int 
 #pragma unroll
             for (int j = 0; j < NJ; ++j) acc[i][j] = mfma_fp8(C.w[j], C.x[i], acc[i][j], C.sw[j], C.sx[i]);
     };
+    const int n = (KB + KS - 1) / KS;   // blocks of a set; the last may lie past the end
     int i = 0;
-    for (; i + 2 < KB; i += 2) {
+    for (; i + 2 < n; i += 2) {
         step(i, A, B);
         products(A);
         step(i + 1, B, A);
         products(B);
     }
-    if (i + 1 < KB) {
+    if (i + 1 < n) {
         step(i, A, B);
         products(A);
-        products(B);
-    } else {
+        ++i;
+        if (KS == 1 || i * KS + ks < KB) products(B);
+    } else if (KS == 1 || i * KS + ks < KB) {
         products(A);
     }
     wait_all();
+    if constexpr (KS > 1) {   // the second set's sums, through the stages: every copy has ended, every read too
+        static_assert(KS == 2 && NW * MI * NJ * 1024 <= KS * S * STAGE, "one set hands over to one");
+        v4f* hand = reinterpret_cast<v4f*>(smem);
+        __syncthreads();
+        if (ks) {
+#pragma unroll
+            for (int q = 0; q < MI * NJ; ++q) hand[(wv * MI * NJ + q) * 64 + lane] = acc[q / NJ][q % NJ];
+        }
+        __syncthreads();
+        if (ks) return;
+#pragma unroll
+        for (int q = 0; q < MI * NJ; ++q) acc[q / NJ][q % NJ] += hand[(wv * MI * NJ + q) * 64 + lane];
+    }
 
     v4f bias[4];
 #pragma unroll
@@ -773,35 +771,39 @@ static size_t deep_lds(bool mx, int rows, int cols, int stages, int KB) {
     return (size_t)stages * (rows + cols) * (kGroup + (mx ? 4 : 0)) + cols * 4 +
            (mx ? 0 : (size_t)KB * rows + (KB * ((cols + 127) / 128) + 15) / 16 * 16);
 }
-template <bool MX, int MI, int NJ, int WM, int WN, int S>
+template <bool MX, int MI, int NJ, int WM, int WN, int S, int KS>
 static hipError_t run_deep_t(const LinArgs& a, hipStream_t st) {
     constexpr int ROWS = 16 * MI * WM, COLS = 16 * NJ * WN;
     const int tm = (int)ceil_div(a.T, ROWS), tn = (int)ceil_div(a.N, COLS);
-    const size_t lds = deep_lds(MX, ROWS, COLS, S, a.K / kGroup);
-    return launch_tiles<k_linear_deep<MX, MI, NJ, WM, WN, S>>(a, tm, tn, 64 * WM * WN, lds, st);
+    const size_t lds = deep_lds(MX, ROWS, COLS, KS * S, a.K / kGroup);
+    return launch_tiles<k_linear_deep<MX, MI, NJ, WM, WN, S, KS>>(a, tm, tn, 64 * WM * WN * KS, lds, st);
 }
-template <int MI, int NJ, int WM, int WN, int S>
+template <int MI, int NJ, int WM, int WN, int S, int KS>
 static hipError_t run_deep(const LinArgs& a, hipStream_t st) {
-    return a.mx ? run_deep_t<true, MI, NJ, WM, WN, S>(a, st) : run_deep_t<false, MI, NJ, WM, WN, S>(a, st);
+    return a.mx ? run_deep_t<true, MI, NJ, WM, WN, S, KS>(a, st) : run_deep_t<false, MI, NJ, WM, WN, S, KS>(a, st);
 }
 
-template <int MF, int NF, int WK, int PF>
+template <int NF, int WK, int PF>
 static hipError_t run_stream(const LinArgs& a, hipStream_t st) {
-    const dim3 grid((unsigned)ceil_div(a.N, 16 * NF), (unsigned)ceil_div(a.T, 16 * MF));
-    if (a.mx) hipLaunchKernelGGL((k_linear_stream<true, MF, NF, WK, PF>), grid, dim3(64 * WK), 0, st, a);
-    else hipLaunchKernelGGL((k_linear_stream<false, MF, NF, WK, PF>), grid, dim3(64 * WK), 0, st, a);
+    const dim3 grid((unsigned)ceil_div(a.N, 16 * NF), (unsigned)ceil_div(a.T, 16));
+    if (a.mx) hipLaunchKernelGGL((k_linear_stream<true, NF, WK, PF>), grid, dim3(64 * WK), 0, st, a);
+    else hipLaunchKernelGGL((k_linear_stream<false, NF, WK, PF>), grid, dim3(64 * WK), 0, st, a);
     return hipGetLastError();
 }
 
-// Variant by the number of workgroups that a tile size makes, times measured with a residual.
-//   * The stream kernel takes the smallest tile that does not make more of them than there are CUs,
-//     256: below that a larger tile only lengthens the one round (32 x 4096 x 512: 6.7 us on 16 x 16
-//     tiles, 11.7 on 32 x 32), above it every tile reads the operands again (64 x 7168 x 7168: 20.7 us on
-//     64 x 32 tiles, 224 of them, 37 on 16 x 32).  No tile is taller than the rows need.
-//   * 64 x 128 tiles with deep copies while at most two workgroups share a CU, with four stages where
-//     each has one to itself (512 x 4096 x 4096: 15.8 us; k_linear_tile on the same tiles 22.2;
-//     192 x 7168 x 7168: 22.8, 64 x 64 stream tiles 47) and three, which fit twice, else
-//     (1024 x 4096 x 4096: 24.1, four stages 29.7).
+// Variant by the number of workgroups that a tile size makes (256: one per CU), times measured with a
+// residual.
+//   * The stream kernel while its 16-row tiles are no more than that: the narrower of its two (32 x 4096 x 512:
+//     6.7 us on 16 columns, 11.7 on 32), then the other (48 x 7168 x 2048: 10.0; deep 64 x 64 tiles 13.2).  More
+//     tiles would read the activations again and again (32 x 2048 x 5632: 8.7, deep 6.7).
+//   * Deep 64 x 64 tiles with two sets of waves, which halve a tile's chain of K blocks (64 x 7168 x 7168: 14.1 us,
+//     one set 16.7, stream tiles 20; 128 x 4096 x 4096: 9.6, deep 64 x 128 tiles 15).
+//   * Up to eight rows, whose re-reading costs little, the stream kernel again where those would be more tiles
+//     (1 x 7168 x 18432: 24 us, 64 x 128 tiles 30; 16 x 2048 x 20480: 13.7 and 10.3).
+//   * Deep 64 x 128 tiles, with four stages where each has a CU to itself (512 x 4096 x 4096: 15.6 us, a second set
+//     of waves 17.6, k_linear_tile on the same tiles 22.2; 192 x 7168 x 7168: 22.8) and three, which fit twice,
+//     while two share one (1024 x 4096 x 4096: 23.2, four stages 29.0) or there is one row of tiles
+//     (64 x 4096 x 131072: 95, 128 x 256 tiles 103).
 //   * Then 128 x 256 tiles.  While each has a CU to itself, deep copies with eight waves (2048 x 4096 x 4096:
 //     36.7 us, MXFP8 43.9; k_linear_tile on 64 x 256 tiles 37.9 and 50.7, deep 64 x 128 tiles 44.6 and 48.9),
 //     but with 128-element scales 64 x 256 k_linear_tile if they leave more than a few CUs idle (1300 x 2048 x
@@ -814,15 +816,15 @@ hipError_t launch_linear(const LinArgs& args, hipStream_t st) {
     // running tiles share (16384 x 4096 x 4096 in bf16: 238 -> 224 us).
     a.nt = (int64_t)a.T * a.N * (a.out_bf16 ? 2 : 4) >= (32 << 20);
     auto fits = [&](int rows, int cols, int64_t most) { return ceil_div(a.T, rows) * ceil_div(a.N, cols) <= most; };
-    if (fits(16, 16, 256)) return run_stream<1, 1, 4, 4>(a, st);
-    if (fits(16, 32, 256) || a.T <= 16) return run_stream<1, 2, 4, 4>(a, st);
-    if (fits(32, 32, 256) || a.T <= 32) return run_stream<2, 2, 4, 4>(a, st);
-    if (fits(64, 32, 256) || a.T <= 64) return run_stream<4, 2, 4, 3>(a, st);
-    if (fits(64, 128, 256)) return run_deep<2, 4, 2, 2, 4>(a, st);
-    if (fits(64, 128, 512)) return run_deep<2, 4, 2, 2, 3>(a, st);
+    if (fits(16, 16, 256)) return run_stream<1, 4, 4>(a, st);
+    if (fits(16, 32, 256)) return run_stream<2, 4, 4>(a, st);
+    if (fits(64, 64, 256)) return run_deep<1, 4, 4, 1, 4, 2>(a, st);
+    if (a.T <= 8) return run_stream<2, 4, 4>(a, st);
+    if (fits(64, 128, 256)) return run_deep<2, 4, 2, 2, 4, 1>(a, st);
+    if (fits(64, 128, 512) || a.T <= 64) return run_deep<2, 4, 2, 2, 3, 1>(a, st);
     if (fits(128, 256, 256)) {
         if ((a.mx || !fits(128, 256, 208)) && deep_lds(a.mx, 128, 256, 3, a.K / kGroup) <= kLdsBytes)
-            return run_deep<4, 4, 2, 4, 3>(a, st);
+            return run_deep<4, 4, 2, 4, 3, 1>(a, st);
         return run_tile<4, 4, 1, 4>(a, st);
     }
     return run_tile<8, 4, 1, 4>(a, st);

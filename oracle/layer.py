@@ -91,7 +91,8 @@ def _scores(logits, scoring):
         lse = np.where(tot[:, 0] != 0, np.where(np.isneginf(m), 0.0, m)[:, 0] + np.log(tot[:, 0]), 0.0)
     if scoring == "softmax":
         return soft, soft, np.ones_like(soft), soft, lse
-    e = np.exp(-l)
+    with np.errstate(over="ignore"):
+        e = np.exp(-l)
     s = 1.0 / (1.0 + e)
     z = s.sum(axis=1, keepdims=True)
     p = np.divide(s, z, out=np.zeros_like(s), where=z != 0)

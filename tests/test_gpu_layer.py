@@ -300,6 +300,11 @@ LINEAR_CASES = [  # T, K, N, scheme, act, bias, residual, out
     (2850, 640, 6160, "fp8", "none", True, False, "f32"), (3000, 128, 6160, "fp8", "relu", True, True, "bf16"),
     (1100, 512, 4112, "mxfp8", "gelu", True, True, "bf16"), (1900, 384, 2832, "fp8", "none", True, True, "f32"),
     (1900, 640, 3856, "fp8", "silu", True, False, "bf16"),
+    (60, 128, 8208, "mxfp8", "none", True, True, "bf16"), (20, 640, 12304, "fp8", "gelu", False, True, "f32"),
+    (130, 256, 4112, "fp8", "none", True, False, "bf16"), (3, 256, 16528, "fp8", "none", True, True, "bf16"),
+    (8, 128, 16528, "mxfp8", "silu", False, False, "f32"), (20, 384, 16528, "mxfp8", "none", True, True, "bf16"),
+    (10, 128, 32912, "fp8", "relu", True, False, "bf16"), (400, 384, 3600, "mxfp8", "gelu_tanh", True, True, "f32"),
+    (400, 512, 3600, "fp8", "none", False, True, "bf16"), (64, 32768, 528, "mxfp8", "none", False, False, "bf16"),
     (900, 15104, 7184, "fp8", "none", False, True, "bf16"), (900, 15232, 7184, "fp8", "none", True, False, "bf16"),
 ]
 
