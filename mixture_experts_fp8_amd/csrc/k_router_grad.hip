@@ -569,8 +569,8 @@ hipError_t launch_route_backward(const RouteBwdArgs& a, hipStream_t st) {
 // past the caches.
 typedef unsigned v4u_t __attribute__((ext_vector_type(4)));
 template <bool BF16, int G, bool DOUT>
-__global__ __launch_bounds__(256) void k_combine_bwd(CombineBwdArgs a) {
-    constexpr int RPB = 256 / G, CW = BF16 ? 8 : 4, NW = G / 64;
+__global__ __launch_bounds__(G < 256 ? 256 : G) void k_combine_bwd(CombineBwdArgs a) {
+    constexpr int RPB = G < 256 ? 256 / G : 1, CW = BF16 ? 8 : 4, NW = G / 64;
     __shared__ float s_dot[RPB][NW][8];
     const int sub = threadIdx.x % G, r = threadIdx.x / G;
     const int64_t tt = (int64_t)blockIdx.x * RPB + r;
@@ -661,21 +661,26 @@ __global__ __launch_bounds__(256) void k_combine_bwd(CombineBwdArgs a) {
 
 template <bool BF16, int G>
 static void run_combine_bwd(const CombineBwdArgs& a, hipStream_t st) {
-    const dim3 grid((unsigned)ceil_div(a.T, 256 / G));
-    if (a.deo) hipLaunchKernelGGL((k_combine_bwd<BF16, G, true>), grid, dim3(256), 0, st, a);
-    else hipLaunchKernelGGL((k_combine_bwd<BF16, G, false>), grid, dim3(256), 0, st, a);
+    constexpr int RPB = G < 256 ? 256 / G : 1;
+    const dim3 grid((unsigned)ceil_div(a.T, RPB)), block(G * RPB);
+    if (a.deo) hipLaunchKernelGGL((k_combine_bwd<BF16, G, true>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((k_combine_bwd<BF16, G, false>), grid, block, 0, st, a);
 }
 
 // Threads per token, by its nv vectors.  Few tokens: as many as there are vectors, one round of loads
-// (64 x 4096 bf16: 6.3 us with 256 threads, 15 with 64).  Otherwise fewer where rows are short, for more
-// rounds in flight from fewer workgroups (2047 x 768 float32: 128 threads 11.6 us, 256 14.8), and a wave
-// where dexpert_out is written too (2047 x 2816 bf16: 40 us, 128 threads 46); 256 from 512 vectors on
-// (4096 x 4096 bf16 with dexpert_out: 108 us, 64 threads 138).
+// (64 x 4096 bf16: 5.4 us with 512 threads, 6.1 with 256, 15 with 64; 1024 have no registers for eight
+// rows in flight), but no more than 256 where there are more tokens than CUs (512 x 7168: 27 us, 512
+// threads 30).  Otherwise fewer where rows are short, for more rounds in flight from fewer workgroups: 128
+// (2047 x 768 float32: 11.3 us, 256 threads 14.8; 1100 x 4000 bf16: 17.8, 64 threads 23.6), and a wave where
+// every CU has 16 tokens (16384 x 768 bf16: 45.9 us, 128 threads 52.6; 4096 x 1024: 9.9 and 11.9); 256 from
+// 512 vectors on (4096 x 4096 bf16 with dexpert_out: 108 us, 64 threads 138).  The choice does not look at
+// dexpert_out: the weights' gradient has the same bits with and without it.
 template <bool BF16>
 static void pick_combine_bwd(const CombineBwdArgs& a, hipStream_t st) {
     const int nv = a.H / (BF16 ? 8 : 4);
-    if (nv <= 64 || (a.T >= 1024 && nv < 512 && a.deo)) run_combine_bwd<BF16, 64>(a, st);
+    if (nv <= 64 || (a.T >= 4096 && nv < 512)) run_combine_bwd<BF16, 64>(a, st);
     else if (nv <= 128 || (a.T >= 1024 && nv < 512)) run_combine_bwd<BF16, 128>(a, st);
+    else if (a.T <= 256 && nv > 256) run_combine_bwd<BF16, 512>(a, st);
     else run_combine_bwd<BF16, 256>(a, st);
 }
 

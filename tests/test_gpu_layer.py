@@ -593,7 +593,8 @@ def test_balance_counts_are_the_routers():
 
 # ---- combine --------------------------------------------------------------------------------
 COMBINE_CASES = [(1, 1, 8, "bf16"), (3, 2, 768, "f32"), (5, 8, 1024, "bf16"), (4, 9, 1032, "f32"), (2, 17, 2816, "bf16"),
-                 (37, 8, 4096, "bf16"), (6, 3, 8192, "f32"), (130, 1, 264, "bf16")]
+                 (37, 8, 4096, "bf16"), (6, 3, 8192, "f32"), (130, 1, 264, "bf16"),
+                 (256, 2, 2064, "bf16"), (257, 2, 2064, "bf16"), (9, 10, 4104, "f32"), (1030, 1, 4096, "f32"), (1024, 3, 520, "f32")]
 
 
 @pytest.mark.parametrize("T,k,H,dtype", COMBINE_CASES)
