@@ -80,12 +80,13 @@ __device__ __forceinline__ double rsqrt_f64(double x) {
 
 // A double as a float that rounds to the same bf16: rounded to odd (towards zero, the last bit set where
 // anything was cut off).  Rounded to nearest it could land on the middle of two bf16 values and be
-// rounded the other way then, which happens to one value in 2^17.
+// rounded the other way then, which happens to one value in 2^17.  Infinities (of an infinite weight) and NaN
+// have no remainder that compares with 0 and stay as they are.
 __device__ __forceinline__ float round_odd(double d) {
     const float f = (float)d;
     const double r = d - (double)f;
     uint32_t u = __float_as_uint(f);
-    if (r != 0.0) u = (u - ((r > 0.0) != (d > 0.0) ? 1u : 0u)) | 1u;
+    if (r < 0.0 || r > 0.0) u = (u - ((r > 0.0) != (d > 0.0) ? 1u : 0u)) | 1u;
     return __uint_as_float(u);
 }
 
