@@ -563,11 +563,14 @@ int moe_route_backward(const moe_route_backward_args* a);
  *   dtopk_weights[t, j]             = sum_c dy[t, c] * expert_out[assign_pos[t*k+j], c]   (float32)
  *   dexpert_out[assign_pos[t*k+j]]  = topk_weights[t, j] * dy[t]     (dtype, rounded once)
  * Either output may be NULL (then expert_out, or topk_weights, may be too).  Entries of
- * assign_pos outside [0, T*k) are dropped assignments: their weight gradient is 0, and rows of
- * dexpert_out that no entry names are left as they were.  No two entries may name the same row
- * with dexpert_out.
+ * assign_pos outside [0, T*k) are dropped assignments: their weight gradient is 0.  Rows of
+ * dexpert_out that no entry names are left as they were, or set to 0 with clear_rows, which a
+ * buffer that is written call after call needs where assignments may be dropped.  No two entries
+ * may name the same row with dexpert_out.
  *   expert_out, dexpert_out  [T*k, H] of dtype MOE_DTYPE_F32 or MOE_DTYPE_BF16, 16-byte aligned;
- *   dexpert_out may be expert_out itself.  dy 16-byte aligned.  H % 8 == 0; T * k < 2^29. */
+ *   without clear_rows dexpert_out may be expert_out itself.  dy 16-byte aligned.  H % 8 == 0;
+ *   T * k < 2^29.
+ *   clear_rows  0 or 1; ignored without dexpert_out. */
 typedef struct moe_combine_backward_args {
     int32_t T, k, H;
     int32_t dtype;
@@ -578,6 +581,7 @@ typedef struct moe_combine_backward_args {
     float*          dtopk_weights;
     void*           dexpert_out;
     void*           stream;
+    int32_t         clear_rows;
 } moe_combine_backward_args;
 int moe_combine_backward(const moe_combine_backward_args* a);
 

@@ -568,12 +568,53 @@ hipError_t launch_route_backward(const RouteBwdArgs& a, hipStream_t st) {
 // for every 8 slots.  Bound by HBM: the expert rows are read once and (dexpert_out) written once, both
 // past the caches.
 typedef unsigned v4u_t __attribute__((ext_vector_type(4)));
+
+// Rows that no assignment names: each of the first nclear workgroups takes `per` rows, marks in LDS
+// those that an entry of pos names (all entries pass by, from the caches) and writes zeros to the others:
+// no launch, workspace or atomic in memory of its own.
+constexpr int kClearMost = 256, kClearRows = 1 << 16;   // workgroups, rows of one
+template <bool BF16, int NT>
+__device__ __forceinline__ void clear_rows(const CombineBwdArgs& a, int per, uint32_t* s_bits) {
+    const int tid = threadIdx.x, A = a.T * a.k;
+    const int lo = blockIdx.x * per, n = min(per, A - lo);
+    for (int i = tid; i < (per + 31) / 32; i += NT) s_bits[i] = 0;
+    __syncthreads();
+    auto mark = [&](int p) __attribute__((always_inline)) {
+        const uint32_t r = (uint32_t)p - (uint32_t)lo;
+        if (r < (uint32_t)n) atomicOr(&s_bits[r >> 5], 1u << (r & 31));
+    };
+    const int head = min(A, (int)(-(reinterpret_cast<uintptr_t>(a.pos) >> 2) & 3)), nq = (A - head) / 4;
+    const int4* q = reinterpret_cast<const int4*>(a.pos + head);
+    for (int i0 = 0; i0 < nq; i0 += 8 * NT) {   // eight vectors of 4 in flight
+        int4 p[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int i = i0 + u * NT + tid;
+            p[u] = i < nq ? q[i] : make_int4(-1, -1, -1, -1);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) mark(p[u].x), mark(p[u].y), mark(p[u].z), mark(p[u].w);
+    }
+    if (tid < head) mark(a.pos[tid]);
+    if (tid < A - head - 4 * nq) mark(a.pos[head + 4 * nq + tid]);
+    __syncthreads();
+    const int nv = a.H / (BF16 ? 8 : 4);
+    for (int r = tid >> 6; r < n; r += NT / 64)
+        if (!(s_bits[r >> 5] >> (r & 31) & 1))
+            for (int v = tid & 63; v < nv; v += 64)
+                __builtin_nontemporal_store(v4u_t{0, 0, 0, 0}, reinterpret_cast<v4u_t*>(a.deo) + (int64_t)(lo + r) * nv + v);
+}
+
 template <bool BF16, int G, bool DOUT>
-__global__ __launch_bounds__(G < 256 ? 256 : G) void k_combine_bwd(CombineBwdArgs a) {
+__global__ __launch_bounds__(G < 256 ? 256 : G) void k_combine_bwd(CombineBwdArgs a, int nclear, int per) {
     constexpr int RPB = G < 256 ? 256 / G : 1, CW = BF16 ? 8 : 4, NW = G / 64;
     __shared__ float s_dot[RPB][NW][8];
+    if constexpr (DOUT) {
+        __shared__ uint32_t s_bits[kClearRows / 32];
+        if (blockIdx.x < nclear) return clear_rows<BF16, G * RPB>(a, per, s_bits);   // (uniform)
+    }
     const int sub = threadIdx.x % G, r = threadIdx.x / G;
-    const int64_t tt = (int64_t)blockIdx.x * RPB + r;
+    const int64_t tt = (int64_t)(blockIdx.x - nclear) * RPB + r;
     const bool on = tt < a.T;           // (the barriers below are for every thread)
     const int64_t t = on ? tt : a.T - 1;
     const int nv = on ? a.H / CW : 0;
@@ -659,12 +700,29 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_combine_bwd(CombineBwdArg
     }
 }
 
+// Zeros for all of dexpert_out, before the rows that are named.
+__global__ __launch_bounds__(256) void k_zero(v4u_t* p, int64_t n) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+        __builtin_nontemporal_store(v4u_t{0, 0, 0, 0}, p + i);
+}
+
 template <bool BF16, int G>
 static void run_combine_bwd(const CombineBwdArgs& a, hipStream_t st) {
     constexpr int RPB = G < 256 ? 256 / G : 1;
-    const dim3 grid((unsigned)ceil_div(a.T, RPB)), block(G * RPB);
-    if (a.deo) hipLaunchKernelGGL((k_combine_bwd<BF16, G, true>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((k_combine_bwd<BF16, G, false>), grid, block, 0, st, a);
+    const int64_t A = (int64_t)a.T * a.k;
+    int nclear = 0, per = 0;
+    // In the kernel itself (16384 x 8 x 4096 bf16: 434 us, without clearing 431, zeros first 596; 32 x 8 x 2816:
+    // 5.6, 5.6 and 7.4), but zeros first where reading all entries 256 times takes longer than writing the rows
+    // (65536 x 8 x 64 bf16: 139 us, in the kernel 157; x 256: 194 and 190) or LDS holds too few marks.
+    if (a.clear && A <= (int64_t)kClearMost * kClearRows && (A <= (1 << 16) || a.H * (BF16 ? 2 : 4) >= 256)) {
+        per = (int)std::max<int64_t>(64, ceil_div(A, kClearMost));
+        nclear = (int)ceil_div(A, per);
+    } else if (a.clear) {
+        hipLaunchKernelGGL(k_zero, dim3(2048), dim3(256), 0, st, static_cast<v4u_t*>(a.deo), A * a.H / (BF16 ? 8 : 4));
+    }
+    const dim3 grid((unsigned)ceil_div(a.T, RPB) + nclear), block(G * RPB);
+    if (a.deo) hipLaunchKernelGGL((k_combine_bwd<BF16, G, true>), grid, block, 0, st, a, nclear, per);
+    else hipLaunchKernelGGL((k_combine_bwd<BF16, G, false>), grid, block, 0, st, a, 0, 0);
 }
 
 // Threads per token, by its nv vectors.  Few tokens: as many as there are vectors, one round of loads

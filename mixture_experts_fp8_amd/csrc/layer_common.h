@@ -119,6 +119,7 @@ struct CombineBwdArgs {
     const float* wt;      // or NULL with deo NULL
     float* dwt;
     void* deo;
+    int clear;            // rows of deo that pos does not name become 0
 };
 hipError_t launch_combine_backward(const CombineBwdArgs& a, hipStream_t st);
 

@@ -303,6 +303,8 @@ int check_combine_backward(const moe_combine_backward_args* a) {
         return fail(MOE_ERR_INVALID, "%s: one of dtopk_weights and dexpert_out must be given", op);
     if (a->dtopk_weights && !a->expert_out) return fail(MOE_ERR_INVALID, "%s: dtopk_weights needs expert_out", op);
     if (a->dexpert_out && !a->topk_weights) return fail(MOE_ERR_INVALID, "%s: dexpert_out needs topk_weights", op);
+    if (a->clear_rows != 0 && a->clear_rows != 1)
+        return fail(MOE_ERR_INVALID, "%s: clear_rows (%d) must be 0 or 1", op, a->clear_rows);
     if (!aligned(a->dy, 16) || !aligned(a->expert_out, 16) || !aligned(a->dexpert_out, 16))
         return fail(MOE_ERR_UNSUPPORTED, "%s: dy, expert_out and dexpert_out must be 16-byte aligned", op);
     const uint64_t ne = (uint64_t)T * k * H * (a->dtype == MOE_DTYPE_BF16 ? 2 : 4), nk = (uint64_t)T * k * 4;
@@ -312,7 +314,7 @@ int check_combine_backward(const moe_combine_backward_args* a) {
     if (int rc = check_outputs(op, out, 2)) return rc;
     for (int i = 0; i < 2; ++i)
         for (int j = 0; j < 4; ++j)
-            if (int rc = check_io(op, out[i], in[j], i == 1 && j == 1)) return rc;
+            if (int rc = check_io(op, out[i], in[j], i == 1 && j == 1 && !a->clear_rows)) return rc;
     return MOE_OK;
 }
 

@@ -57,7 +57,7 @@ class RouteBackwardArgs(ctypes.Structure):
 class CombineBackwardArgs(ctypes.Structure):
     _fields_ = [("T", _i32), ("k", _i32), ("H", _i32), ("dtype", _i32), ("dy", _vp), ("expert_out", _vp),
                 ("assign_pos", _vp), ("topk_weights", _vp), ("dtopk_weights", _vp), ("dexpert_out", _vp),
-                ("stream", _vp)]
+                ("stream", _vp), ("clear_rows", _i32)]
 
 
 # The current device and a device's current stream as plain integers, without building a Stream object
@@ -372,8 +372,9 @@ class MoeCombineBackward(_Call):
     """Gradients of moe_combine from dy bf16 [T, H].  A call returns {"dweights": float32 [T, k] (None
     with want_dweights=False), "d_expert_out": [T*k, H] of expert_out's dtype (None unless asked for)}.
 
-    d_expert_out: False, True (a new tensor) or the tensor to write (it may be expert_out itself); rows
-    that assign_pos does not name are left as they are (a new tensor is filled with zeros once)."""
+    d_expert_out: False, True (a new tensor) or the tensor to write (it may be expert_out itself).  Every
+    call sets the rows of a new tensor that assign_pos does not name to 0; those of a given one are left
+    as they are."""
 
     def __init__(self, dy: torch.Tensor, expert_out: torch.Tensor, assign_pos: torch.Tensor, topk_weights: torch.Tensor,
                  d_expert_out=False, want_dweights: bool = True):
@@ -392,13 +393,13 @@ class MoeCombineBackward(_Call):
             deo = d_expert_out
             _need(deo, "d_expert_out", expert_out.dtype, (T * k, H))
         elif d_expert_out:
-            deo = torch.zeros_like(expert_out)
+            deo = torch.empty_like(expert_out)
         dw = torch.empty(T, k, dtype=torch.float32, device=dy.device) if want_dweights else None
         dt = B.MOE_DTYPE_BF16 if expert_out.dtype == torch.bfloat16 else B.MOE_DTYPE_F32
         self.out = {"dweights": dw, "d_expert_out": deo}
         self._hold("moe_combine_backward",
                    CombineBackwardArgs(T, k, H, dt, _ptr(dy), _ptr(expert_out), _ptr(assign_pos), _ptr(topk_weights),
-                                       _ptr(dw), _ptr(deo), None),
+                                       _ptr(dw), _ptr(deo), None, int(deo is not None and deo is not d_expert_out)),
                    (dy, expert_out, assign_pos, topk_weights, dw, deo))
 
     def __call__(self, stream: Optional[int] = None) -> dict:

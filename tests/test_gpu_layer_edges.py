@@ -38,3 +38,76 @@ def test_add_rmsnorm_infinite_weights(H, quant):
     if quant:
         q, s = M.moe_quant_act(out["y"]) if quant == "fp8" else M.moe_quant_act_mx(out["y"])
         assert torch.equal(out["yq"], q) and torch.equal(out["ys"], s)
+
+
+# ---- combine --------------------------------------------------------------------------------
+def _combine_inputs(T, k, H, dtype, key):
+    g = rng(33, T, k, H, key)
+    mk = bf16 if dtype == "bf16" else f32
+    return mk(g.standard_normal((T * k, H)))[0], bf16(g.standard_normal((T, H)))[0], f32(g.random((T, k)))[0], g
+
+
+def _rows_of(pos, T, k, H, w, dy, dtype):
+    """d_expert_out: the named rows' gradients (one float32 product, then rounded to dtype), zeros beside them."""
+    want = torch.zeros(T * k, H, dtype=dtype, device=DEV)
+    f = np.nonzero((pos >= 0) & (pos < T * k))[0]
+    rows, f = torch.from_numpy(pos[f].astype(np.int64)).to(DEV), torch.from_numpy(f).to(DEV)
+    want[rows] = (w.reshape(-1)[f, None] * dy.float()[f // k]).to(dtype)
+    return want
+
+
+COMBINE_EDGES = [(1, 1, 8, "bf16"), (5, 8, 1024, "bf16"), (4, 9, 1032, "f32"), (300, 8, 264, "bf16"), (300, 3, 4096, "f32"),
+                 (4099, 2, 1032, "bf16"), (4099, 1, 264, "f32"), (70000, 1, 8, "bf16"), (2100, 10, 72, "f32"),
+                 (40001, 2, 128, "bf16")]
+
+
+@pytest.mark.parametrize("T,k,H,dtype", COMBINE_EDGES)
+def test_combine_handle_with_changing_assignments(T, k, H, dtype):
+    """Rows that a later call no longer names hold that call's gradient, 0, not an earlier one's."""
+    eo, dy, w, g = _combine_inputs(T, k, H, dtype, 1)
+    A = T * k
+    at = T % 4                      # (entries at any 4-byte address)
+    pos = torch.zeros(A + 4, dtype=torch.int32, device=DEV)[at:at + A]
+    pos.copy_(torch.from_numpy(g.permutation(A).astype(np.int32)))
+    call = M.MoeCombineBackward(dy, eo, pos, w, d_expert_out=True)
+    for share in (0.0, 0.3, 0.9, 1.0, 0.05):
+        p = g.permutation(A).astype(np.int32)
+        p[g.random(A) < share] = -1
+        if share == 0.3:
+            p[p == -1] = A + 5      # (past the end is dropped as well)
+        pos.copy_(torch.from_numpy(p))
+        out = call()
+        want = _rows_of(p, T, k, H, w, dy, eo.dtype)
+        assert torch.equal(out["d_expert_out"], want), share
+        assert torch.equal(M.moe_combine_backward(dy, eo, pos, w, d_expert_out=True)["d_expert_out"], want)
+    # whatever the buffer held
+    call.out["d_expert_out"].fill_(float("nan"))
+    assert torch.equal(call()["d_expert_out"], want)
+    # a caller's own tensor keeps its other rows
+    mine = torch.full_like(eo, 3.0)
+    M.moe_combine_backward(dy, eo, pos, w, d_expert_out=mine)
+    named = torch.zeros(A, dtype=torch.bool, device=DEV)
+    named[pos[(pos >= 0) & (pos < A)].long()] = True
+    assert (mine[~named] == 3.0).all() and torch.equal(mine[named], want[named])
+
+
+def test_combine_handle_with_changing_assignments_in_a_graph():
+    T, k, H = 500, 4, 520
+    eo, dy, w, g = _combine_inputs(T, k, H, "bf16", 2)
+    pos = torch.from_numpy(g.permutation(T * k).astype(np.int32)).to(DEV)
+    call = M.MoeCombineBackward(dy, eo, pos, w, d_expert_out=True)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            call()
+    for share in (0.5, 0.0, 0.9, 0.2):
+        p = g.permutation(T * k).astype(np.int32)
+        p[g.random(T * k) < share] = -1
+        pos.copy_(torch.from_numpy(p))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(call.out["d_expert_out"], _rows_of(p, T, k, H, w, dy, eo.dtype)), share
+        M.moe_combine_backward(dy, eo, pos, w)
+        torch.cuda.synchronize()
