@@ -459,6 +459,9 @@ size_t moe_add_rmsnorm_backward_workspace_size(int32_t T, int32_t H);
 #define MOE_ACT_SILU       2   /* v / (1 + exp(-v))                                        */
 #define MOE_ACT_GELU       3   /* v * (1 + erf(v / sqrt 2)) / 2                            */
 #define MOE_ACT_GELU_TANH  4   /* v * (1 + tanh(sqrt(2/pi) * (v + 0.044715 v^3))) / 2       */
+/* They are formed in float32 without cancellation, so that small values keep their digits: off by at most
+ * (3 x + 32) 2^-24 of the value, where x is the exponent in it: |v| (SILU), v^2 / 2 (GELU), or 7/3 of the
+ * doubled argument of tanh (GELU_TANH).  Values under 2^-122 may be 0. */
 
 /* moe_linear: y = act( dequant(xq, xs) @ dequant(w, w_scale) + bias ) + residual, FP8 x FP8 with
  * float32 accumulation and one rounding to y's type at the end.  (The matrix instruction aligns the

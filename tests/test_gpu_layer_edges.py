@@ -40,6 +40,41 @@ def test_add_rmsnorm_infinite_weights(H, quant):
         assert torch.equal(out["yq"], q) and torch.equal(out["ys"], s)
 
 
+# ---- linear -------------------------------------------------------------------------------
+def _tail(name, v):
+    """The activation in 64 bits without the cancellation of 1 + erf(v / sqrt 2) and 1 + tanh u."""
+    from scipy.special import ndtr
+    if name == "gelu":
+        return v * ndtr(v)
+    if name == "silu":
+        return v / (1.0 + np.exp(-v))
+    u = np.sqrt(2.0 / np.pi) * (v + 0.044715 * v ** 3)
+    return v / (1.0 + np.exp(-2.0 * u))
+
+
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("T,N", [(1, 8192), (80, 8192), (600, 4096), (2100, 8192)])
+def test_linear_activation_tails(act, T, N):
+    """Relative to the activation's own value, also where that is small.  With rows of zeros the sum is
+    0 and the activation's argument is the bias itself."""
+    w = M.LinearWeights.from_float(torch.zeros(128, N, device=DEV))
+    v, vf = f32(np.concatenate([np.linspace(-12.8, -0.01, N // 2), np.linspace(1e-3, 9.0, N // 2)]))
+    w.bias = v
+    xq, xs = M.moe_quant_act(torch.zeros(T, 128, dtype=torch.bfloat16, device=DEV))
+    want = _tail(act, vf)[None]
+    # The exponent x is off by 3 u |x| (a product or two and a constant), which is the relative error of
+    # exp x: |x| is v^2 / 2, |2 u(v)| (whose argument adds another 4 u) and |v|.  Beside it: reciprocal and
+    # exponential instructions (one unit in the last place, 2 u each), the polynomial of GELU (fit 3 u,
+    # eight terms of one size 8 u, its argument's 6 u) and the last products.
+    x = {"gelu": 0.5 * vf ** 2, "silu": np.abs(vf),
+         "gelu_tanh": 2 * np.abs(np.sqrt(2 / np.pi) * (vf + 0.044715 * vf ** 3)) * 7 / 3}[act][None]
+    rel = (3 * x + 32) * U
+    for dt in (torch.float32, torch.bfloat16):
+        got = host(M.moe_linear(xq, xs, w, act, out_dtype=dt))
+        tol = rel * np.abs(want) + 2.0 ** -122 + (UB * np.abs(want) * (1 + rel) if dt == torch.bfloat16 else 0)
+        within(got, np.broadcast_to(want, got.shape), np.broadcast_to(tol, got.shape), f"{act} {dt}")
+
+
 # ---- combine --------------------------------------------------------------------------------
 def _combine_inputs(T, k, H, dtype, key):
     g = rng(33, T, k, H, key)
