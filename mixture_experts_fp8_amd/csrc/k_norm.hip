@@ -200,11 +200,24 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_rmsnorm(NormArgs a) {
 }
 
 template <int G, int VPT>
-static void run_norm(const NormArgs& a, hipStream_t st) {
+static void run_norm(const NormArgs& args, hipStream_t st) {
     constexpr int RPB = G < 256 ? 256 / G : 1;
-    const dim3 grid((unsigned)ceil_div(a.T, RPB)), block(G < 256 ? 256 : G);
-    if (streamed(a.T, a.H)) hipLaunchKernelGGL((k_add_rmsnorm<G, VPT, true>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((k_add_rmsnorm<G, VPT, false>), grid, block, 0, st, a);
+    const dim3 block(G < 256 ? 256 : G);
+    NormArgs a = args;
+    for (int64_t t = 0; t < args.T; t += launch_rows(G)) {
+        a.T = (int)std::min<int64_t>(args.T - t, launch_rows(G));
+        a.x = args.x + t * args.ldx;
+        if (args.res) a.res = args.res + t * args.ldr;
+        if (args.h) a.h = args.h + t * args.H;
+        if (args.y) a.y = args.y + t * args.H;
+        if (args.yq) {
+            a.yq = args.yq + t * args.H;
+            a.ys = args.ys + t * (args.H / args.group);
+        }
+        const dim3 grid((unsigned)ceil_div(a.T, RPB));
+        if (streamed(args.T, args.H)) hipLaunchKernelGGL((k_add_rmsnorm<G, VPT, true>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((k_add_rmsnorm<G, VPT, false>), grid, block, 0, st, a);
+    }
 }
 
 hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t st) {

@@ -377,7 +377,6 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouteBwdArgs a) {
     __shared__ int s_n[2][4];
     __shared__ __align__(16) float s_d[NG][L * N], s_m[NG][L * N];
     const int tid = threadIdx.x, g = tid / L, sub = tid % L;
-    const int64_t t = (int64_t)blockIdx.x * NG + g;
     const Seqs sq{a.off, a.S, a.T};
     const bool staged = a.off && a.S <= kSeqLds;
     int live = 1, valid = a.T;
@@ -403,152 +402,153 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouteBwdArgs a) {
         live = s_n[0][0] + s_n[0][1] + s_n[0][2] + s_n[0][3];
         valid = s_n[1][0] + s_n[1][1] + s_n[1][2] + s_n[1][3];
     }
-    if (t >= a.T) return;
     const Seqs sl{staged ? s_off : a.off, a.S, a.T};
-    const int s = sl.find((int)t), t0 = sl.begin(s), t1 = sl.end(s);
-    float d[N];
+    for (int64_t t = (int64_t)blockIdx.x * NG + g; t < a.T; t += (int64_t)gridDim.x * NG) {
+        const int s = sl.find((int)t), t0 = sl.begin(s), t1 = sl.end(s);
+        float d[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) d[i] = 0.f;
-    if (t >= t0 && t < t1) {
-        const bool sig = a.scoring == MOE_SCORING_SIGMOID;
-        float l[N], v[N], sc[N], om[N], shift;   // om: 1 - s for the sigmoid, 1 for softmax
-        load_row<L, Q, VEC>(a.logits + t * a.E, a.E, sub, -INFINITY, l);
-        int id0 = -1, c[N];     // everything else the row needs is requested now as well
-        float dw0 = 0.f;
-        if (a.dw && sub < a.k) {
-            id0 = a.ids[t * a.k + sub];
-            dw0 = a.dw[t * a.k + sub];
-        }
-        if (a.counts) load_row<L, Q, VEC>(a.counts + (int64_t)s * a.E, a.E, sub, 0, c);
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = l[i];
-        float sum = 0.f;
-        if (!sig || a.cz != 0.f) sum = softmax_row<L, Q>(v, shift);
-        const float inv = rcp_or_0(sum);
-        float pinv = inv;
-        if (sig) {
-            float z = 0.f;
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const float ex = exp_fast(-l[i]);
-                sc[i] = __builtin_amdgcn_rcpf(1.0f + ex);
-                om[i] = ex < INFINITY ? ex * sc[i] : 1.0f - sc[i];
-                z += sc[i];
+        for (int i = 0; i < N; ++i) d[i] = 0.f;
+        if (t >= t0 && t < t1) {
+            const bool sig = a.scoring == MOE_SCORING_SIGMOID;
+            float l[N], v[N], sc[N], om[N], shift;   // om: 1 - s for the sigmoid, 1 for softmax
+            load_row<L, Q, VEC>(a.logits + t * a.E, a.E, sub, -INFINITY, l);
+            int id0 = -1, c[N];     // everything else the row needs is requested now as well
+            float dw0 = 0.f;
+            if (a.dw && sub < a.k) {
+                id0 = a.ids[t * a.k + sub];
+                dw0 = a.dw[t * a.k + sub];
             }
-            z = rsum<L>(z);
-            pinv = rcp_or_0(z);
-        } else {
+            if (a.counts) load_row<L, Q, VEC>(a.counts + (int64_t)s * a.E, a.E, sub, 0, c);
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                sc[i] = v[i];
-                om[i] = 1.0f;
-            }
-        }
-        if (a.counts) {
-            const float rl = __builtin_amdgcn_rcpf((float)(t1 - t0));
-            const float cu = a.ca * __builtin_amdgcn_rcpf((float)live) * a.load * rl * rl;
-            float pu = 0.f;
-#pragma unroll
-            for (int i = 0; i < N; ++i) pu = fmaf(sc[i], (float)c[i], pu);
-            pu = rsum<L>(pu) * pinv;      // sum p c
-            const float f = cu * pinv;
+            for (int i = 0; i < N; ++i) v[i] = l[i];
+            float sum = 0.f;
+            if (!sig || a.cz != 0.f) sum = softmax_row<L, Q>(v, shift);
+            const float inv = rcp_or_0(sum);
+            float pinv = inv;
             if (sig) {
-#pragma unroll
-                for (int i = 0; i < N; ++i) d[i] = f * sc[i] * om[i] * ((float)c[i] - pu);
-            } else {
-#pragma unroll
-                for (int i = 0; i < N; ++i) d[i] = f * sc[i] * ((float)c[i] - pu);
-            }
-        }
-        if (a.cz != 0.f && sum != 0.f) {
-            const float cz = 2.0f * a.cz * __builtin_amdgcn_rcpf((float)valid) * (shift + log_fast(sum)) * inv;
-#pragma unroll
-            for (int i = 0; i < N; ++i) d[i] = fmaf(cz, v[i], d[i]);
-        }
-        if (a.dw) {
-            // D and m through the row's LDS lines: lane j adds up the slots that chose the same expert as
-            // slot j, in slot order, and all of them store that sum (comparing every expert with every
-            // slot instead took 640 instructions of a row's 1100 at 256 experts and 8 slots)
-            float D[N], m[N];
-            float* dl = s_d[g];
-            float* ml = s_m[g];
-#pragma unroll
-            for (int i = 0; i < Q; ++i) {
-                *reinterpret_cast<float4*>(dl + 4 * (sub + L * i)) = make_float4(0.f, 0.f, 0.f, 0.f);
-                *reinterpret_cast<float4*>(ml + 4 * (sub + L * i)) = make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-            wave_lds_fence();
-            for (int j0 = 0; j0 < a.k; j0 += L) {
-                const int id = j0 == 0 ? id0 : j0 + sub < a.k ? a.ids[t * a.k + j0 + sub] : -1;
-                const float w = j0 == 0 ? dw0 : j0 + sub < a.k ? a.dw[t * a.k + j0 + sub] : 0.f;
-                const bool in = id >= 0 && id < a.E;
-                float sum = in ? dl[id] : 0.f, cnt = in ? ml[id] : 0.f;   // (slots of earlier rounds)
-                wave_lds_fence();
-                const int n = min(L, a.k - j0);
-                for (int j = 0; j < n; ++j) {
-                    const bool same = __shfl(id, j, L) == id;
-                    const float wj = __shfl(w, j, L);
-                    sum += same ? wj : 0.f;
-                    cnt += same ? 1.f : 0.f;
-                }
-                if (in) {
-                    dl[id] = sum;
-                    ml[id] = cnt;
-                }
-                wave_lds_fence();
-            }
-#pragma unroll
-            for (int i = 0; i < Q; ++i) {
-                const float4 x = *reinterpret_cast<const float4*>(dl + 4 * (sub + L * i));
-                const float4 y = *reinterpret_cast<const float4*>(ml + 4 * (sub + L * i));
-                D[4 * i] = x.x, D[4 * i + 1] = x.y, D[4 * i + 2] = x.z, D[4 * i + 3] = x.w;
-                m[4 * i] = y.x, m[4 * i + 1] = y.y, m[4 * i + 2] = y.z, m[4 * i + 3] = y.w;
-            }
-            if (!sig && !a.renorm) {
-                float pd = 0.f;
-#pragma unroll
-                for (int i = 0; i < N; ++i) pd = fmaf(v[i], D[i], pd);
-                pd = rsum<L>(pd) * inv;
-                const float f = a.rsf * inv;
-#pragma unroll
-                for (int i = 0; i < N; ++i) d[i] = fmaf(f * v[i], D[i] - pd, d[i]);
-            } else {
-                // Scores relative to the largest chosen one, as the forward weights are (softmax: by its
-                // logit), and exactly 1 there: a row with a single choice then has the gradient 0, not
-                // the rounding of D - D (which a small balance loss would be lost in).
-                float q[N], mx = -INFINITY, z = 0.f, qd = 0.f;
-#pragma unroll
-                for (int i = 0; i < N; ++i) mx = m[i] > 0.f ? fmaxf(mx, sig ? sc[i] : l[i]) : mx;
-                mx = rmax<L>(mx);
-                if (mx == -INFINITY) mx = 0.f;
-                const float rmx = rcp_or_0(mx);
+                float z = 0.f;
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    const float s = sig ? (sc[i] == mx && mx > 0.f ? 1.f : sc[i] * rmx) : exp_fast(l[i] - mx);
-                    q[i] = m[i] > 0.f ? s : 0.f;
-                    z = fmaf(m[i], q[i], z);
-                    qd = fmaf(q[i], D[i], qd);
+                    const float ex = exp_fast(-l[i]);
+                    sc[i] = __builtin_amdgcn_rcpf(1.0f + ex);
+                    om[i] = ex < INFINITY ? ex * sc[i] : 1.0f - sc[i];
+                    z += sc[i];
                 }
                 z = rsum<L>(z);
-                qd = rsum<L>(qd);
-                const float zi = rcp_or_0(z);
-                qd *= zi;
-                const float f = a.rsf * zi;
+                pinv = rcp_or_0(z);
+            } else {
 #pragma unroll
-                for (int i = 0; i < N; ++i) d[i] = fmaf(f * q[i] * om[i], D[i] - m[i] * qd, d[i]);
+                for (int i = 0; i < N; ++i) {
+                    sc[i] = v[i];
+                    om[i] = 1.0f;
+                }
+            }
+            if (a.counts) {
+                const float rl = __builtin_amdgcn_rcpf((float)(t1 - t0));
+                const float cu = a.ca * __builtin_amdgcn_rcpf((float)live) * a.load * rl * rl;
+                float pu = 0.f;
+#pragma unroll
+                for (int i = 0; i < N; ++i) pu = fmaf(sc[i], (float)c[i], pu);
+                pu = rsum<L>(pu) * pinv;      // sum p c
+                const float f = cu * pinv;
+                if (sig) {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) d[i] = f * sc[i] * om[i] * ((float)c[i] - pu);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) d[i] = f * sc[i] * ((float)c[i] - pu);
+                }
+            }
+            if (a.cz != 0.f && sum != 0.f) {
+                const float cz = 2.0f * a.cz * __builtin_amdgcn_rcpf((float)valid) * (shift + log_fast(sum)) * inv;
+#pragma unroll
+                for (int i = 0; i < N; ++i) d[i] = fmaf(cz, v[i], d[i]);
+            }
+            if (a.dw) {
+                // D and m through the row's LDS lines: lane j adds up the slots that chose the same expert as
+                // slot j, in slot order, and all of them store that sum (comparing every expert with every
+                // slot instead took 640 instructions of a row's 1100 at 256 experts and 8 slots)
+                float D[N], m[N];
+                float* dl = s_d[g];
+                float* ml = s_m[g];
+#pragma unroll
+                for (int i = 0; i < Q; ++i) {
+                    *reinterpret_cast<float4*>(dl + 4 * (sub + L * i)) = make_float4(0.f, 0.f, 0.f, 0.f);
+                    *reinterpret_cast<float4*>(ml + 4 * (sub + L * i)) = make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+                wave_lds_fence();
+                for (int j0 = 0; j0 < a.k; j0 += L) {
+                    const int id = j0 == 0 ? id0 : j0 + sub < a.k ? a.ids[t * a.k + j0 + sub] : -1;
+                    const float w = j0 == 0 ? dw0 : j0 + sub < a.k ? a.dw[t * a.k + j0 + sub] : 0.f;
+                    const bool in = id >= 0 && id < a.E;
+                    float sum = in ? dl[id] : 0.f, cnt = in ? ml[id] : 0.f;   // (slots of earlier rounds)
+                    wave_lds_fence();
+                    const int n = min(L, a.k - j0);
+                    for (int j = 0; j < n; ++j) {
+                        const bool same = __shfl(id, j, L) == id;
+                        const float wj = __shfl(w, j, L);
+                        sum += same ? wj : 0.f;
+                        cnt += same ? 1.f : 0.f;
+                    }
+                    if (in) {
+                        dl[id] = sum;
+                        ml[id] = cnt;
+                    }
+                    wave_lds_fence();
+                }
+#pragma unroll
+                for (int i = 0; i < Q; ++i) {
+                    const float4 x = *reinterpret_cast<const float4*>(dl + 4 * (sub + L * i));
+                    const float4 y = *reinterpret_cast<const float4*>(ml + 4 * (sub + L * i));
+                    D[4 * i] = x.x, D[4 * i + 1] = x.y, D[4 * i + 2] = x.z, D[4 * i + 3] = x.w;
+                    m[4 * i] = y.x, m[4 * i + 1] = y.y, m[4 * i + 2] = y.z, m[4 * i + 3] = y.w;
+                }
+                if (!sig && !a.renorm) {
+                    float pd = 0.f;
+#pragma unroll
+                    for (int i = 0; i < N; ++i) pd = fmaf(v[i], D[i], pd);
+                    pd = rsum<L>(pd) * inv;
+                    const float f = a.rsf * inv;
+#pragma unroll
+                    for (int i = 0; i < N; ++i) d[i] = fmaf(f * v[i], D[i] - pd, d[i]);
+                } else {
+                    // Scores relative to the largest chosen one, as the forward weights are (softmax: by its
+                    // logit), and exactly 1 there: a row with a single choice then has the gradient 0, not
+                    // the rounding of D - D (which a small balance loss would be lost in).
+                    float q[N], mx = -INFINITY, z = 0.f, qd = 0.f;
+#pragma unroll
+                    for (int i = 0; i < N; ++i) mx = m[i] > 0.f ? fmaxf(mx, sig ? sc[i] : l[i]) : mx;
+                    mx = rmax<L>(mx);
+                    if (mx == -INFINITY) mx = 0.f;
+                    const float rmx = rcp_or_0(mx);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        const float s = sig ? (sc[i] == mx && mx > 0.f ? 1.f : sc[i] * rmx) : exp_fast(l[i] - mx);
+                        q[i] = m[i] > 0.f ? s : 0.f;
+                        z = fmaf(m[i], q[i], z);
+                        qd = fmaf(q[i], D[i], qd);
+                    }
+                    z = rsum<L>(z);
+                    qd = rsum<L>(qd);
+                    const float zi = rcp_or_0(z);
+                    qd *= zi;
+                    const float f = a.rsf * zi;
+#pragma unroll
+                    for (int i = 0; i < N; ++i) d[i] = fmaf(f * q[i] * om[i], D[i] - m[i] * qd, d[i]);
+                }
             }
         }
-    }
-    float* o = a.dlogits + t * a.E;
+        float* o = a.dlogits + t * a.E;
 #pragma unroll
-    for (int i = 0; i < Q; ++i) {
-        const int e = 4 * (sub + L * i);
-        if constexpr (VEC) {
-            if (e < a.E) *reinterpret_cast<float4*>(o + e) = make_float4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]);
-        } else {
+        for (int i = 0; i < Q; ++i) {
+            const int e = 4 * (sub + L * i);
+            if constexpr (VEC) {
+                if (e < a.E) *reinterpret_cast<float4*>(o + e) = make_float4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]);
+            } else {
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                if (e + c < a.E) o[e + c] = d[4 * i + c];
+                for (int c = 0; c < 4; ++c)
+                    if (e + c < a.E) o[e + c] = d[4 * i + c];
+            }
         }
     }
 }
@@ -556,7 +556,8 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouteBwdArgs a) {
 hipError_t launch_route_backward(const RouteBwdArgs& a, hipStream_t st) {
     const bool v = vec4(a.logits, a.E) && vec4(a.dlogits, a.E) && (!a.counts || vec4(a.counts, a.E));
 #define MOE_CALL(L, Q, V) \
-    hipLaunchKernelGGL((k_route_bwd<L, Q, V>), dim3((unsigned)ceil_div(a.T, 256 / L)), dim3(256), 0, st, a)
+    hipLaunchKernelGGL((k_route_bwd<L, Q, V>), dim3((unsigned)ceil_div(std::min<int64_t>(a.T, launch_rows(L)), 256 / L)), \
+                       dim3(256), 0, st, a)
     MOE_ROW_DISPATCH(a.E, v, MOE_CALL);
 #undef MOE_CALL
     return hipGetLastError();
@@ -575,7 +576,7 @@ typedef unsigned v4u_t __attribute__((ext_vector_type(4)));
 constexpr int kClearMost = 256, kClearRows = 1 << 16;   // workgroups, rows of one
 template <bool BF16, int NT>
 __device__ __forceinline__ void clear_rows(const CombineBwdArgs& a, int per, uint32_t* s_bits) {
-    const int tid = threadIdx.x, A = a.T * a.k;
+    const int tid = threadIdx.x, A = a.rows;
     const int lo = blockIdx.x * per, n = min(per, A - lo);
     for (int i = tid; i < (per + 31) / 32; i += NT) s_bits[i] = 0;
     __syncthreads();
@@ -614,11 +615,11 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_combine_bwd(CombineBwdArg
         if (blockIdx.x < nclear) return clear_rows<BF16, G * RPB>(a, per, s_bits);   // (uniform)
     }
     const int sub = threadIdx.x % G, r = threadIdx.x / G;
-    const int64_t tt = (int64_t)(blockIdx.x - nclear) * RPB + r;
+    const int64_t tt = (int64_t)(blockIdx.x - (DOUT ? nclear : 0)) * RPB + r;
     const bool on = tt < a.T;           // (the barriers below are for every thread)
     const int64_t t = on ? tt : a.T - 1;
     const int nv = on ? a.H / CW : 0;
-    const int64_t A = (int64_t)a.T * a.k;
+    const int A = a.rows;
     for (int j0 = 0; j0 < a.k; j0 += 8) {
         int64_t p[8];
         float wj[8], dot[8];
@@ -707,9 +708,10 @@ __global__ __launch_bounds__(256) void k_zero(v4u_t* p, int64_t n) {
 }
 
 template <bool BF16, int G>
-static void run_combine_bwd(const CombineBwdArgs& a, hipStream_t st) {
+static void run_combine_bwd(const CombineBwdArgs& args, hipStream_t st) {
     constexpr int RPB = G < 256 ? 256 / G : 1;
-    const int64_t A = (int64_t)a.T * a.k;
+    CombineBwdArgs a = args;
+    const int64_t A = a.rows;
     int nclear = 0, per = 0;
     // In the kernel itself (16384 x 8 x 4096 bf16: 434 us, without clearing 431, zeros first 596; 32 x 8 x 2816:
     // 5.6, 5.6 and 7.4), but zeros first where reading all entries 256 times takes longer than writing the rows
@@ -720,9 +722,17 @@ static void run_combine_bwd(const CombineBwdArgs& a, hipStream_t st) {
     } else if (a.clear) {
         hipLaunchKernelGGL(k_zero, dim3(2048), dim3(256), 0, st, static_cast<v4u_t*>(a.deo), A * a.H / (BF16 ? 8 : 4));
     }
-    const dim3 grid((unsigned)ceil_div(a.T, RPB) + nclear), block(G * RPB);
-    if (a.deo) hipLaunchKernelGGL((k_combine_bwd<BF16, G, true>), grid, block, 0, st, a, nclear, per);
-    else hipLaunchKernelGGL((k_combine_bwd<BF16, G, false>), grid, block, 0, st, a, 0, 0);
+    for (int64_t t = 0; t < args.T; t += launch_rows(G)) {
+        a.T = (int)std::min<int64_t>(args.T - t, launch_rows(G));
+        a.dy = args.dy + t * a.H;
+        a.pos = args.pos + t * a.k;
+        if (args.wt) a.wt = args.wt + t * a.k;
+        if (args.dwt) a.dwt = args.dwt + t * a.k;
+        const dim3 grid((unsigned)ceil_div(a.T, RPB) + nclear), block(G * RPB);
+        if (a.deo) hipLaunchKernelGGL((k_combine_bwd<BF16, G, true>), grid, block, 0, st, a, nclear, per);
+        else hipLaunchKernelGGL((k_combine_bwd<BF16, G, false>), grid, block, 0, st, a, 0, 0);
+        nclear = 0;   // (the first launch reads all entries)
+    }
 }
 
 // Threads per token, by its nv vectors.  Few tokens: as many as there are vectors, one round of loads

@@ -37,6 +37,10 @@ __device__ __forceinline__ float sum16(float v) {
     return v;
 }
 
+// HIP takes fewer than 2^32 threads in a launch: operators with a fixed number of threads per row launch
+// this many rows at a time.
+constexpr int64_t launch_rows(int threads_per_row) { return ((int64_t)1 << 31) / threads_per_row; }
+
 struct NormArgs {
     int T, H;
     const uint16_t* x;
@@ -113,6 +117,7 @@ hipError_t launch_route_backward(const RouteBwdArgs& a, hipStream_t st);
 
 struct CombineBwdArgs {
     int T, k, H, bf16;
+    int rows;             // T * k of the whole call (below 2^29)
     const uint16_t* dy;
     const void* eo;       // or NULL with dwt NULL
     const int32_t* pos;

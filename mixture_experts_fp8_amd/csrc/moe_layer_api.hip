@@ -70,8 +70,9 @@ int moe_route_backward(const moe_route_backward_args* a) {
 
 int moe_combine_backward(const moe_combine_backward_args* a) {
     if (int rc = moe::host::check_combine_backward(a)) return rc;
-    const moe::CombineBwdArgs c{a->T, a->k, a->H, a->dtype == MOE_DTYPE_BF16, a->dy, a->expert_out, a->assign_pos,
-                                a->topk_weights, a->dtopk_weights, a->dexpert_out, a->dexpert_out && a->clear_rows};
+    const moe::CombineBwdArgs c{a->T, a->k, a->H, a->dtype == MOE_DTYPE_BF16, a->T * a->k, a->dy,
+                                a->expert_out, a->assign_pos, a->topk_weights, a->dtopk_weights, a->dexpert_out,
+                                a->dexpert_out && a->clear_rows};
     return done("moe_combine_backward", moe::launch_combine_backward(c, static_cast<hipStream_t>(a->stream)));
 }
 

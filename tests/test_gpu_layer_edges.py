@@ -146,3 +146,48 @@ def test_combine_handle_with_changing_assignments_in_a_graph():
         assert torch.equal(call.out["d_expert_out"], _rows_of(p, T, k, H, w, dy, eo.dtype)), share
         M.moe_combine_backward(dy, eo, pos, w)
         torch.cuda.synchronize()
+
+
+# ---- more rows than one launch of a thread group per row may hold ------------------------------
+def test_more_rows_than_one_launch():
+    """HIP refuses a launch of 2^32 threads: a wave per row of 8 columns comes to that at 2^26 rows."""
+    H, T = 8, (1 << 26) + 3
+    pick = torch.tensor([0, 1, (1 << 25) - 1, 1 << 25, (1 << 25) + 1, (1 << 26) - 1, 1 << 26, T - 1], device=DEV)
+    x = torch.randn(T, H, device=DEV, dtype=torch.bfloat16)
+    w, _ = f32(1 + 0.1 * rng(34).standard_normal(H))
+    print("norm", flush=True)
+    out = M.moe_add_rmsnorm(x, w, 1e-6, residual=x)
+    few = M.moe_add_rmsnorm(x[pick].contiguous(), w, 1e-6, residual=x[pick].contiguous())
+    assert torch.equal(out["y"][pick], few["y"]) and torch.equal(out["h"][pick], few["h"])
+    assert torch.equal(out["h"], x + x) and torch.isfinite(out["y"]).all()
+    del out
+    print("norm backward", flush=True)
+    d = M.moe_add_rmsnorm_backward(x, x, w, 1e-6, want_dweight=False)["dx"]
+    assert torch.equal(d[pick], M.moe_add_rmsnorm_backward(x[pick].contiguous(), x[pick].contiguous(), w, 1e-6, want_dweight=False)["dx"])
+    del d
+    print("combine", flush=True)
+    pos = torch.arange(T - 1, -1, -1, dtype=torch.int32, device=DEV)
+    cw = torch.rand(T, 1, device=DEV)
+    c = M.moe_combine_backward(x, x, pos, cw, d_expert_out=True)
+    assert torch.equal(c["d_expert_out"], (cw * x.float()).to(torch.bfloat16).flip(0))
+    dots = (x[pick].double() * x.flip(0)[pick].double()).sum(1)
+    mag = (x[pick].double() * x.flip(0)[pick].double()).abs().sum(1)
+    within(host(c["dweights"][pick, 0]), host(dots), 40 * U * host(mag))
+    pos[5] = -1
+    c = M.moe_combine_backward(x, x, pos, cw, d_expert_out=True)
+    assert (c["d_expert_out"][T - 6] == 0).all() and c["dweights"][5, 0] == 0
+
+
+def test_more_router_rows_than_one_launch():
+    """16 lanes per row: 2^32 threads at 2^28 rows."""
+    T, E, k = (1 << 28) + 5, 2, 1
+    l = torch.randn(T, E, device=DEV)
+    pick = torch.tensor([0, 15, 16, (1 << 27) - 1, 1 << 27, (1 << 28) - 1, 1 << 28, T - 1], device=DEV)
+    p = GL._params(E, k, "softmax", True)
+    d = M.moe_route_backward(p, l, None, None, None, None, 0.0, 1.0)
+    sub = l[pick].double()
+    lse = torch.logsumexp(sub, 1, keepdim=True)
+    want = 2.0 / T * lse * torch.softmax(sub, 1)
+    assert ((d[pick].double() - want).abs() <= 1e-5 * want.abs() + 1e-13).all()
+    del l
+    assert torch.isfinite(d).all() and (d != 0).any(1).float().mean() > 0.999
