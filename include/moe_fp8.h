@@ -391,7 +391,8 @@ int moe_fused_static(const moe_fused_args* a);
  * number formats, and the gradients that train its router.  The conventions at the top of this
  * file hold for all of them; in addition:
  *   - outputs must not overlap each other, nor an input, except where an in-place use is named;
- *   - a NULL optional output is not computed. */
+ *   - a NULL optional output is not computed;
+ *   - float32 and int32 buffers are 4-byte aligned where nothing more is asked for. */
 
 /* moe_add_rmsnorm: h = bf16_RNE(x + residual) (h = x without a residual),
  *   y = bf16_RNE(h * r * weight),  r = 1 / sqrt(mean_c h[t, c]^2 + eps),

@@ -75,6 +75,13 @@ int check_io(const char* op, const Span& out, const Span& in, bool same = false)
     return MOE_OK;
 }
 
+// buffers of 4-byte elements start at one
+int check_words(const char* op, const Span* s, int n) {
+    for (int i = 0; i < n; ++i)
+        if (!aligned(s[i].p, 4)) return fail(MOE_ERR_INVALID, "%s: %s must be 4-byte aligned", op, s[i].name);
+    return MOE_OK;
+}
+
 // bytes of a [rows, cols] matrix with rows ld elements apart
 uint64_t span2(int64_t rows, int64_t cols, int64_t ld, int size) {
     return ((uint64_t)(rows - 1) * (uint64_t)ld + (uint64_t)cols) * size;
@@ -260,6 +267,7 @@ int check_balance_loss(const moe_balance_loss_args* a) {
     const Span in[3] = {{"router_logits", a->router_logits, (uint64_t)T * E * 4},
                         {"topk_ids", a->topk_ids, (uint64_t)T * k * 4},
                         {"seq_offsets", a->seq_offsets, (uint64_t)(S + 1) * 4}};
+    if ((rc = check_words(op, out, 3)) || (rc = check_words(op, in, 3))) return rc;
     if ((rc = check_outputs(op, out, 4))) return rc;
     for (int i = 0; i < 4; ++i)
         for (int j = 0; j < 3; ++j)
@@ -283,6 +291,7 @@ int check_route_backward(const moe_route_backward_args* a) {
                         {"dtopk_weights", a->dtopk_weights, (uint64_t)T * k * 4},
                         {"counts", a->counts, (uint64_t)S * E * 4},
                         {"seq_offsets", a->seq_offsets, (uint64_t)(S + 1) * 4}};
+    if ((rc = check_words(op, &out, 1)) || (rc = check_words(op, in, 5))) return rc;
     for (int j = 0; j < 5; ++j)
         if ((rc = check_io(op, out, in[j], j == 0))) return rc;
     return MOE_OK;
@@ -311,6 +320,8 @@ int check_combine_backward(const moe_combine_backward_args* a) {
     const Span out[2] = {{"dtopk_weights", a->dtopk_weights, nk}, {"dexpert_out", a->dexpert_out, ne}};
     const Span in[4] = {{"dy", a->dy, (uint64_t)T * H * 2}, {"expert_out", a->expert_out, ne},
                         {"assign_pos", a->assign_pos, nk}, {"topk_weights", a->topk_weights, nk}};
+    if (int rc = check_words(op, out, 1)) return rc;
+    if (int rc = check_words(op, in + 2, 2)) return rc;
     if (int rc = check_outputs(op, out, 2)) return rc;
     for (int i = 0; i < 2; ++i)
         for (int j = 0; j < 4; ++j)
