@@ -370,7 +370,9 @@ hipError_t launch_balance_loss(const BalanceArgs& a, hipStream_t st) {
 // Orders the LDS accesses of a wave's own lanes (a row's lanes are in one wave).
 __device__ __forceinline__ void wave_lds_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
-template <int L, int Q, bool VEC>
+// WALK: more rows than the grid holds, a workgroup takes several (in a loop the kernel needs a third more
+// registers).
+template <int L, int Q, bool VEC, bool WALK>
 __global__ __launch_bounds__(256) void k_route_bwd(RouteBwdArgs a) {
     constexpr int NG = 256 / L, N = 4 * Q;
     __shared__ int s_off[kSeqLds + 1];
@@ -380,7 +382,9 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouteBwdArgs a) {
     const Seqs sq{a.off, a.S, a.T};
     const bool staged = a.off && a.S <= kSeqLds;
     int live = 1, valid = a.T;
-    if (a.off) {
+    if (a.off && !staged && !a.counts) {   // (live is the balance loss's alone)
+        valid = max(sq.at(a.S) - sq.begin(0), 0);
+    } else if (a.off) {
         live = valid = 0;
         for (int i = tid; i < a.S; i += 256) {
             const int b = sq.begin(i), len = sq.end(i) - b;
@@ -550,14 +554,22 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouteBwdArgs a) {
                     if (e + c < a.E) o[e + c] = d[4 * i + c];
             }
         }
+        if constexpr (!WALK) break;
     }
 }
 
 hipError_t launch_route_backward(const RouteBwdArgs& a, hipStream_t st) {
     const bool v = vec4(a.logits, a.E) && vec4(a.dlogits, a.E) && (!a.counts || vec4(a.counts, a.E));
-#define MOE_CALL(L, Q, V) \
-    hipLaunchKernelGGL((k_route_bwd<L, Q, V>), dim3((unsigned)ceil_div(std::min<int64_t>(a.T, launch_rows(L)), 256 / L)), \
-                       dim3(256), 0, st, a)
+    // With counts every workgroup reads all boundaries for the number of sequences that have rows; beyond those
+    // that LDS holds, no more workgroups than stay resident, each with more rows (2^20 rows of 8 logits, a sequence
+    // each: 2.5 ms, one workgroup for every 16 rows 33.9; 131072 x 64 in 30000: 87 us and 134).
+    const int64_t most = a.off && a.counts && a.S > kSeqLds ? 2048 : launch_rows(256);
+#define MOE_CALL(L, Q, V)                                                                                       \
+    do {                                                                                                        \
+        const int64_t n = ceil_div(a.T, 256 / L);                                                               \
+        if (n > most) hipLaunchKernelGGL((k_route_bwd<L, Q, V, true>), dim3((unsigned)most), dim3(256), 0, st, a); \
+        else hipLaunchKernelGGL((k_route_bwd<L, Q, V, false>), dim3((unsigned)n), dim3(256), 0, st, a);         \
+    } while (0)
     MOE_ROW_DISPATCH(a.E, v, MOE_CALL);
 #undef MOE_CALL
     return hipGetLastError();

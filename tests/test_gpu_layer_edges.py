@@ -191,3 +191,53 @@ def test_more_router_rows_than_one_launch():
     assert ((d[pick].double() - want).abs() <= 1e-5 * want.abs() + 1e-13).all()
     del l
     assert torch.isfinite(d).all() and (d != 0).any(1).float().mean() > 0.999
+
+
+# ---- very many sequences -----------------------------------------------------------------------
+def _us(f, n=3):
+    best = float("inf")
+    for _ in range(n):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        f()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b) * 1e3)
+    return best
+
+
+@pytest.mark.parametrize("E", [8, 300])
+def test_route_backward_with_very_many_sequences(E):
+    """A sequence per row, up to the limit: right, and not a walk over all boundaries for every 16 rows."""
+    T, k = 1 << (20 if E == 8 else 16), 2
+    l, lf, ids, idn, dw, dwf = GL._router_inputs(T, E, k, 21)
+    off = torch.arange(T + 1, dtype=torch.int32, device=DEV)
+    p = GL._params(E, k, "softmax", True, 1.3)
+    counts = torch.zeros(T, E, dtype=torch.int32, device=DEV).scatter_(1, ids.long(), 1)
+    d = M.moe_route_backward(p, l, ids, dw, counts, off, 0.5, 0.1)
+    s = torch.softmax(l.double(), 1)
+    u = 0.5 / T * E / k * counts.double()
+    want = s * (u - (s * u).sum(1, keepdim=True)) + 0.2 / T * torch.logsumexp(l.double(), 1, keepdim=True) * s
+    mag = s * (u + (s * u).sum(1, keepdim=True)) + 0.2 / T * torch.logsumexp(l.double(), 1, keepdim=True).abs() * s
+    q = torch.softmax(torch.gather(l.double(), 1, ids.long()), 1)
+    want = want.scatter_add(1, ids.long(), 1.3 * q * (dw.double() - (q * dw.double()).sum(1, keepdim=True)))
+    mag = mag.scatter_add(1, ids.long(), 1.3 * q * (dw.double().abs() + (q * dw.double().abs()).sum(1, keepdim=True)))
+    R = float(l.max() - l.min())
+    within(host(d), host(want), (4 * (R + 40) + 128) * U * host(mag) + 1e-12)
+    only = M.MoeRouteBackward(p, l, ids, dw, None, off, 0.0, 0.0)
+    full = M.MoeRouteBackward(p, l, ids, dw, counts, off, 0.5, 0.1)
+    one = M.MoeRouteBackward(p, l, ids, dw, None, None, 0.0, 0.0)
+    only(), full(), one()
+    t = [_us(only), _us(full), _us(one)]
+    print("weights alone, everything, one sequence: %.0f %.0f %.0f us" % tuple(t), flush=True)
+    assert t[0] < 10 * t[2] + 200 and t[1] < 5000
+
+
+@pytest.mark.parametrize("S", [1024, 1025, 3000])
+def test_route_backward_sequences_around_the_table(S):
+    """Boundaries held in LDS and searched in memory; uneven lengths, empty sequences, rows outside."""
+    T = 9000
+    g = rng(35, S)
+    off = np.sort(g.integers(3, T - 40, S + 1))
+    off[10:30] = off[10]
+    GL.test_balance_loss_and_route_backward(T, 24, 3, "softmax", True, 1.5, [int(o) for o in off])
