@@ -585,10 +585,6 @@ static hipError_t run_tile_t(const LinArgs& a, hipStream_t st) {
                        (MX ? 3 * ROWS * 4 : (size_t)KB * ROWS + (KB * ((COLS + 127) / 128) + 15) / 16 * 16);
     return launch_tiles<k_linear_tile<MX, MI, NJ, WM, WN>>(a, tm, tn, 64 * WM * WN, lds, st);
 }
-template <int MI, int NJ, int WM, int WN>
-static hipError_t run_tile(const LinArgs& a, hipStream_t st) {
-    return a.mx ? run_tile_t<true, MI, NJ, WM, WN>(a, st) : run_tile_t<false, MI, NJ, WM, WN>(a, st);
-}
 
 // ----------------------------------------------------------------------------------------
 // The same product where there are too few tiles to hide a K block's latency behind another workgroup:
@@ -771,7 +767,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 1) void k_linear_deep(LinArgs a,
 }
 
 // LDS of a deep tile: stages, bias, the 128-element scales of all K blocks.
-static size_t deep_lds(bool mx, int rows, int cols, int stages, int KB) {
+static constexpr size_t deep_lds(bool mx, int rows, int cols, int stages, int KB) {
     return (size_t)stages * (rows + cols) * (kGroup + (mx ? 4 : 0)) + cols * 4 +
            (mx ? 0 : (size_t)KB * rows + (KB * ((cols + 127) / 128) + 15) / 16 * 16);
 }
@@ -827,11 +823,13 @@ hipError_t launch_linear(const LinArgs& args, hipStream_t st) {
     if (fits(64, 128, 256)) return run_deep<2, 4, 2, 2, 4, 1>(a, st);
     if (fits(64, 128, 512) || a.T <= 64) return run_deep<2, 4, 2, 2, 3, 1>(a, st);
     if (fits(128, 256, 256)) {
-        if ((a.mx || !fits(128, 256, 208)) && deep_lds(a.mx, 128, 256, 3, a.K / kGroup) <= kLdsBytes)
-            return run_deep<4, 4, 2, 4, 3, 1>(a, st);
-        return run_tile<4, 4, 1, 4>(a, st);
+        static_assert(deep_lds(true, 128, 256, 3, 1) <= kLdsBytes, "for every K: the scales are in the stages");
+        if (a.mx) return run_deep_t<true, 4, 4, 2, 4, 3, 1>(a, st);
+        if (!fits(128, 256, 208) && deep_lds(false, 128, 256, 3, a.K / kGroup) <= kLdsBytes)
+            return run_deep_t<false, 4, 4, 2, 4, 3, 1>(a, st);
+        return run_tile_t<false, 4, 4, 1, 4>(a, st);
     }
-    return run_tile<8, 4, 1, 4>(a, st);
+    return a.mx ? run_tile_t<true, 8, 4, 1, 4>(a, st) : run_tile_t<false, 8, 4, 1, 4>(a, st);
 }
 
 }  // namespace moe
