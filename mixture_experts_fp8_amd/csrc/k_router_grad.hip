@@ -585,7 +585,7 @@ typedef unsigned v4u_t __attribute__((ext_vector_type(4)));
 // Rows that no assignment names: each of the first nclear workgroups takes `per` rows, marks in LDS
 // those that an entry of pos names (all entries pass by, from the caches) and writes zeros to the others:
 // no launch, workspace or atomic in memory of its own.
-constexpr int kClearMost = 256, kClearRows = 1 << 16;   // workgroups, rows of one
+constexpr int kClearMost = 128, kClearRows = 1 << 17;   // workgroups, rows of one
 template <bool BF16, int NT>
 __device__ __forceinline__ void clear_rows(const CombineBwdArgs& a, int per, uint32_t* s_bits) {
     const int tid = threadIdx.x, A = a.rows;
@@ -725,10 +725,12 @@ static void run_combine_bwd(const CombineBwdArgs& args, hipStream_t st) {
     CombineBwdArgs a = args;
     const int64_t A = a.rows;
     int nclear = 0, per = 0;
-    // In the kernel itself (16384 x 8 x 4096 bf16: 434 us, without clearing 431, zeros first 596; 32 x 8 x 2816:
-    // 5.6, 5.6 and 7.4), but zeros first where reading all entries 256 times takes longer than writing the rows
-    // (65536 x 8 x 64 bf16: 139 us, in the kernel 157; x 256: 194 and 190) or LDS holds too few marks.
-    if (a.clear && A <= (int64_t)kClearMost * kClearRows && (A <= (1 << 16) || a.H * (BF16 ? 2 : 4) >= 256)) {
+    // In the kernel itself (16384 x 8 x 4096 bf16 over three sets of inputs: 457 us, without clearing 455, a fill
+    // before it 598 to 432 on one set; 32 x 8 x 2816: 5.6, 5.7 and 7.5; with 256 workgroups 461, with 64 456 but 326
+    // instead of 313 where seven of eight are dropped).  Zeros first where reading all entries 128 times takes
+    // longer than writing the rows (16384 x 8 x 128 bf16: 42 us, in the kernel 46; 65536 x 8 x 256: 191 and 187) or
+    // LDS holds too few marks.
+    if (a.clear && A <= (int64_t)kClearMost * kClearRows && (A <= (1 << 16) || a.H * (BF16 ? 2 : 4) >= 512)) {
         per = (int)std::max<int64_t>(64, ceil_div(A, kClearMost));
         nclear = (int)ceil_div(A, per);
     } else if (a.clear) {
