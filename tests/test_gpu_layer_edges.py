@@ -40,6 +40,34 @@ def test_add_rmsnorm_infinite_weights(H, quant):
         assert torch.equal(out["yq"], q) and torch.equal(out["ys"], s)
 
 
+# Matrices of 32 MiB and more go past the caches, by kernels of their own.
+@pytest.mark.parametrize("T,H,quant,residual", [(4097, 4104, None, True), (2400, 7168, "mxfp8", True), (2341, 7168, "fp8", False),
+                                                (33000, 512, "fp8", True), (8200, 2048, "mxfp8", True), (1025, 16384, None, True),
+                                                (513, 32768, "fp8", True)])
+def test_add_rmsnorm_streamed(T, H, quant, residual):
+    x, xf, r, rf, w, wf = GL._norm_inputs(T, H, 5)
+    out = M.moe_add_rmsnorm(x, w, 1e-6, residual=r if residual else None, quant=None if quant is None else M.QUANT_SCHEMES[quant])
+    h, y = OL.add_rmsnorm(xf, rf if residual else None, wf, 1e-6)
+    if residual:
+        assert np.array_equal(host(out["h"]), h)
+    # (bounds as in test_add_rmsnorm)
+    near = bf16_rne(y * (1 + 2.0 ** -30)) != bf16_rne(y * (1 - 2.0 ** -30))
+    assert np.array_equal(host(out["y"])[~near], bf16_rne(y)[~near]) and near.mean() < 1e-4
+    if quant:
+        q, s = M.moe_quant_act(out["y"]) if quant == "fp8" else M.moe_quant_act_mx(out["y"])
+        assert torch.equal(out["yq"], q) and torch.equal(out["ys"], s)
+    # the last rows alone, by the kernels of small matrices: the same bits
+    few = M.moe_add_rmsnorm(x[-3:], w, 1e-6, residual=r[-3:] if residual else None)
+    assert torch.equal(few["y"], out["y"][-3:])
+
+
+# Several rows per workgroup in every kernel, both numbers of workgroups, and streamed matrices.
+@pytest.mark.parametrize("T,H", [(700, 1544), (700, 2816), (600, 7168), (4500, 1544), (33000, 40), (33000, 512), (2600, 1000),
+                                 (4200, 4096), (2400, 7168), (8300, 2048), (1100, 16384), (600, 32768), (17000, 1024)])
+def test_add_rmsnorm_backward_many_rows(T, H):
+    GL.test_add_rmsnorm_backward(T, H, T % 3 != 0)
+
+
 # ---- linear -------------------------------------------------------------------------------
 def _tail(name, v):
     """The activation in 64 bits without the cancellation of 1 + erf(v / sqrt 2) and 1 + tanh u."""
@@ -146,6 +174,11 @@ def test_combine_handle_with_changing_assignments_in_a_graph():
         assert torch.equal(call.out["d_expert_out"], _rows_of(p, T, k, H, w, dy, eo.dtype)), share
         M.moe_combine_backward(dy, eo, pos, w)
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("T,k,H,dtype", [(4099, 2, 1032, "bf16"), (4100, 1, 264, "f32"), (1025, 2, 1100 * 8, "bf16"), (200, 3, 2064, "f32")])
+def test_combine_backward_variants(T, k, H, dtype):
+    GL.test_combine_backward(T, k, H, dtype)
 
 
 # ---- more rows than one launch of a thread group per row may hold ------------------------------
