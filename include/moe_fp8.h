@@ -547,6 +547,9 @@ size_t moe_balance_loss_workspace_size(int32_t T, int32_t E, int32_t num_seqs);
  *     assignments: they are not among those that the weights are normalised over;
  *   - the losses of moe_balance_loss, from its counts (NULL: none, then seq_offsets only marks
  *     the rows).  z_coef needs no counts.
+ * The weights are those of router logits.  moe_route's gate prelude does not give out its logits: a
+ * router that is trained forms them itself, and where its weights were multiplied by
+ * per_expert_scale[id], so is dtopk_weights before this call (softmax with renormalize).
  * Rows outside the sequences get a zero gradient; their logits, ids and dtopk_weights are not
  * read.  dlogits may be router_logits itself.  Deterministic. */
 typedef struct moe_route_backward_args {
@@ -565,7 +568,9 @@ int moe_route_backward(const moe_route_backward_args* a);
 
 /* moe_combine_backward: gradients of moe_combine, from dy [T, H] bf16:
  *   dtopk_weights[t, j]             = sum_c dy[t, c] * expert_out[assign_pos[t*k+j], c]   (float32)
- *   dexpert_out[assign_pos[t*k+j]]  = topk_weights[t, j] * dy[t]     (dtype, rounded once)
+ *   dexpert_out[assign_pos[t*k+j]]  = topk_weights[t, j] * dy[t]     (a float32 product, then
+ *                                     rounded to dtype: in bf16 a product beside the middle of two
+ *                                     values, one in about 10^5, may go to the farther one)
  * Either output may be NULL (then expert_out, or topk_weights, may be too).  Entries of
  * assign_pos outside [0, T*k) are dropped assignments: their weight gradient is 0.  Rows of
  * dexpert_out that no entry names are left as they were, or set to 0 with clear_rows, which a
