@@ -274,3 +274,21 @@ def test_route_backward_sequences_around_the_table(S):
     off = np.sort(g.integers(3, T - 40, S + 1))
     off[10:30] = off[10]
     GL.test_balance_loss_and_route_backward(T, 24, 3, "softmax", True, 1.5, [int(o) for o in off])
+
+
+@pytest.mark.parametrize("T,E,k,scoring", [(40000, 60, 4, "softmax"), (40000, 67, 3, "sigmoid"), (33000, 128, 8, "softmax"),
+                                           (33000, 130, 8, "sigmoid"), (33000, 256, 20, "softmax"), (8300, 260, 5, "softmax"),
+                                           (8300, 513, 70, "sigmoid"), (8300, 1001, 12, "softmax"), (8300, 1024, 8, "sigmoid")])
+def test_route_backward_rows_in_turn(T, E, k, scoring):
+    """Workgroups that take several rows (more sequences than LDS holds, and counts): the same bits as one row
+    each, which the same boundaries take without the empty sequences behind them."""
+    l, _, ids, _, dw, _ = GL._router_inputs(T, E, k, 22)
+    off = np.sort(rng(36, T, E).integers(0, T + 1, 1025)).astype(np.int32)
+    more = np.concatenate([off, np.full(200, off[-1], dtype=np.int32)])
+    p = GL._params(E, k, scoring, True, 0.8)
+    few = M.moe_balance_loss(p, l, ids, torch.from_numpy(off).to(DEV), 0.3, 0.02)
+    many = M.moe_balance_loss(p, l, ids, torch.from_numpy(more).to(DEV), 0.3, 0.02)
+    assert torch.equal(many["counts"][:1024], few["counts"]) and (many["counts"][1024:] == 0).all()
+    a = M.moe_route_backward(p, l, ids, dw, few["counts"], torch.from_numpy(off).to(DEV), 0.3, 0.02)
+    b = M.moe_route_backward(p, l, ids, dw, many["counts"], torch.from_numpy(more).to(DEV), 0.3, 0.02)
+    assert torch.equal(a, b) and (a != 0).any()
