@@ -185,16 +185,17 @@ __global__ __launch_bounds__(64 * WK) void k_linear_stream(LinArgs a) {
 // accumulator holds row l % 16 of a fragment and four consecutive columns, 4 (l / 16) ...: the
 // epilogue then works on whole vectors of a row, without LDS.
 //   * Activations: every row fragment is read by WN waves, so they go through LDS, three stages of
-//     one K block, filled by LDS-DMA two blocks ahead.  A row's 16-byte chunks stand at
-//     slot ^ (row % 8), where chunk c has slot c (32-element scales) or c / 2 + 4 (c % 2): a lane
-//     needs slots l / 16 and l / 16 + 4 in both cases, without bank conflicts.
+//     one K block, filled by LDS-DMA: block kb + 2's copies are issued in block kb and waited for at its
+//     end, with everything else (two workgroups share a CU, and one computes while the other waits).  A
+//     row's 16-byte chunks stand at slot ^ (row % 8), where chunk c has slot c (32-element scales) or
+//     c / 2 + 4 (c % 2): a lane needs slots l / 16 and l / 16 + 4 in both cases, without bank conflicts.
 //   * Weights: a fragment is read by WM waves only, and its packed order is the operand's, so it goes
 //     straight to registers one block ahead: staging it too would make the LDS the bound (two waves
 //     per SIMD read 24 KB of operands per 32 instructions otherwise).
 //   * The first row fragments of block kb + 1 are read during block kb, so that matrix instructions
 //     follow the barrier at once.
-// 16384 x 4096 x 4096 in bf16: 223 us, 2.46 PFLOP/s, the time of the library's FP8 product of this size; the
-// matrix cores bound it.  With a residual 262-267 us: its 134 MB come when the K loop is over (128 x 256 tiles
+// 16384 x 4096 x 4096 in bf16: 223-237 us with the operands (the clock moves), 2.3-2.5 PFLOP/s, as the
+// library's FP8 product of this size; the matrix cores bound it.  With a residual 262-267 us: its 134 MB come when the K loop is over (128 x 256 tiles
 // leave no registers for it before), and two workgroups per CU hide that only in part.
 __device__ __forceinline__ v4i_t make_srd(const void* base, uint32_t bytes) {
     const uint64_t b = reinterpret_cast<uint64_t>(base);
@@ -409,7 +410,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_tile(LinArgs a, int 
     int tm, tn;
     if (!tile_of(tiles_m, tiles_n, tm, tn)) return;
     // Two workgroups share a CU.  The one that was dealt second runs ahead at equal work, so that their
-    // epilogues (memory) and K loops (matrix cores) fall apart: 262 -> 258 us at 16384 x 4096 x 4096.
+    // epilogues (memory) and K loops (matrix cores) fall apart: 4 us of 267 at 16384 x 4096 x 4096.
     if (MI > 4 && ((blockIdx.x >> 8) & 1)) __builtin_amdgcn_s_setprio(1);
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wv / WN, wn = wv % WN, r16 = lane & 15, G = lane >> 4, x8 = r16 & 7;

@@ -227,9 +227,10 @@ __global__ __launch_bounds__(kRowsThreads) void k_balance_rows(BalanceArgs a, Ba
 }
 
 // One workgroup per sequence: its parts' sums in row order -> counts, mean probabilities and the
-// sequence's share of the losses.  6.3 us for 16384 x 128, 7.4 for 4096 x 256 in 9 sequences: latency, of
-// boundaries, parts, the sums through LDS and the ticket, each waiting for the one before.  A thread takes four experts of every NG-th part; with several
-// sequences the last workgroup to finish adds the shares in sequence order.
+// sequence's share of the losses.  A thread takes four experts of every NG-th part; with several sequences
+// the last workgroup to finish adds the shares in sequence order.  6.3 us for 16384 x 128, 7.4 for 4096 x 256
+// in 9 sequences: latency, of boundaries, parts, the sums through LDS and the ticket, each waiting for the
+// one before.
 __global__ __launch_bounds__(1024) void k_balance_reduce(BalanceArgs a, BalancePlan p, int c4) {
     __shared__ __align__(16) float4 s_p[1024];
     __shared__ __align__(16) int4 s_h[1024];
