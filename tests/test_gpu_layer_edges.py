@@ -263,7 +263,7 @@ def test_route_backward_with_very_many_sequences(E):
     only(), full(), one()
     t = [_us(only), _us(full), _us(one)]
     print("weights alone, everything, one sequence: %.0f %.0f %.0f us" % tuple(t), flush=True)
-    assert t[0] < 10 * t[2] + 200 and t[1] < 5000
+    assert t[0] < 10 * t[2] + 1000 and t[1] < 12000      # (one workgroup per 16 rows: 33900 us each)
 
 
 @pytest.mark.parametrize("S", [1024, 1025, 3000])
