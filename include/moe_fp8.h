@@ -454,6 +454,52 @@ typedef struct moe_add_rmsnorm_backward_args {
 int moe_add_rmsnorm_backward(const moe_add_rmsnorm_backward_args* a);
 size_t moe_add_rmsnorm_backward_workspace_size(int32_t T, int32_t H);
 
+/* moe_add_layernorm: the layer norm in the place of moe_add_rmsnorm's RMS norm,
+ *   y = bf16_RNE((h - m) * r * weight + bias),  m = mean_c h[t, c],  r = 1 / sqrt(mean_c (h[t, c] - m)^2 + eps),
+ * with everything else as there: h, the codes, sizes, alignments, in-place uses.  Formed in double and
+ * rounded once; a row of equal values has deviations of exactly 0 (y is the bias then, with eps > 0).
+ *   weight, bias  [H] float32, 16-byte aligned; bias NULL for none. */
+typedef struct moe_add_layernorm_args {
+    int32_t T, H;
+    const uint16_t* x;
+    int64_t         ld_x;
+    const uint16_t* residual;
+    int64_t         ld_residual;
+    const float*    weight;
+    const float*    bias;
+    float           eps;
+    uint16_t*       h;
+    uint16_t*       y;
+    uint8_t*        yq;
+    uint8_t*        ys;
+    int32_t         quant;
+    void*           stream;
+} moe_add_layernorm_args;
+int moe_add_layernorm(const moe_add_layernorm_args* a);
+
+/* moe_add_layernorm_backward: as moe_add_rmsnorm_backward, with xhat = (h - m) * r and g = dy * weight:
+ *   dx[t, :]   = bf16_RNE( r * (g - mean_c(g) - xhat * mean_c(g * xhat)) + dh );
+ *   dweight[c] = sum_t dy[t, c] * xhat[t, c],  dbias[c] = sum_t dy[t, c]   (float32, each optional).
+ * dx is formed in double, the two gradients' sums in float32.  Buffers as there; workspace >=
+ * moe_add_layernorm_backward_workspace_size(T, H) bytes, used for dweight and dbias only (may be NULL
+ * without both).  Deterministic. */
+typedef struct moe_add_layernorm_backward_args {
+    int32_t T, H;
+    const uint16_t* dy;
+    const uint16_t* h;
+    const float*    weight;
+    float           eps;
+    const uint16_t* dh;
+    uint16_t*       dx;
+    float*          dweight;
+    float*          dbias;
+    void*           workspace;
+    size_t          workspace_bytes;
+    void*           stream;
+} moe_add_layernorm_backward_args;
+int moe_add_layernorm_backward(const moe_add_layernorm_backward_args* a);
+size_t moe_add_layernorm_backward_workspace_size(int32_t T, int32_t H);
+
 /* Activations of moe_linear's epilogue. */
 #define MOE_ACT_NONE       0
 #define MOE_ACT_RELU       1
@@ -502,6 +548,32 @@ typedef struct moe_linear_args {
 } moe_linear_args;
 int moe_linear(const moe_linear_args* a);
 size_t moe_linear_workspace_size(int32_t T, int32_t K, int32_t N, int32_t quant);
+
+/* moe_gated_linear: the first half of a gated feed-forward block, both projections in one pass over x:
+ *   [g | u] = dequant(xq, xs) @ dequant(w, w_scale) + bias,   h = bf16_RNE( act(g) * u ),
+ * float32 sums as in moe_linear, rounded once.  w holds the gate projection in columns [0, I) and the up
+ * projection in [I, 2I), as an expert's w13, in moe_linear's layouts with N = 2I.
+ *   T, K, I    K % 128 == 0, K <= 32768; I % 32 == 0; T * K < 2^31, K * 2I < 2^31, T * 2I < 2^40.
+ *   quant, xq, xs, w, w_scale, activation  as in moe_linear.
+ *   bias       [2I] float32 (gate, then up) or NULL.
+ *   h          [T, I] bf16 out, 16-byte aligned.
+ *   gu         [T, 2I] bf16 out, 16-byte aligned, or NULL: g and u as rounded to bf16, what
+ *              moe_gated_linear_backward reads (h is formed from the unrounded ones).
+ * h's codes for the block's second product are moe_quant_act's or moe_quant_act_mx's.  Deterministic. */
+typedef struct moe_gated_linear_args {
+    int32_t T, K, I;
+    const uint8_t* xq;
+    const uint8_t* xs;
+    const uint8_t* w;
+    const uint8_t* w_scale;
+    const float*   bias;
+    int32_t        activation;
+    uint16_t*      h;
+    uint16_t*      gu;
+    int32_t        quant;
+    void*          stream;
+} moe_gated_linear_args;
+int moe_gated_linear(const moe_gated_linear_args* a);
 
 /* moe_balance_loss: load-balance and z losses of a router, with per-expert counts.  The rows are
  * num_seqs packed sequences, sequence s in rows [seq_offsets[s], seq_offsets[s+1]); seq_offsets

@@ -1,4 +1,4 @@
-// Residual addition + RMS norm with E4M3 codes, and its backward pass (gfx950).
+// Residual addition + RMS norm or layer norm with E4M3 codes, and their backward passes (gfx950).
 //
 // One pass: a row's vectors of 8 columns stay in registers between the sum of squares and the
 // output, so every input byte is read once and every output byte written once; the kernels are
@@ -70,6 +70,26 @@ __device__ __forceinline__ double row_sum(double v, double* s) {
     return v;
 }
 
+// The same for two sums in one exchange.
+template <int G>
+__device__ __forceinline__ void row_sums(double& v, double& u, double* s, double* t) {
+    v = wave_sum(v);
+    u = wave_sum(u);
+    if constexpr (G > 64) {
+        if ((threadIdx.x & 63) == 0) {
+            s[threadIdx.x >> 6] = v;
+            t[threadIdx.x >> 6] = u;
+        }
+        __syncthreads();
+        v = u = 0.0;
+#pragma unroll
+        for (int i = 0; i < G / 64; ++i) {
+            v += s[i];
+            u += t[i];
+        }
+    }
+}
+
 // 1 / sqrt(x) to double precision: the instruction's estimate (about 2^-26 off) and one Newton step,
 // which would make NaN of the infinity and the zero that the ends of the range give.
 __device__ __forceinline__ double rsqrt_f64(double x) {
@@ -115,17 +135,22 @@ __device__ __forceinline__ uint2 group_codes(const float (&f)[8], int& e) {
 // memory hides: y is then the definition's value rounded once, and the codes, which a value beside a
 // border would otherwise tip, are the definition's codes.  4096 x 7168 with residual and 32-column codes:
 // 50 us, 5.3 TB/s of what it must move; 32 x 2816: 3.7 us, a launch.
-template <int G, int VPT, bool ST>
-__global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_rmsnorm(NormArgs a) {
+//
+// LN: layer norm, y = (h - m) r w + b with r = 1 / sqrt(mean((h - m)^2) + eps).  Both sums in one exchange:
+// of d = h - h[0] and of d^2, in double, from which m - h[0] = mean(d) and the variance mean(d^2) - mean(d)^2
+// follow.  The shift by a value of the row itself keeps them from cancelling: the two terms differ by a factor
+// of at most H, and a constant row's variance is 0.
+template <int G, int VPT, bool ST, bool LN>
+__device__ __forceinline__ void add_norm(const NormArgs& a) {
     constexpr int RPB = G < 256 ? 256 / G : 1;
-    __shared__ double s_sum[G / 64];
+    __shared__ double s_sum[LN ? 2 : 1][G / 64];
     const int sub = threadIdx.x % G, nv = a.H >> 3;
     const int64_t t = (int64_t)blockIdx.x * RPB + threadIdx.x / G;
     if (RPB > 1 && t >= a.T) return;   // (RPB > 1 only with G = 64: no barrier follows)
     const uint16_t* xr = a.x + t * a.ldx;
     const uint16_t* rr = a.res ? a.res + t * a.ldr : nullptr;
     uint4 vx[VPT], vr[VPT];
-    float4 w0[VPT], w1[VPT];
+    float4 w0[VPT], w1[VPT], b0[LN ? VPT : 1], b1[LN ? VPT : 1];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int v = sub + i * G;
@@ -147,8 +172,20 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_rmsnorm(NormArgs a) {
             w0[i] = *reinterpret_cast<const float4*>(a.w + v * 8);
             w1[i] = *reinterpret_cast<const float4*>(a.w + v * 8 + 4);
         }
+        if constexpr (LN) {
+            b0[i] = b1[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (a.b && v < nv) {
+                b0[i] = *reinterpret_cast<const float4*>(a.b + v * 8);
+                b1[i] = *reinterpret_cast<const float4*>(a.b + v * 8 + 4);
+            }
+        }
     }
-    double ss = 0.0;
+    double ss = 0.0, sd = 0.0, h0 = 0.0;
+    if constexpr (LN) {   // h[0]
+        float f = bf16_to_f32(xr[0]);
+        if (rr) f = bf16_to_f32(pack_bf16(f + bf16_to_f32(rr[0]), 0.f) & 0xFFFFu);
+        h0 = (double)f;
+    }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         float f[8];
@@ -161,26 +198,56 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_rmsnorm(NormArgs a) {
             vx[i] = pack8(f);      // h, rounded once; kept as bf16
             unpack8(vx[i], f);
         }
+        if constexpr (LN) {
+            if (sub + i * G < nv) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fma((double)f[j], (double)f[j], ss);
+                for (int j = 0; j < 8; ++j) {
+                    const double d = (double)f[j] - h0;
+                    sd += d;
+                    ss = fma(d, d, ss);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss = fma((double)f[j], (double)f[j], ss);
+        }
     }
-    if (a.h) {
+    const auto put_h = [&]() __attribute__((always_inline)) {
+        if (!a.h) return;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = sub + i * G;
             if (v < nv) st16<ST>(a.h + t * a.H + v * 8, vx[i]);
         }
-    }
+    };
+    if (!LN || (!a.y && !a.yq)) put_h();
     if (!a.y && !a.yq) return;   // (uniform)
-    const double r = rsqrt_f64(fma(row_sum<G>(ss, s_sum), a.inv_h, (double)a.eps));
+    double r, mean = 0.0;
+    if constexpr (LN) {
+        row_sums<G>(ss, sd, s_sum[0], s_sum[1]);
+        put_h();   // behind the exchange: h may be x or residual, and every wave has read its first column by now
+        const double m = sd * a.inv_h;
+        r = rsqrt_f64(fma(-m, m, ss * a.inv_h) + (double)a.eps);
+        mean = h0 + m;
+    } else {
+        r = rsqrt_f64(fma(row_sum<G>(ss, s_sum[0]), a.inv_h, (double)a.eps));
+    }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int v = sub + i * G;
         float f[8];
         unpack8(vx[i], f);
         const float w[8] = {w0[i].x, w0[i].y, w0[i].z, w0[i].w, w1[i].x, w1[i].y, w1[i].z, w1[i].w};
+        float b[8] = {};
+        if constexpr (LN) {
+            const float4 lo = b0[i], hi = b1[i];
+            b[0] = lo.x, b[1] = lo.y, b[2] = lo.z, b[3] = lo.w, b[4] = hi.x, b[5] = hi.y, b[6] = hi.z, b[7] = hi.w;
+        }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = round_odd((double)f[j] * r * (double)w[j]);
+        for (int j = 0; j < 8; ++j) {
+            if constexpr (LN) f[j] = round_odd(fma(((double)f[j] - mean) * r, (double)w[j], (double)b[j]));
+            else f[j] = round_odd((double)f[j] * r * (double)w[j]);
+        }
         const uint4 o = pack8(f);
         if (v < nv) {   // a scale's lanes are all in or all out: H is a multiple of its columns
             if (a.y) st16<ST>(a.y + t * a.H + v * 8, o);
@@ -199,7 +266,16 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_rmsnorm(NormArgs a) {
     }
 }
 
-template <int G, int VPT>
+template <int G, int VPT, bool ST>
+__global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_rmsnorm(NormArgs a) {
+    add_norm<G, VPT, ST, false>(a);
+}
+template <int G, int VPT, bool ST>
+__global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_layernorm(NormArgs a) {
+    add_norm<G, VPT, ST, true>(a);
+}
+
+template <int G, int VPT, bool LN>
 static void run_norm(const NormArgs& args, hipStream_t st) {
     constexpr int RPB = G < 256 ? 256 / G : 1;
     const dim3 block(G < 256 ? 256 : G);
@@ -215,21 +291,30 @@ static void run_norm(const NormArgs& args, hipStream_t st) {
             a.ys = args.ys + t * (args.H / args.group);
         }
         const dim3 grid((unsigned)ceil_div(a.T, RPB));
-        if (streamed(args.T, args.H)) hipLaunchKernelGGL((k_add_rmsnorm<G, VPT, true>), grid, block, 0, st, a);
-        else hipLaunchKernelGGL((k_add_rmsnorm<G, VPT, false>), grid, block, 0, st, a);
+        const bool far = streamed(args.T, args.H);
+        if constexpr (LN) {
+            if (far) hipLaunchKernelGGL((k_add_layernorm<G, VPT, true>), grid, block, 0, st, a);
+            else hipLaunchKernelGGL((k_add_layernorm<G, VPT, false>), grid, block, 0, st, a);
+        } else {
+            if (far) hipLaunchKernelGGL((k_add_rmsnorm<G, VPT, true>), grid, block, 0, st, a);
+            else hipLaunchKernelGGL((k_add_rmsnorm<G, VPT, false>), grid, block, 0, st, a);
+        }
     }
 }
 
-hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t st) {
+template <bool LN>
+static hipError_t launch_norm(const NormArgs& a, hipStream_t st) {
     const int nv = a.H / 8;
-    if (nv <= 64) run_norm<64, 1>(a, st);
-    else if (nv <= 256) run_norm<256, 1>(a, st);
-    else if (nv <= 512) run_norm<512, 1>(a, st);
-    else if (nv <= 1024) run_norm<512, 2>(a, st);   // (with one vector each, 1024 threads are 2% slower at 4096 x 7168)
-    else if (nv <= 2048) run_norm<1024, 2>(a, st);
-    else run_norm<1024, 4>(a, st);
+    if (nv <= 64) run_norm<64, 1, LN>(a, st);
+    else if (nv <= 256) run_norm<256, 1, LN>(a, st);
+    else if (nv <= 512) run_norm<512, 1, LN>(a, st);
+    else if (nv <= 1024) run_norm<512, 2, LN>(a, st);   // (with one vector each, 1024 threads are 2% slower at 4096 x 7168)
+    else if (nv <= 2048) run_norm<1024, 2, LN>(a, st);
+    else run_norm<1024, 4, LN>(a, st);
     return hipGetLastError();
 }
+hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t st) { return launch_norm<false>(a, st); }
+hipError_t launch_add_layernorm(const NormArgs& a, hipStream_t st) { return launch_norm<true>(a, st); }
 
 // ----------------------------------------------------------------------------------------
 // Backward.  With xhat = h r and g = dy w:  dx = r (g - xhat mean(g xhat)) + dh, and the weight
@@ -240,12 +325,24 @@ hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t st) {
 // dh 90 us, 6.0 TB/s of what it must move.  The next row is in flight over this one's sums, so long rows take
 // more vectors per thread, not more threads: 512 threads have the registers for it (2048 x 16384: 61 us,
 // 1024 threads 69, with spills).
-template <int G, int VPT, bool ST>
-__global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_rmsnorm_bwd(NormBwdArgs a) {
+//
+// LN: xhat = (h - m) r and dx = r (g - mean(g) - xhat mean(g xhat)) + dh; the bias's gradient sum_t dy takes
+// its place beside the weight's, in registers and in a second set of parts.  With d = h - h[0] (as in the
+// forward pass) the four sums of d, d^2, g and g d need one exchange: sum g (h - m) = sum g d - mean(d) sum g.
+template <int G, int VPT, bool ST, bool LN>
+__device__ __forceinline__ void add_norm_bwd(const NormBwdArgs& a) {
     constexpr int RPB = G < 256 ? 256 / G : 1;
-    constexpr bool AHEAD = VPT <= 4;   // else the registers hold no second row and no weights
-    __shared__ double s_sum[2][2][G / 64];
+    constexpr bool AHEAD = VPT <= (LN ? 2 : 4);   // else the registers hold no second row and no weights
+    constexpr int NS = LN ? 4 : 2;
+    __shared__ double s_sum[2][NS][G / 64];
     __shared__ __align__(16) float s_dw[RPB][RPB > 1 ? VPT * G * 8 : 4];
+    float db[LN ? VPT : 1][8];
+    if constexpr (LN) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) db[i][j] = 0.f;
+    }
     const int sub = RPB > 1 ? threadIdx.x % G : threadIdx.x, rw = RPB > 1 ? threadIdx.x / G : 0, nv = a.H >> 3;
     const int64_t step = (int64_t)gridDim.x * RPB;
     float dw[VPT][8], wk[AHEAD ? VPT : 1][8];
@@ -289,7 +386,8 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_rmsnorm_bwd(NormBwdAr
         for (int i = 0; i < VPT; ++i) vh[i] = nx.h[i], vd[i] = nx.d[i], vr[i] = nx.r[i];
         if (AHEAD && t + step < a.T) load(t + step, nx);   // in flight over this row's sums
         // sum h^2 and sum g h in one exchange: mean(g xhat) = r sum(g h) / H
-        double ss = 0.0, gh = 0.0;
+        double ss = 0.0, gh = 0.0, sd = 0.0, sg = 0.0, h0 = 0.0;
+        if constexpr (LN) h0 = (double)bf16_to_f32(a.h[t * a.H]);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             float h[8], d[8], wt[8];
@@ -298,27 +396,58 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_rmsnorm_bwd(NormBwdAr
             if constexpr (!AHEAD) weights(i, wt);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                ss = fma((double)h[j], (double)h[j], ss);
-                gh = fma((double)(d[j] * (AHEAD ? wk[AHEAD ? i : 0][j] : wt[j])), (double)h[j], gh);
+                if constexpr (LN) {
+                    // (no weight, and no gradient, behind the row's end: only d has to be left out there)
+                    const double x = sub + i * G < nv ? (double)h[j] - h0 : 0.0;
+                    const double g = (double)d[j] * (double)(AHEAD ? wk[AHEAD ? i : 0][j] : wt[j]);
+                    sd += x;
+                    sg += g;
+                    ss = fma(x, x, ss);
+                    gh = fma(g, x, gh);
+                } else {
+                    ss = fma((double)h[j], (double)h[j], ss);
+                    gh = fma((double)(d[j] * (AHEAD ? wk[AHEAD ? i : 0][j] : wt[j])), (double)h[j], gh);
+                }
             }
             if constexpr (VPT > 2) __builtin_amdgcn_sched_barrier(0);   // one vector's values at a time
         }
         ss = wave_sum(ss);
         gh = wave_sum(gh);
+        if constexpr (LN) {
+            sd = wave_sum(sd);
+            sg = wave_sum(sg);
+        }
         if constexpr (G > 64) {
             if ((sub & 63) == 0) {
                 s_sum[par][0][sub >> 6] = ss;
                 s_sum[par][1][sub >> 6] = gh;
+                if constexpr (LN) {
+                    s_sum[par][2][sub >> 6] = sd;
+                    s_sum[par][3][sub >> 6] = sg;
+                }
             }
             __syncthreads();
-            ss = gh = 0.0;
+            ss = gh = sd = sg = 0.0;
 #pragma unroll
             for (int i = 0; i < G / 64; ++i) {
                 ss += s_sum[par][0][i];
                 gh += s_sum[par][1][i];
+                if constexpr (LN) {
+                    sd += s_sum[par][2][i];
+                    sg += s_sum[par][3][i];
+                }
             }
         }
-        const double rd = rsqrt_f64(fma(ss, a.inv_h, (double)a.eps));
+        double rd, mean = 0.0, mg = 0.0, mx = 0.0;   // LN: mean(h), mean(g), mean(g xhat)
+        if constexpr (LN) {
+            const double md = sd * a.inv_h;
+            rd = rsqrt_f64(fma(-md, md, ss * a.inv_h) + (double)a.eps);
+            mean = h0 + md;
+            mg = sg * a.inv_h;
+            mx = (gh * a.inv_h - md * mg) * rd;
+        } else {
+            rd = rsqrt_f64(fma(ss, a.inv_h, (double)a.eps));
+        }
         const float r = (float)rd, m = (float)(gh * a.inv_h * rd);   // m = mean(g xhat)
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
@@ -334,46 +463,72 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_rmsnorm_bwd(NormBwdAr
             if constexpr (!AHEAD) weights(i, wt);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float x = (float)((double)h[j] * rd);
-                dw[i][j] = fmaf(d[j], x, dw[i][j]);
-                const float g = r * (d[j] * (AHEAD ? wk[AHEAD ? i : 0][j] : wt[j]) - x * m);
-                e[j] = a.dh ? g + e[j] : g;
+                if constexpr (LN) {
+                    const double x = ((double)h[j] - mean) * rd, gw = (double)d[j] * (double)(AHEAD ? wk[AHEAD ? i : 0][j] : wt[j]);
+                    dw[i][j] = fmaf(d[j], (float)x, dw[i][j]);
+                    db[i][j] += d[j];
+                    const float g = (float)(rd * fma(-x, mx, gw - mg));
+                    e[j] = a.dh ? g + e[j] : g;
+                } else {
+                    const float x = (float)((double)h[j] * rd);
+                    dw[i][j] = fmaf(d[j], x, dw[i][j]);
+                    const float g = r * (d[j] * (AHEAD ? wk[AHEAD ? i : 0][j] : wt[j]) - x * m);
+                    e[j] = a.dh ? g + e[j] : g;
+                }
             }
             if (v < nv) st16<ST>(a.dx + t * a.H + v * 8, pack8(e));
             if constexpr (VPT > 2) __builtin_amdgcn_sched_barrier(0);
         }
     }
-    if (a.dw) {
+    auto part = [&](float (&dw)[VPT][8], float* out) __attribute__((always_inline)) {
         if constexpr (RPB > 1) {   // the waves' sums, in order
 #pragma unroll
             for (int i = 0; i < VPT; ++i)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) s_dw[rw][(sub + i * G) * 8 + j] = dw[i][j];
             __syncthreads();
-            if (rw) return;
+            if (rw == 0) {
 #pragma unroll
-            for (int i = 0; i < VPT; ++i)
+                for (int i = 0; i < VPT; ++i)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                    for (int j = 0; j < 8; ++j) {
 #pragma unroll
-                    for (int w = 1; w < RPB; ++w) dw[i][j] += s_dw[w][(sub + i * G) * 8 + j];
-                }
+                        for (int w = 1; w < RPB; ++w) dw[i][j] += s_dw[w][(sub + i * G) * 8 + j];
+                    }
+            }
         }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = sub + i * G;
-            if (v < nv) {
-                float* p = a.part + (int64_t)blockIdx.x * a.H + v * 8;
+            if (rw == 0 && v < nv) {
+                float* p = out + (int64_t)blockIdx.x * a.H + v * 8;
                 *reinterpret_cast<float4*>(p) = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
                 *reinterpret_cast<float4*>(p + 4) = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
             }
         }
+    };
+    if (a.dw) part(dw, a.part);
+    if constexpr (LN) {
+        if (a.db) {
+            if (RPB > 1 && a.dw) __syncthreads();   // s_dw has been read
+            part(db, a.part_b);
+        }
     }
 }
 
+template <int G, int VPT, bool ST>
+__global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_rmsnorm_bwd(NormBwdArgs a) {
+    add_norm_bwd<G, VPT, ST, false>(a);
+}
+template <int G, int VPT, bool ST>
+__global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_layernorm_bwd(NormBwdArgs a) {
+    add_norm_bwd<G, VPT, ST, true>(a);
+}
+
 // dweight[c] = sum of the partial rows: 32 columns per workgroup as 8 vectors of 4, 32 row groups, whose
-// sums are then added in order through LDS.
-__global__ __launch_bounds__(256) void k_norm_dw(const float* __restrict__ part, int np, int H, float* __restrict__ dw) {
+// sums are then added in order through LDS.  Workgroups (.., 1) sum a second set, the bias's.
+__global__ __launch_bounds__(256) void k_norm_dw(const float* part, int np, int H, float* dw, const float* part1, float* dw1) {
+    if (blockIdx.y) part = part1, dw = dw1;
     __shared__ __align__(16) float s[32][32];
     const int c = threadIdx.x & 7, g = threadIdx.x >> 3, col = blockIdx.x * 32 + 4 * c;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -395,28 +550,41 @@ __global__ __launch_bounds__(256) void k_norm_dw(const float* __restrict__ part,
     }
 }
 
-template <int G, int VPT>
+template <int G, int VPT, bool LN>
 static void run_norm_bwd(const NormBwdArgs& a, int grid, hipStream_t st) {
-    if (streamed(a.T, a.H)) hipLaunchKernelGGL((k_add_rmsnorm_bwd<G, VPT, true>), dim3(grid), dim3(G < 256 ? 256 : G), 0, st, a);
-    else hipLaunchKernelGGL((k_add_rmsnorm_bwd<G, VPT, false>), dim3(grid), dim3(G < 256 ? 256 : G), 0, st, a);
+    const dim3 block(G < 256 ? 256 : G);
+    const bool far = streamed(a.T, a.H);
+    if constexpr (LN) {
+        if (far) hipLaunchKernelGGL((k_add_layernorm_bwd<G, VPT, true>), dim3(grid), block, 0, st, a);
+        else hipLaunchKernelGGL((k_add_layernorm_bwd<G, VPT, false>), dim3(grid), block, 0, st, a);
+    } else {
+        if (far) hipLaunchKernelGGL((k_add_rmsnorm_bwd<G, VPT, true>), dim3(grid), block, 0, st, a);
+        else hipLaunchKernelGGL((k_add_rmsnorm_bwd<G, VPT, false>), dim3(grid), block, 0, st, a);
+    }
 }
 
-hipError_t launch_add_rmsnorm_backward(const NormBwdArgs& args, hipStream_t st) {
+template <bool LN>
+static hipError_t launch_norm_backward(const NormBwdArgs& args, hipStream_t st) {
     NormBwdArgs a = args;
     const int nv = a.H / 8, grid = norm_bwd_parts(a.T, a.H);
-    const bool one = grid == 1 && !(reinterpret_cast<uintptr_t>(a.dw) & 15);   // the only part is the sum
-    if (one) a.part = a.dw;
-    if (nv <= 64) run_norm_bwd<64, 1>(a, grid, st);
-    else if (nv <= 128) run_norm_bwd<64, 2>(a, grid, st);
-    else if (nv <= 256) run_norm_bwd<256, 1>(a, grid, st);
-    else if (nv <= 512) run_norm_bwd<512, 1>(a, grid, st);
-    else if (nv <= 1024) run_norm_bwd<512, 2>(a, grid, st);
-    else if (nv <= 2048) run_norm_bwd<512, 4>(a, grid, st);
-    else run_norm_bwd<512, 8>(a, grid, st);
+    const auto odd = [](const float* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; };
+    const bool one = grid == 1 && !odd(a.dw) && !odd(a.db);   // the only part is the sum
+    if (one) a.part = a.dw, a.part_b = a.db;
+    if (nv <= 64) run_norm_bwd<64, 1, LN>(a, grid, st);
+    else if (nv <= 128) run_norm_bwd<64, 2, LN>(a, grid, st);
+    else if (nv <= 256) run_norm_bwd<256, 1, LN>(a, grid, st);
+    else if (nv <= 512) run_norm_bwd<512, 1, LN>(a, grid, st);
+    else if (nv <= 1024) run_norm_bwd<512, 2, LN>(a, grid, st);
+    else if (nv <= 2048) run_norm_bwd<512, 4, LN>(a, grid, st);
+    else run_norm_bwd<512, 8, LN>(a, grid, st);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !a.dw || one) return e;
-    hipLaunchKernelGGL(k_norm_dw, dim3((unsigned)ceil_div(a.H, 32)), dim3(256), 0, st, a.part, grid, a.H, a.dw);
+    if (e != hipSuccess || (!a.dw && !a.db) || one) return e;
+    const float* first = a.dw ? a.part : a.part_b;
+    hipLaunchKernelGGL(k_norm_dw, dim3((unsigned)ceil_div(a.H, 32), a.dw && a.db ? 2 : 1), dim3(256), 0, st, first, grid, a.H,
+                       a.dw ? a.dw : a.db, a.part_b, a.db);
     return hipGetLastError();
 }
+hipError_t launch_add_rmsnorm_backward(const NormBwdArgs& a, hipStream_t st) { return launch_norm_backward<false>(a, st); }
+hipError_t launch_add_layernorm_backward(const NormBwdArgs& a, hipStream_t st) { return launch_norm_backward<true>(a, st); }
 
 }  // namespace moe

@@ -55,8 +55,10 @@ struct NormArgs {
     uint8_t* ys;
     int group;       // columns per scale: 0 (no codes), 32 or 128
     double inv_h;    // 1 / H
+    const float* b = nullptr;   // layer norm: bias or NULL
 };
 hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t st);
+hipError_t launch_add_layernorm(const NormArgs& a, hipStream_t st);
 
 struct NormBwdArgs {
     int T, H;
@@ -69,8 +71,11 @@ struct NormBwdArgs {
     float* dw;            // or NULL
     float* part;          // workspace: [norm_bwd_parts(T, H)][H], used with dw
     double inv_h;         // 1 / H
+    float* db = nullptr;      // layer norm: the bias's gradient or NULL, and its parts as those of dw
+    float* part_b = nullptr;
 };
 hipError_t launch_add_rmsnorm_backward(const NormBwdArgs& a, hipStream_t st);
+hipError_t launch_add_layernorm_backward(const NormBwdArgs& a, hipStream_t st);
 
 struct LinArgs {
     int T, K, N;
@@ -84,9 +89,12 @@ struct LinArgs {
     void* y;
     int64_t ldy;
     int act, out_bf16, mx;
-    int nt = 0;           // outputs past the caches (set by launch_linear)
+    int nt = 0;           // outputs past the caches (set by the launchers)
+    uint16_t* gu = nullptr;   // gated block: both sums, [T, N] bf16, or NULL
 };
 hipError_t launch_linear(const LinArgs& a, hipStream_t st);
+// y = act(gate) * up, bf16 [T, N / 2] without strides; no residual
+hipError_t launch_gated_linear(const LinArgs& a, hipStream_t st);
 
 struct BalanceArgs {
     int T, E, k, S, scoring;

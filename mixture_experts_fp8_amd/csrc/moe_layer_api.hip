@@ -34,6 +34,26 @@ int moe_add_rmsnorm_backward(const moe_add_rmsnorm_backward_args* a) {
     return done("moe_add_rmsnorm_backward", moe::launch_add_rmsnorm_backward(n, static_cast<hipStream_t>(a->stream)));
 }
 
+int moe_add_layernorm(const moe_add_layernorm_args* a) {
+    if (int rc = moe::host::check_add_layernorm(a)) return rc;
+    const int group = !a->yq ? 0 : a->quant == MOE_QUANT_FP8_BLOCK128 ? 128 : 32;
+    const moe::NormArgs n{a->T, a->H, a->x, a->ld_x, a->residual, a->ld_residual, a->weight, a->eps,
+                          a->h, a->y, a->yq, a->ys, group, 1.0 / a->H, a->bias};
+    return done("moe_add_layernorm", moe::launch_add_layernorm(n, static_cast<hipStream_t>(a->stream)));
+}
+
+size_t moe_add_layernorm_backward_workspace_size(int32_t T, int32_t H) {
+    return T < 1 || H < 1 ? 0 : 2 * moe::norm_bwd_ws_bytes(T, H);
+}
+
+int moe_add_layernorm_backward(const moe_add_layernorm_backward_args* a) {
+    if (int rc = moe::host::check_add_layernorm_backward(a)) return rc;
+    float* part = static_cast<float*>(a->workspace);
+    const moe::NormBwdArgs n{a->T, a->H, a->dy, a->h, a->weight, a->eps, a->dh, a->dx, a->dweight,
+                             part, 1.0 / a->H, a->dbias, part ? part + moe::norm_bwd_ws_bytes(a->T, a->H) / 4 : nullptr};
+    return done("moe_add_layernorm_backward", moe::launch_add_layernorm_backward(n, static_cast<hipStream_t>(a->stream)));
+}
+
 size_t moe_linear_workspace_size(int32_t T, int32_t K, int32_t N, int32_t quant) {
     (void)T, (void)K, (void)N, (void)quant;
     return 0;
@@ -44,6 +64,14 @@ int moe_linear(const moe_linear_args* a) {
     const moe::LinArgs l{a->T, a->K, a->N, a->xq, a->xs, a->w, a->w_scale, a->bias, a->residual, a->ld_residual,
                          a->y, a->ld_y, a->activation, a->out_dtype == MOE_DTYPE_BF16, a->quant == MOE_QUANT_MXFP8};
     return done("moe_linear", moe::launch_linear(l, static_cast<hipStream_t>(a->stream)));
+}
+
+int moe_gated_linear(const moe_gated_linear_args* a) {
+    if (int rc = moe::host::check_gated_linear(a)) return rc;
+    moe::LinArgs l{a->T, a->K, 2 * a->I, a->xq, a->xs, a->w, a->w_scale, a->bias, nullptr, 0,
+                   a->h, a->I, a->activation, 1, a->quant == MOE_QUANT_MXFP8};
+    l.gu = a->gu;
+    return done("moe_gated_linear", moe::launch_gated_linear(l, static_cast<hipStream_t>(a->stream)));
 }
 
 size_t moe_balance_loss_workspace_size(int32_t T, int32_t E, int32_t num_seqs) {

@@ -120,6 +120,22 @@ int check_router(const char* op, const moe_route_params* p, int T, int S, const 
     return MOE_OK;
 }
 
+// Scheme, depth and activation of a gated block's products of T rows, N = 2I wide.
+int check_gated(const char* op, int T, int K, int64_t N, int quant, int activation) {
+    if (quant < MOE_QUANT_FP8_BLOCK128 || quant > MOE_QUANT_W8A16)
+        return fail(MOE_ERR_INVALID, "%s: quant (%d) must be one of MOE_QUANT_*", op, quant);
+    if (quant != MOE_QUANT_FP8_BLOCK128 && quant != MOE_QUANT_MXFP8)
+        return fail(MOE_ERR_UNSUPPORTED, "%s: quant (%d) must be MOE_QUANT_FP8_BLOCK128 or MOE_QUANT_MXFP8", op, quant);
+    if (K % 128) return fail(MOE_ERR_UNSUPPORTED, "%s: K (%d) must be a multiple of 128", op, K);
+    if (K > 32768) return fail(MOE_ERR_UNSUPPORTED, "%s: K (%d) must not exceed 32768", op, K);
+    if ((int64_t)T * K >= ((int64_t)1 << 31) || K * N >= ((int64_t)1 << 31))
+        return fail(MOE_ERR_UNSUPPORTED, "%s: T * K (%lld) and K * 2I (%lld) must be below 2^31 (32-bit offsets)", op,
+                    (long long)T * K, (long long)(K * N));
+    if (activation < MOE_ACT_NONE || activation > MOE_ACT_GELU_TANH)
+        return fail(MOE_ERR_INVALID, "%s: activation (%d) must be one of MOE_ACT_*", op, activation);
+    return MOE_OK;
+}
+
 int check_ws(const char* op, const void* ws, size_t have, size_t need) {
     if (!need) return MOE_OK;
     if (!ws || have < need)
@@ -129,11 +145,8 @@ int check_ws(const char* op, const void* ws, size_t have, size_t need) {
     return MOE_OK;
 }
 
-}  // namespace
-
-int check_add_rmsnorm(const moe_add_rmsnorm_args* a) {
-    const char* op = "moe_add_rmsnorm";
-    if (!a) return fail(MOE_ERR_INVALID, "%s: args must not be NULL", op);
+template <typename Args>
+int check_norm(const char* op, const Args* a, const float* bias) {
     int rc = check_norm_shape(op, a->T, a->H, a->eps);
     if (rc) return rc;
     const int T = a->T, H = a->H;
@@ -153,26 +166,25 @@ int check_add_rmsnorm(const moe_add_rmsnorm_args* a) {
         return fail(MOE_ERR_INVALID, "%s: ld_x (%lld) and ld_residual (%lld) must be >= H (%d)", op,
                     (long long)a->ld_x, (long long)a->ld_residual, H);
     if (a->ld_x % 8 || (a->residual && a->ld_residual % 8) || !aligned(a->x, 16) || !aligned(a->residual, 16) ||
-        !aligned(a->weight, 16) || !aligned(a->h, 16) || !aligned(a->y, 16))
-        return fail(MOE_ERR_UNSUPPORTED, "%s: x, residual, weight, h and y must be 16-byte aligned, rows a multiple of "
-                    "8 elements apart", op);
+        !aligned(a->weight, 16) || !aligned(bias, 16) || !aligned(a->h, 16) || !aligned(a->y, 16))
+        return fail(MOE_ERR_UNSUPPORTED, "%s: x, residual, weight%s, h and y must be 16-byte aligned, rows a multiple of "
+                    "8 elements apart", op, bias ? ", bias" : "");
     const Span x{"x", a->x, span2(T, H, a->ld_x, 2)};
     const Span res{"residual", a->residual, a->residual ? span2(T, H, a->ld_residual, 2) : 0};
-    const Span w{"weight", a->weight, (uint64_t)H * 4};
+    const Span w{"weight", a->weight, (uint64_t)H * 4}, b{"bias", bias, (uint64_t)H * 4};
     const uint64_t n = (uint64_t)T * H;
     const Span out[4] = {{"h", a->h, n * 2}, {"y", a->y, n * 2}, {"yq", a->yq, n}, {"ys", a->ys, group ? n / group : 0}};
     if ((rc = check_outputs(op, out, 4))) return rc;
     for (int i = 0; i < 4; ++i) {
         if ((rc = check_io(op, out[i], x, i < 2 && a->ld_x == H))) return rc;
         if ((rc = check_io(op, out[i], res, i == 0 && a->ld_residual == H))) return rc;
-        if ((rc = check_io(op, out[i], w))) return rc;
+        if ((rc = check_io(op, out[i], w)) || (rc = check_io(op, out[i], b))) return rc;
     }
     return MOE_OK;
 }
 
-int check_add_rmsnorm_backward(const moe_add_rmsnorm_backward_args* a) {
-    const char* op = "moe_add_rmsnorm_backward";
-    if (!a) return fail(MOE_ERR_INVALID, "%s: args must not be NULL", op);
+template <typename Args>
+int check_norm_backward(const char* op, const Args* a, float* dbias, size_t need) {
     int rc = check_norm_shape(op, a->T, a->H, a->eps);
     if (rc) return rc;
     if (!a->dy || !a->h || !a->weight || !a->dx)
@@ -180,16 +192,39 @@ int check_add_rmsnorm_backward(const moe_add_rmsnorm_backward_args* a) {
     if (!aligned(a->dy, 16) || !aligned(a->h, 16) || !aligned(a->weight, 16) || !aligned(a->dh, 16) || !aligned(a->dx, 16))
         return fail(MOE_ERR_UNSUPPORTED, "%s: dy, h, weight, dh and dx must be 16-byte aligned", op);
     if (!aligned(a->dweight, 4)) return fail(MOE_ERR_INVALID, "%s: dweight must be 4-byte aligned", op);
-    const size_t need = a->dweight ? norm_bwd_ws_bytes(a->T, a->H) : 0;
+    if (!aligned(dbias, 4)) return fail(MOE_ERR_INVALID, "%s: dbias must be 4-byte aligned", op);
+    if (!a->dweight && !dbias) need = 0;
     const uint64_t n = (uint64_t)a->T * a->H * 2, nw = (uint64_t)a->H * 4;
-    const Span out[3] = {{"dx", a->dx, n}, {"dweight", a->dweight, nw}, {"workspace", need ? a->workspace : nullptr, need}};
+    const Span out[4] = {{"dx", a->dx, n}, {"dweight", a->dweight, nw}, {"dbias", dbias, nw},
+                         {"workspace", need ? a->workspace : nullptr, need}};
     const Span in[4] = {{"dy", a->dy, n}, {"h", a->h, n}, {"dh", a->dh, n}, {"weight", a->weight, nw}};
     if ((rc = check_ws(op, a->workspace, a->workspace_bytes, need))) return rc;
-    if ((rc = check_outputs(op, out, 3))) return rc;
-    for (int i = 0; i < 3; ++i)
+    if ((rc = check_outputs(op, out, 4))) return rc;
+    for (int i = 0; i < 4; ++i)
         for (int j = 0; j < 4; ++j)
             if ((rc = check_io(op, out[i], in[j], i == 0 && (j == 0 || j == 2)))) return rc;
     return MOE_OK;
+}
+
+}  // namespace
+
+int check_add_rmsnorm(const moe_add_rmsnorm_args* a) {
+    const char* op = "moe_add_rmsnorm";
+    return a ? check_norm(op, a, nullptr) : fail(MOE_ERR_INVALID, "%s: args must not be NULL", op);
+}
+int check_add_layernorm(const moe_add_layernorm_args* a) {
+    const char* op = "moe_add_layernorm";
+    return a ? check_norm(op, a, a->bias) : fail(MOE_ERR_INVALID, "%s: args must not be NULL", op);
+}
+int check_add_rmsnorm_backward(const moe_add_rmsnorm_backward_args* a) {
+    const char* op = "moe_add_rmsnorm_backward";
+    if (!a) return fail(MOE_ERR_INVALID, "%s: args must not be NULL", op);
+    return check_norm_backward(op, a, nullptr, a->T < 1 || a->H < 1 ? 0 : norm_bwd_ws_bytes(a->T, a->H));
+}
+int check_add_layernorm_backward(const moe_add_layernorm_backward_args* a) {
+    const char* op = "moe_add_layernorm_backward";
+    if (!a) return fail(MOE_ERR_INVALID, "%s: args must not be NULL", op);
+    return check_norm_backward(op, a, a->dbias, a->T < 1 || a->H < 1 ? 0 : 2 * norm_bwd_ws_bytes(a->T, a->H));
 }
 
 int check_linear(const moe_linear_args* a) {
@@ -245,6 +280,38 @@ int check_linear(const moe_linear_args* a) {
         if (a->y != a->residual && d >= used && row - d >= used) return MOE_OK;
     }
     if (int rc = check_io(op, y, in[5], a->ld_residual == a->ld_y)) return rc;
+    return MOE_OK;
+}
+
+int check_gated_linear(const moe_gated_linear_args* a) {
+    const char* op = "moe_gated_linear";
+    if (!a) return fail(MOE_ERR_INVALID, "%s: args must not be NULL", op);
+    const int T = a->T, K = a->K, I = a->I;
+    if (T < 1 || K < 1 || I < 1) return fail(MOE_ERR_INVALID, "%s: T, K, I (%d, %d, %d) must be > 0", op, T, K, I);
+    if (I % 32) return fail(MOE_ERR_UNSUPPORTED, "%s: I (%d) must be a multiple of 32", op, I);
+    const int64_t N = 2 * (int64_t)I;
+    int rc = check_gated(op, T, K, N, a->quant, a->activation);
+    if (rc) return rc;
+    if (T * N >= ((int64_t)1 << 40))
+        return fail(MOE_ERR_UNSUPPORTED, "%s: T * 2I (%lld) must be below 2^40", op, (long long)(T * N));
+    if (!a->xq || !a->xs || !a->w || !a->w_scale || !a->h)
+        return fail(MOE_ERR_INVALID, "%s: xq, xs, w, w_scale and h must not be NULL", op);
+    if (!aligned(a->xq, 16) || !aligned(a->w, 16) || !aligned(a->h, 16) || !aligned(a->gu, 16))
+        return fail(MOE_ERR_UNSUPPORTED, "%s: xq, w, h and gu must be 16-byte aligned", op);
+    const bool mx = a->quant == MOE_QUANT_MXFP8;
+    if (mx && (!aligned(a->xs, 4) || !aligned(a->w_scale, 4)))
+        return fail(MOE_ERR_UNSUPPORTED, "%s: xs and w_scale must be 4-byte aligned for MOE_QUANT_MXFP8", op);
+    if (!aligned(a->bias, 4)) return fail(MOE_ERR_INVALID, "%s: bias must be 4-byte aligned", op);
+    const Span out[2] = {{"h", a->h, (uint64_t)T * I * 2}, {"gu", a->gu, (uint64_t)T * N * 2}};
+    const Span in[5] = {{"xq", a->xq, (uint64_t)T * K},
+                        {"xs", a->xs, (uint64_t)T * (K / (mx ? 32 : 128))},
+                        {"w", a->w, (uint64_t)K * N},
+                        {"w_scale", a->w_scale, mx ? (uint64_t)K * N / 32 : (uint64_t)(K / 128) * cdiv(N, 128)},
+                        {"bias", a->bias, (uint64_t)N * 4}};
+    if ((rc = check_outputs(op, out, 2))) return rc;
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 5; ++j)
+            if ((rc = check_io(op, out[i], in[j]))) return rc;
     return MOE_OK;
 }
 

@@ -22,7 +22,10 @@ BalancePlan balance_plan(int T, int E, int S);
 namespace host {
 int check_add_rmsnorm(const moe_add_rmsnorm_args* a);
 int check_add_rmsnorm_backward(const moe_add_rmsnorm_backward_args* a);
+int check_add_layernorm(const moe_add_layernorm_args* a);
+int check_add_layernorm_backward(const moe_add_layernorm_backward_args* a);
 int check_linear(const moe_linear_args* a);
+int check_gated_linear(const moe_gated_linear_args* a);
 int check_balance_loss(const moe_balance_loss_args* a);
 int check_route_backward(const moe_route_backward_args* a);
 int check_combine_backward(const moe_combine_backward_args* a);

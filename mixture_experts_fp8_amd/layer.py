@@ -35,11 +35,28 @@ class AddRmsNormBackwardArgs(ctypes.Structure):
                 ("dx", _vp), ("dweight", _vp), ("workspace", _vp), ("workspace_bytes", _sz), ("stream", _vp)]
 
 
+class AddLayerNormArgs(ctypes.Structure):
+    _fields_ = [("T", _i32), ("H", _i32), ("x", _vp), ("ld_x", _i64), ("residual", _vp), ("ld_residual", _i64),
+                ("weight", _vp), ("bias", _vp), ("eps", _f32), ("h", _vp), ("y", _vp), ("yq", _vp), ("ys", _vp),
+                ("quant", _i32), ("stream", _vp)]
+
+
+class AddLayerNormBackwardArgs(ctypes.Structure):
+    _fields_ = [("T", _i32), ("H", _i32), ("dy", _vp), ("h", _vp), ("weight", _vp), ("eps", _f32), ("dh", _vp),
+                ("dx", _vp), ("dweight", _vp), ("dbias", _vp), ("workspace", _vp), ("workspace_bytes", _sz),
+                ("stream", _vp)]
+
+
 class LinearArgs(ctypes.Structure):
     _fields_ = [("T", _i32), ("K", _i32), ("N", _i32), ("xq", _vp), ("xs", _vp), ("w", _vp), ("w_scale", _vp),
                 ("bias", _vp), ("activation", _i32), ("residual", _vp), ("ld_residual", _i64), ("y", _vp),
                 ("ld_y", _i64), ("out_dtype", _i32), ("quant", _i32), ("workspace", _vp), ("workspace_bytes", _sz),
                 ("stream", _vp)]
+
+
+class GatedLinearArgs(ctypes.Structure):
+    _fields_ = [("T", _i32), ("K", _i32), ("I", _i32), ("xq", _vp), ("xs", _vp), ("w", _vp), ("w_scale", _vp),
+                ("bias", _vp), ("activation", _i32), ("h", _vp), ("gu", _vp), ("quant", _i32), ("stream", _vp)]
 
 
 class BalanceLossArgs(ctypes.Structure):
@@ -107,6 +124,29 @@ def _quant_group(quant: int) -> int:
     return 128 if quant == B.MOE_QUANT_FP8_BLOCK128 else 32
 
 
+def _norm_call(x, weight, bias, residual, quant, want_y, h, y):
+    """Checks a norm's inputs; (ld_x, ld_residual, h, y, yq, ys)."""
+    T, H = x.shape
+    ldx = _rows(x, "x", torch.bfloat16, (T, H))
+    ldr = _rows(residual, "residual", torch.bfloat16, (T, H)) if residual is not None else H
+    _need(weight, "weight", torch.float32, (H,))
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (H,))
+    new = dict(device=x.device)
+    if h is None and residual is not None:
+        h = torch.empty(T, H, dtype=torch.bfloat16, **new)
+    if y is None and want_y:
+        y = torch.empty(T, H, dtype=torch.bfloat16, **new)
+    for t, name in ((h, "h"), (y, "y")):
+        if t is not None:
+            _need(t, name, torch.bfloat16, (T, H))
+    yq = ys = None
+    if quant is not None:
+        yq = torch.empty(T, H, dtype=torch.uint8, **new)
+        ys = torch.empty(T, max(H // _quant_group(quant), 1), dtype=torch.uint8, **new)
+    return ldx, ldr, h, y, yq, ys
+
+
 class MoeAddRmsNorm(_Call):
     """h = bf16(x + residual), y = bf16(h * rsqrt(mean(h^2) + eps) * weight) and y's E4M3 codes.
 
@@ -121,21 +161,7 @@ class MoeAddRmsNorm(_Call):
                  residual: Optional[torch.Tensor] = None, quant: Optional[int] = None, want_y: bool = True,
                  h: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None):
         T, H = x.shape
-        ldx = _rows(x, "x", torch.bfloat16, (T, H))
-        ldr = _rows(residual, "residual", torch.bfloat16, (T, H)) if residual is not None else H
-        _need(weight, "weight", torch.float32, (H,))
-        new = dict(device=x.device)
-        if h is None and residual is not None:
-            h = torch.empty(T, H, dtype=torch.bfloat16, **new)
-        if y is None and want_y:
-            y = torch.empty(T, H, dtype=torch.bfloat16, **new)
-        for t, name in ((h, "h"), (y, "y")):
-            if t is not None:
-                _need(t, name, torch.bfloat16, (T, H))
-        yq = ys = None
-        if quant is not None:
-            yq = torch.empty(T, H, dtype=torch.uint8, **new)
-            ys = torch.empty(T, max(H // _quant_group(quant), 1), dtype=torch.uint8, **new)
+        ldx, ldr, h, y, yq, ys = _norm_call(x, weight, None, residual, quant, want_y, h, y)
         self.h, self.y, self.yq, self.ys = h, y, yq, ys
         self.out = {"h": h, "y": y, "yq": yq, "ys": ys}
         self._hold("moe_add_rmsnorm",
@@ -185,6 +211,72 @@ def moe_add_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Te
     return MoeAddRmsNormBackward(dy, h, weight, eps, dh, want_dweight)()
 
 
+class MoeAddLayerNorm(_Call):
+    """h = bf16(x + residual), y = bf16((h - mean) * rsqrt(var + eps) * weight + bias) and y's E4M3 codes.
+
+    weight, bias: float32 [H], bias None for none; everything else as in MoeAddRmsNorm.
+    A call returns {"h", "y", "yq", "ys"}, None for what is not computed."""
+
+    def __init__(self, x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                 residual: Optional[torch.Tensor] = None, quant: Optional[int] = None, want_y: bool = True,
+                 h: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None):
+        T, H = x.shape
+        ldx, ldr, h, y, yq, ys = _norm_call(x, weight, bias, residual, quant, want_y, h, y)
+        self.h, self.y, self.yq, self.ys = h, y, yq, ys
+        self.out = {"h": h, "y": y, "yq": yq, "ys": ys}
+        self._hold("moe_add_layernorm",
+                   AddLayerNormArgs(T, H, _ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), _ptr(bias), eps, _ptr(h),
+                                    _ptr(y), _ptr(yq), _ptr(ys), quant or 0, None),
+                   (x, residual, weight, bias, h, y, yq, ys))
+
+    def __call__(self, stream: Optional[int] = None) -> dict:
+        self._run(stream)
+        return self.out
+
+
+def moe_add_layernorm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                      residual: Optional[torch.Tensor] = None, quant: Optional[int] = None, want_y: bool = True,
+                      h: Optional[torch.Tensor] = None) -> dict:
+    """One call of MoeAddLayerNorm."""
+    return MoeAddLayerNorm(x, weight, bias, eps, residual, quant, want_y, h)()
+
+
+class MoeAddLayerNormBackward(_Call):
+    """Gradients of MoeAddLayerNorm from dy (of y) and dh (of h, optional), as MoeAddRmsNormBackward.  A call
+    returns {"dx", "dweight", "dbias"}: the last two float32 [H], None where not wanted."""
+
+    def __init__(self, dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
+                 dh: Optional[torch.Tensor] = None, want_dweight: bool = True, want_dbias: bool = True,
+                 dx: Optional[torch.Tensor] = None):
+        T, H = h.shape
+        for t, name in ((h, "h"), (dy, "dy"), (dh, "dh"), (dx, "dx")):
+            if t is not None:
+                _need(t, name, torch.bfloat16, (T, H))
+        _need(weight, "weight", torch.float32, (H,))
+        dx = torch.empty_like(h) if dx is None else dx
+        dw = torch.empty(H, dtype=torch.float32, device=h.device) if want_dweight else None
+        db = torch.empty(H, dtype=torch.float32, device=h.device) if want_dbias else None
+        ws = None
+        if want_dweight or want_dbias:
+            ws = workspace(lib().moe_add_layernorm_backward_workspace_size(T, H), h.device)
+        self.out = {"dx": dx, "dweight": dw, "dbias": db}
+        self._hold("moe_add_layernorm_backward",
+                   AddLayerNormBackwardArgs(T, H, _ptr(dy), _ptr(h), _ptr(weight), eps, _ptr(dh), _ptr(dx), _ptr(dw),
+                                            _ptr(db), _ptr(ws), ws.numel() if ws is not None else 0, None),
+                   (dy, h, weight, dh, dx, dw, db, ws))
+
+    def __call__(self, stream: Optional[int] = None) -> dict:
+        self._run(stream)
+        return self.out
+
+
+def moe_add_layernorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
+                               dh: Optional[torch.Tensor] = None, want_dweight: bool = True,
+                               want_dbias: bool = True) -> dict:
+    """One call of MoeAddLayerNormBackward."""
+    return MoeAddLayerNormBackward(dy, h, weight, eps, dh, want_dweight, want_dbias)()
+
+
 @dataclass
 class LinearWeights:
     """Packed weights of one [K, N] product, their scales and an optional float32 bias [N]."""
@@ -227,6 +319,24 @@ class LinearWeights:
         return LinearWeights.from_logical(q[0][:, :N].contiguous(), s[0], quant, bias)
 
 
+def _need_weights(w: LinearWeights) -> None:
+    # (the packed sizes; shapes that the packing refuses are refused by the call)
+    sizes = {"w": w.K * w.N, "w_scale": w.K * w.N // 32 if w.quant == B.MOE_QUANT_MXFP8 else w.K // 128 * -(-w.N // 128)}
+    for name, n in sizes.items():
+        t = getattr(w, name)
+        _need(t, name, torch.uint8)
+        if t.numel() != n:
+            raise ValueError(f"{name}: expected {n} elements, got {t.numel()}")
+    if w.bias is not None:
+        _need(w.bias, "bias", torch.float32, (w.N,))
+
+
+def _need_activation(activation: str) -> int:
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation: expected one of {sorted(ACTIVATIONS)}, got {activation!r}")
+    return ACTIVATIONS[activation]
+
+
 class MoeLinear(_Call):
     """y = act(dequant(xq, xs) @ w + bias) + residual.
 
@@ -240,20 +350,11 @@ class MoeLinear(_Call):
         K, N = w.K, w.N
         _need(xq, "xq", torch.uint8, (T, K))
         _need(xs, "xs", torch.uint8, (T, K // _quant_group(w.quant)))
-        if activation not in ACTIVATIONS:
-            raise ValueError(f"activation: expected one of {sorted(ACTIVATIONS)}, got {activation!r}")
+        act = _need_activation(activation)
         if out_dtype not in (torch.float32, torch.bfloat16):
             raise TypeError(f"out_dtype: expected float32 or bfloat16, got {out_dtype}")
         dt = B.MOE_DTYPE_F32 if out_dtype == torch.float32 else B.MOE_DTYPE_BF16
-        # (the packed sizes; shapes that the packing refuses are refused by the call)
-        sizes = {"w": K * N, "w_scale": K * N // 32 if w.quant == B.MOE_QUANT_MXFP8 else K // 128 * -(-N // 128)}
-        for name, n in sizes.items():
-            t = getattr(w, name)
-            _need(t, name, torch.uint8)
-            if t.numel() != n:
-                raise ValueError(f"{name}: expected {n} elements, got {t.numel()}")
-        if w.bias is not None:
-            _need(w.bias, "bias", torch.float32, (N,))
+        _need_weights(w)
         ldr = _rows(residual, "residual", out_dtype, (T, N)) if residual is not None else N
         if y is None:   # (rows 8 elements apart: N is a multiple of 16)
             y = torch.empty(T, N, dtype=out_dtype, device=xq.device)
@@ -263,7 +364,7 @@ class MoeLinear(_Call):
         self.y = y
         self._hold("moe_linear",
                    LinearArgs(T, K, N, _ptr(xq), _ptr(xs), _ptr(w.w), _ptr(w.w_scale), _ptr(w.bias),
-                              ACTIVATIONS[activation], _ptr(residual), ldr, _ptr(y), ldy, dt, w.quant, _ptr(ws),
+                              act, _ptr(residual), ldr, _ptr(y), ldy, dt, w.quant, _ptr(ws),
                               ws.numel() if ws is not None else 0, None),
                    (xq, xs, w.w, w.w_scale, w.bias, residual, y, ws))
 
@@ -277,6 +378,49 @@ def moe_linear(xq: torch.Tensor, xs: torch.Tensor, w: LinearWeights, activation:
                y: Optional[torch.Tensor] = None) -> torch.Tensor:
     """One call of MoeLinear."""
     return MoeLinear(xq, xs, w, activation, residual, out_dtype, y)()
+
+
+def _gated_shape(xq: torch.Tensor, xs: torch.Tensor, w: LinearWeights, T: int) -> None:
+    _need(xq, "xq", torch.uint8, (T, w.K))
+    _need(xs, "xs", torch.uint8, (T, w.K // _quant_group(w.quant)))
+
+
+class MoeGatedLinear(_Call):
+    """h = act(x @ Wg + bg) * (x @ Wu + bu), bf16 [T, I], x = dequant(xq, xs).
+
+    xq, xs as in MoeLinear; w: LinearWeights of N = 2I columns, gate columns before up columns (an expert's
+    w13), its bias [2I]; activation one of ACTIVATIONS.  want_gu: also the two sums, bf16 [T, 2I], which
+    MoeGatedLinearBackward reads.  A call returns {"h", "gu"}, gu None unless asked for."""
+
+    def __init__(self, xq: torch.Tensor, xs: torch.Tensor, w: LinearWeights, activation: str = "silu",
+                 want_gu: bool = False, h: Optional[torch.Tensor] = None):
+        T, I = xq.shape[0], w.N // 2
+        _gated_shape(xq, xs, w, T)
+        if w.N % 2:
+            raise ValueError(f"w: expected an even number of columns, got {w.N}")
+        act = _need_activation(activation)
+        _need_weights(w)
+        new = dict(dtype=torch.bfloat16, device=xq.device)
+        if h is None:
+            h = torch.empty(T, I, **new)
+        _need(h, "h", torch.bfloat16, (T, I))
+        gu = torch.empty(T, 2 * I, **new) if want_gu else None
+        self.h, self.gu = h, gu
+        self.out = {"h": h, "gu": gu}
+        self._hold("moe_gated_linear",
+                   GatedLinearArgs(T, w.K, I, _ptr(xq), _ptr(xs), _ptr(w.w), _ptr(w.w_scale), _ptr(w.bias), act, _ptr(h),
+                                   _ptr(gu), w.quant, None),
+                   (xq, xs, w.w, w.w_scale, w.bias, h, gu))
+
+    def __call__(self, stream: Optional[int] = None) -> dict:
+        self._run(stream)
+        return self.out
+
+
+def moe_gated_linear(xq: torch.Tensor, xs: torch.Tensor, w: LinearWeights, activation: str = "silu",
+                     want_gu: bool = False, h: Optional[torch.Tensor] = None) -> dict:
+    """One call of MoeGatedLinear."""
+    return MoeGatedLinear(xq, xs, w, activation, want_gu, h)()
 
 
 def _router_inputs(params: RouteParams, logits: torch.Tensor, ids: Optional[torch.Tensor],
