@@ -575,6 +575,49 @@ typedef struct moe_gated_linear_args {
 } moe_gated_linear_args;
 int moe_gated_linear(const moe_gated_linear_args* a);
 
+/* moe_gated_linear_backward: gradients of moe_gated_linear from dh, that of h, and its gu:
+ *   dgu   = bf16_RNE([ dh * u * act'(g) | dh * act(g) ])       (the gradient of g and u);
+ *   dx    = bf16_RNE( dgu @ dequant(w, w_scale)^T );
+ *   dw    = dequant(xq, xs)^T @ dgu                            (the gradient of w's values; rounded to dw_dtype);
+ *   dbias = column sums of [ dh * u * act'(g) | dh * act(g) ]  (float32, before the rounding of dgu).
+ * dx and dw are products of the rounded dgu, with float32 sums: the matrix cores take bf16 operands, and
+ * dequantised E4M3 values are bf16 values (scales from 2^-124 to 2^119 keep every code's value inside bf16's range; beyond
+ * it, values round to 0 or infinity).  The codes' rounding has no gradient of its own.  act' of RELU is 0 at 0;
+ * slopes and activations under 2^-115 may be 0.
+ *   T, K, I, quant, activation  as in moe_gated_linear, and with T up to the next multiple of 64: T * 2I,
+ *              T * K and K * 2I below 2^30.
+ *   dh         [T, I] bf16.    gu  [T, 2I] bf16.
+ *   dgu        [T, 2I] bf16 out; may be gu itself.
+ *   dx         [T, K] bf16 out, or NULL; needs w and w_scale (packed as for the forward call).
+ *   dw         [K, 2I] of dw_dtype (MOE_DTYPE_*) out, or NULL; needs xq and xs.
+ *   dbias      [2I] float32 out, or NULL.
+ *   All but dbias, xs and w_scale 16-byte aligned.
+ *   workspace  >= moe_gated_linear_backward_workspace_size(T, K, I, dx != NULL, dw != NULL, dbias != NULL)
+ *              bytes, 256-byte aligned (NULL where that is 0).
+ * Deterministic. */
+typedef struct moe_gated_linear_backward_args {
+    int32_t T, K, I;
+    const uint16_t* dh;
+    const uint16_t* gu;
+    int32_t         activation;
+    const uint8_t*  xq;
+    const uint8_t*  xs;
+    const uint8_t*  w;
+    const uint8_t*  w_scale;
+    int32_t         quant;
+    uint16_t*       dgu;
+    uint16_t*       dx;
+    void*           dw;
+    int32_t         dw_dtype;
+    float*          dbias;
+    void*           workspace;
+    size_t          workspace_bytes;
+    void*           stream;
+} moe_gated_linear_backward_args;
+int moe_gated_linear_backward(const moe_gated_linear_backward_args* a);
+size_t moe_gated_linear_backward_workspace_size(int32_t T, int32_t K, int32_t I, int32_t with_dx, int32_t with_dw,
+                                                int32_t with_dbias);
+
 /* moe_balance_loss: load-balance and z losses of a router, with per-expert counts.  The rows are
  * num_seqs packed sequences, sequence s in rows [seq_offsets[s], seq_offsets[s+1]); seq_offsets
  * NULL: one sequence of all T rows (num_seqs 1).  With T_s rows in sequence s, S' sequences that

@@ -14,7 +14,7 @@ from .binding import (  # noqa: F401
 )
 from .layer import (  # noqa: F401
     ACTIVATIONS, LinearWeights, MoeAddLayerNorm, MoeAddLayerNormBackward, MoeAddRmsNorm, MoeAddRmsNormBackward,
-    MoeBalanceLoss, MoeCombineBackward, MoeGatedLinear, MoeLinear, MoeRouteBackward, moe_add_layernorm, moe_add_layernorm_backward,
-    moe_add_rmsnorm, moe_gated_linear, moe_add_rmsnorm_backward, moe_balance_loss, moe_combine_backward, moe_linear,
-    moe_route_backward,
+    MoeBalanceLoss, MoeCombineBackward, MoeGatedLinear, MoeGatedLinearBackward, MoeLinear, MoeRouteBackward,
+    moe_add_layernorm, moe_add_layernorm_backward, moe_add_rmsnorm, moe_add_rmsnorm_backward, moe_balance_loss,
+    moe_combine_backward, moe_gated_linear, moe_gated_linear_backward, moe_linear, moe_route_backward,
 )

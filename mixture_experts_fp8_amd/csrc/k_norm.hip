@@ -584,6 +584,10 @@ static hipError_t launch_norm_backward(const NormBwdArgs& args, hipStream_t st) 
                        a.dw ? a.dw : a.db, a.part_b, a.db);
     return hipGetLastError();
 }
+hipError_t launch_column_sums(const float* part, int np, int n, float* out, hipStream_t st) {
+    hipLaunchKernelGGL(k_norm_dw, dim3((unsigned)ceil_div(n, 32)), dim3(256), 0, st, part, np, n, out, nullptr, nullptr);
+    return hipGetLastError();
+}
 hipError_t launch_add_rmsnorm_backward(const NormBwdArgs& a, hipStream_t st) { return launch_norm_backward<false>(a, st); }
 hipError_t launch_add_layernorm_backward(const NormBwdArgs& a, hipStream_t st) { return launch_norm_backward<true>(a, st); }
 

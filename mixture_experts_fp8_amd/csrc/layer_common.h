@@ -96,6 +96,25 @@ hipError_t launch_linear(const LinArgs& a, hipStream_t st);
 // y = act(gate) * up, bf16 [T, N / 2] without strides; no residual
 hipError_t launch_gated_linear(const LinArgs& a, hipStream_t st);
 
+struct GatedBwdArgs {
+    int T, K, I, act, mx, dw_bf16;
+    const uint16_t* dh;
+    const uint16_t* gu;
+    const uint8_t* xq;    // with dw
+    const uint8_t* xs;
+    const uint8_t* w;     // with dx
+    const uint8_t* wsc;
+    uint16_t* dgu;        // may be gu
+    uint16_t* dx;         // or NULL
+    void* dw;             // or NULL
+    float* dbias;         // or NULL
+    uint8_t* ws;          // laid out by gated_bwd_plan
+};
+hipError_t launch_gated_backward(const GatedBwdArgs& a, hipStream_t st);
+
+// out[c] = sum of the np rows of part [np][n], in a fixed order
+hipError_t launch_column_sums(const float* part, int np, int n, float* out, hipStream_t st);
+
 struct BalanceArgs {
     int T, E, k, S, scoring;
     const float* logits;

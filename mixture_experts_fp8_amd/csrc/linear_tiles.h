@@ -29,27 +29,30 @@ typedef unsigned v4u_t __attribute__((ext_vector_type(4)));
 // the activations below multiply by at most x exp(-|x|).
 __device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
 
+// The normal distribution function, which GELU multiplies v by.
+__device__ __forceinline__ float normal_cdf(float v) {
+    // exp(z^2) erfc(z) / 2 with z = |v| / sqrt 2 as a polynomial in t = 1 / (1 + 0.42 z): the minimax fit
+    // in relative error over z <= 9.4, 1.4e-7.  (A fit in absolute error loses the negative tail: 1e-2 of
+    // the value at v = -8.)  One term fewer: 1.0e-6.
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.296984851f, fabsf(v), 1.0f));
+    float p = fmaf(0.0352053866f, t, -0.160467133f);
+    p = fmaf(p, t, 0.220853359f);
+    p = fmaf(p, t, -0.0656716153f);
+    p = fmaf(p, t, 0.134549260f);
+    p = fmaf(p, t, 0.0973208472f);
+    p = fmaf(p, t, 0.119797952f);
+    p = fmaf(p, t, 0.118411876f);
+    const float c = p * t * __builtin_amdgcn_exp2f(v * v * -0.72134752f);     // erfc(z) / 2
+    return v < 0.f ? c : 1.0f - c;
+}
+
 // The activations take one or two transcendental instructions: with library exp, erfc and division
 // the epilogue of a 768-deep product cost as much as its K loop.
 __device__ __forceinline__ float act_fn(float v, int act) {
     switch (act) {
         case MOE_ACT_RELU: return v < 0.f ? 0.f : v;
         case MOE_ACT_SILU: return v * __builtin_amdgcn_rcpf(1.0f + exp_fast(-v));
-        case MOE_ACT_GELU: {
-            // exp(z^2) erfc(z) / 2 with z = |v| / sqrt 2 as a polynomial in t = 1 / (1 + 0.42 z): the minimax fit
-            // in relative error over z <= 9.4, 1.4e-7.  (A fit in absolute error loses the negative tail: 1e-2 of
-            // the value at v = -8.)  One term fewer: 1.0e-6.
-            const float t = __builtin_amdgcn_rcpf(fmaf(0.296984851f, fabsf(v), 1.0f));
-            float p = fmaf(0.0352053866f, t, -0.160467133f);
-            p = fmaf(p, t, 0.220853359f);
-            p = fmaf(p, t, -0.0656716153f);
-            p = fmaf(p, t, 0.134549260f);
-            p = fmaf(p, t, 0.0973208472f);
-            p = fmaf(p, t, 0.119797952f);
-            p = fmaf(p, t, 0.118411876f);
-            const float c = p * t * __builtin_amdgcn_exp2f(v * v * -0.72134752f);     // erfc(z) / 2
-            return v * (v < 0.f ? c : 1.0f - c);
-        }
+        case MOE_ACT_GELU: return v * normal_cdf(v);
         case MOE_ACT_GELU_TANH: {   // (1 + tanh u) / 2 = 1 / (1 + exp(-2 u))
             const float u = 0.79788456f * fmaf(0.044715f * v * v, v, v);
             return v * __builtin_amdgcn_rcpf(1.0f + exp_fast(-2.0f * u));

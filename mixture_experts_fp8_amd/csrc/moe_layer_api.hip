@@ -74,6 +74,19 @@ int moe_gated_linear(const moe_gated_linear_args* a) {
     return done("moe_gated_linear", moe::launch_gated_linear(l, static_cast<hipStream_t>(a->stream)));
 }
 
+size_t moe_gated_linear_backward_workspace_size(int32_t T, int32_t K, int32_t I, int32_t with_dx, int32_t with_dw,
+                                                int32_t with_dbias) {
+    return T < 1 || K < 1 || I < 1 ? 0 : moe::gated_bwd_plan(T, K, I, with_dx, with_dw, with_dbias).end;
+}
+
+int moe_gated_linear_backward(const moe_gated_linear_backward_args* a) {
+    if (int rc = moe::host::check_gated_linear_backward(a)) return rc;
+    const moe::GatedBwdArgs g{a->T, a->K, a->I, a->activation, a->quant == MOE_QUANT_MXFP8, a->dw_dtype == MOE_DTYPE_BF16,
+                              a->dh, a->gu, a->xq, a->xs, a->w, a->w_scale, a->dgu, a->dx, a->dw, a->dbias,
+                              static_cast<uint8_t*>(a->workspace)};
+    return done("moe_gated_linear_backward", moe::launch_gated_backward(g, static_cast<hipStream_t>(a->stream)));
+}
+
 size_t moe_balance_loss_workspace_size(int32_t T, int32_t E, int32_t num_seqs) {
     return T < 1 || E < 1 || num_seqs < 1 ? 0 : moe::balance_plan(T, E, num_seqs).end;
 }

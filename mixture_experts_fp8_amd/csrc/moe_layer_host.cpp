@@ -45,6 +45,25 @@ BalancePlan balance_plan(int T, int E, int S) {
     return p;
 }
 
+GatedBwdPlan gated_bwd_plan(int T, int K, int I, bool dx, bool dw, bool dbias) {
+    GatedBwdPlan p;
+    p.row_blocks = (int)cdiv(T, 64);
+    p.parts = std::min(p.row_blocks, 256);
+    const size_t N = 2 * (size_t)I, rows = 64 * (size_t)p.row_blocks;
+    size_t o = 0;
+    auto take = [&](bool on, size_t n) {
+        const size_t r = o;
+        if (on) o += align256(n);
+        return r;
+    };
+    p.part = take(dbias, p.parts * N * 4);
+    p.weights = take(dx, K * N * 2);
+    p.rows = take(dw, K * rows * 2);
+    p.dgu_packed = take(dw, N * rows * 2);
+    p.end = o;
+    return p;
+}
+
 namespace host {
 namespace {
 
@@ -312,6 +331,49 @@ int check_gated_linear(const moe_gated_linear_args* a) {
     for (int i = 0; i < 2; ++i)
         for (int j = 0; j < 5; ++j)
             if ((rc = check_io(op, out[i], in[j]))) return rc;
+    return MOE_OK;
+}
+
+int check_gated_linear_backward(const moe_gated_linear_backward_args* a) {
+    const char* op = "moe_gated_linear_backward";
+    if (!a) return fail(MOE_ERR_INVALID, "%s: args must not be NULL", op);
+    const int T = a->T, K = a->K, I = a->I;
+    if (T < 1 || K < 1 || I < 1) return fail(MOE_ERR_INVALID, "%s: T, K, I (%d, %d, %d) must be > 0", op, T, K, I);
+    if (I % 32) return fail(MOE_ERR_UNSUPPORTED, "%s: I (%d) must be a multiple of 32", op, I);
+    const int64_t N = 2 * (int64_t)I, rows = cdiv(T, 64) * 64;
+    int rc = check_gated(op, T, K, N, a->quant, a->activation);
+    if (rc) return rc;
+    if (rows * N >= ((int64_t)1 << 30) || rows * K >= ((int64_t)1 << 30) || K * N >= ((int64_t)1 << 30))
+        return fail(MOE_ERR_UNSUPPORTED, "%s: T * 2I, T * K (T up to a multiple of 64) and K * 2I must be below 2^30", op);
+    if (!a->dh || !a->gu || !a->dgu) return fail(MOE_ERR_INVALID, "%s: dh, gu and dgu must not be NULL", op);
+    if (a->dx && (!a->w || !a->w_scale)) return fail(MOE_ERR_INVALID, "%s: dx needs w and w_scale", op);
+    if (a->dw && (!a->xq || !a->xs)) return fail(MOE_ERR_INVALID, "%s: dw needs xq and xs", op);
+    if (a->dw && a->dw_dtype != MOE_DTYPE_F32 && a->dw_dtype != MOE_DTYPE_BF16)
+        return fail(MOE_ERR_INVALID, "%s: dw_dtype (%d) must be MOE_DTYPE_F32 or MOE_DTYPE_BF16", op, a->dw_dtype);
+    if (!aligned(a->dh, 16) || !aligned(a->gu, 16) || !aligned(a->dgu, 16) || !aligned(a->dx, 16) || !aligned(a->dw, 16) ||
+        !aligned(a->xq, 16) || !aligned(a->w, 16))
+        return fail(MOE_ERR_UNSUPPORTED, "%s: dh, gu, dgu, dx, dw, xq and w must be 16-byte aligned", op);
+    const bool mx = a->quant == MOE_QUANT_MXFP8;
+    if (mx && (!aligned(a->xs, 4) || !aligned(a->w_scale, 4)))
+        return fail(MOE_ERR_UNSUPPORTED, "%s: xs and w_scale must be 4-byte aligned for MOE_QUANT_MXFP8", op);
+    if (!aligned(a->dbias, 4)) return fail(MOE_ERR_INVALID, "%s: dbias must be 4-byte aligned", op);
+    const size_t need = gated_bwd_plan(T, K, I, a->dx, a->dw, a->dbias).end;
+    if ((rc = check_ws(op, a->workspace, a->workspace_bytes, need))) return rc;
+    const Span out[5] = {{"dgu", a->dgu, (uint64_t)T * N * 2},
+                         {"dx", a->dx, (uint64_t)T * K * 2},
+                         {"dw", a->dw, (uint64_t)K * N * (a->dw_dtype == MOE_DTYPE_BF16 ? 2 : 4)},
+                         {"dbias", a->dbias, (uint64_t)N * 4},
+                         {"workspace", need ? a->workspace : nullptr, need}};
+    const Span in[6] = {{"gu", a->gu, (uint64_t)T * N * 2},
+                        {"dh", a->dh, (uint64_t)T * I * 2},
+                        {"xq", a->dw ? a->xq : nullptr, (uint64_t)T * K},
+                        {"xs", a->dw ? a->xs : nullptr, (uint64_t)T * (K / (mx ? 32 : 128))},
+                        {"w", a->dx ? a->w : nullptr, (uint64_t)K * N},
+                        {"w_scale", a->dx ? a->w_scale : nullptr, mx ? (uint64_t)K * N / 32 : (uint64_t)(K / 128) * cdiv(N, 128)}};
+    if ((rc = check_outputs(op, out, 5))) return rc;
+    for (int i = 0; i < 5; ++i)
+        for (int j = 0; j < 6; ++j)
+            if ((rc = check_io(op, out[i], in[j], i == 0 && j == 0))) return rc;
     return MOE_OK;
 }
 

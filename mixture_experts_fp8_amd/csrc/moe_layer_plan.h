@@ -19,6 +19,13 @@ struct BalancePlan {
 };
 BalancePlan balance_plan(int T, int E, int S);
 
+// ---- gated block backward: operands of its bf16 products, and partial rows of the bias's gradient
+struct GatedBwdPlan {
+    int row_blocks, parts;                             // blocks of 64 rows; partial rows [parts][2I] floats
+    size_t part, weights, rows, dgu_packed, end;       // byte offsets; a part that is not needed takes nothing
+};
+GatedBwdPlan gated_bwd_plan(int T, int K, int I, bool dx, bool dw, bool dbias);
+
 namespace host {
 int check_add_rmsnorm(const moe_add_rmsnorm_args* a);
 int check_add_rmsnorm_backward(const moe_add_rmsnorm_backward_args* a);
@@ -26,6 +33,7 @@ int check_add_layernorm(const moe_add_layernorm_args* a);
 int check_add_layernorm_backward(const moe_add_layernorm_backward_args* a);
 int check_linear(const moe_linear_args* a);
 int check_gated_linear(const moe_gated_linear_args* a);
+int check_gated_linear_backward(const moe_gated_linear_backward_args* a);
 int check_balance_loss(const moe_balance_loss_args* a);
 int check_route_backward(const moe_route_backward_args* a);
 int check_combine_backward(const moe_combine_backward_args* a);

@@ -59,6 +59,12 @@ class GatedLinearArgs(ctypes.Structure):
                 ("bias", _vp), ("activation", _i32), ("h", _vp), ("gu", _vp), ("quant", _i32), ("stream", _vp)]
 
 
+class GatedLinearBackwardArgs(ctypes.Structure):
+    _fields_ = [("T", _i32), ("K", _i32), ("I", _i32), ("dh", _vp), ("gu", _vp), ("activation", _i32), ("xq", _vp),
+                ("xs", _vp), ("w", _vp), ("w_scale", _vp), ("quant", _i32), ("dgu", _vp), ("dx", _vp), ("dw", _vp),
+                ("dw_dtype", _i32), ("dbias", _vp), ("workspace", _vp), ("workspace_bytes", _sz), ("stream", _vp)]
+
+
 class BalanceLossArgs(ctypes.Structure):
     _fields_ = [("route", ctypes.POINTER(RouteParams)), ("T", _i32), ("num_seqs", _i32), ("router_logits", _vp),
                 ("topk_ids", _vp), ("seq_offsets", _vp), ("balance_coef", _f32), ("z_coef", _f32), ("losses", _vp),
@@ -421,6 +427,65 @@ def moe_gated_linear(xq: torch.Tensor, xs: torch.Tensor, w: LinearWeights, activ
                      want_gu: bool = False, h: Optional[torch.Tensor] = None) -> dict:
     """One call of MoeGatedLinear."""
     return MoeGatedLinear(xq, xs, w, activation, want_gu, h)()
+
+
+class MoeGatedLinearBackward(_Call):
+    """Gradients of MoeGatedLinear from dh bf16 [T, I] and its gu bf16 [T, 2I].
+
+    w: the forward call's weights.  want_dx: the input's gradient.  want_dw: the weights' values' gradient,
+    [K, 2I] of dw_dtype (float32 or bfloat16), from the forward call's xq and xs; by default where those are
+    given.  want_dbias: the bias's; by default where w has one.  dgu: the tensor that receives the sums'
+    gradient (it may be gu itself).  A call returns {"dgu", "dx", "dw", "dbias"}, None for what is not
+    computed."""
+
+    def __init__(self, dh: torch.Tensor, gu: torch.Tensor, w: LinearWeights, xq: Optional[torch.Tensor] = None,
+                 xs: Optional[torch.Tensor] = None, activation: str = "silu", want_dx: bool = True,
+                 want_dw: Optional[bool] = None, want_dbias: Optional[bool] = None, dw_dtype=torch.float32,
+                 dgu: Optional[torch.Tensor] = None):
+        T, K, N = dh.shape[0], w.K, w.N
+        if N % 2:
+            raise ValueError(f"w: expected an even number of columns, got {N}")
+        _need(dh, "dh", torch.bfloat16, (T, N // 2))
+        _need(gu, "gu", torch.bfloat16, (T, N))
+        act = _need_activation(activation)
+        _need_weights(w)
+        want_dw = xq is not None if want_dw is None else want_dw
+        want_dbias = w.bias is not None if want_dbias is None else want_dbias
+        if want_dw:
+            if xq is None or xs is None:
+                raise ValueError("dw needs xq and xs")
+            _gated_shape(xq, xs, w, T)
+        if dw_dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"dw_dtype: expected float32 or bfloat16, got {dw_dtype}")
+        dev = dh.device
+        dgu = torch.empty_like(gu) if dgu is None else dgu
+        _need(dgu, "dgu", torch.bfloat16, (T, N))
+        dx = torch.empty(T, K, dtype=torch.bfloat16, device=dev) if want_dx else None
+        dw = torch.empty(K, N, dtype=dw_dtype, device=dev) if want_dw else None
+        db = torch.empty(N, dtype=torch.float32, device=dev) if want_dbias else None
+        nbytes = lib().moe_gated_linear_backward_workspace_size(T, K, N // 2, int(want_dx), int(want_dw), int(want_dbias))
+        ws = workspace(nbytes, dev) if nbytes else None
+        dt = B.MOE_DTYPE_F32 if dw_dtype == torch.float32 else B.MOE_DTYPE_BF16
+        self.out = {"dgu": dgu, "dx": dx, "dw": dw, "dbias": db}
+        if not want_dw:
+            xq = xs = None
+        self._hold("moe_gated_linear_backward",
+                   GatedLinearBackwardArgs(T, K, N // 2, _ptr(dh), _ptr(gu), act, _ptr(xq), _ptr(xs), _ptr(w.w),
+                                           _ptr(w.w_scale), w.quant, _ptr(dgu), _ptr(dx), _ptr(dw), dt, _ptr(db), _ptr(ws),
+                                           ws.numel() if ws is not None else 0, None),
+                   (dh, gu, xq, xs, w.w, w.w_scale, dgu, dx, dw, db, ws))
+
+    def __call__(self, stream: Optional[int] = None) -> dict:
+        self._run(stream)
+        return self.out
+
+
+def moe_gated_linear_backward(dh: torch.Tensor, gu: torch.Tensor, w: LinearWeights, xq: Optional[torch.Tensor] = None,
+                              xs: Optional[torch.Tensor] = None, activation: str = "silu", want_dx: bool = True,
+                              want_dw: Optional[bool] = None, want_dbias: Optional[bool] = None,
+                              dw_dtype=torch.float32) -> dict:
+    """One call of MoeGatedLinearBackward."""
+    return MoeGatedLinearBackward(dh, gu, w, xq, xs, activation, want_dx, want_dw, want_dbias, dw_dtype)()
 
 
 def _router_inputs(params: RouteParams, logits: torch.Tensor, ids: Optional[torch.Tensor],

@@ -8,9 +8,10 @@ with central differences of the forward functions here; closed forms and hand va
 """
 from __future__ import annotations
 
+import math
+
 import numpy as np
 
-from .layer import activation
 from .w8a16 import bf16_rne
 
 
@@ -44,6 +45,50 @@ def layernorm_backward(dy, h, weight, eps, dh=None):
 
 
 # ---- gated feed-forward block ------------------------------------------------------------
+_erfc = np.vectorize(math.erfc, otypes=[np.float64])
+
+
+def _factor(v, name):
+    """(p, q, slope of the logistic's argument): the activation is v p, and q = 1 - p.  1 + tanh(t) is formed as
+    2 / (1 + exp(-2 t)) and 1 + erf(t) as erfc(-t): their sums lose every digit far below 0."""
+    with np.errstate(over="ignore"):
+        if name == "silu":
+            return 1.0 / (1.0 + np.exp(-v)), 1.0 / (1.0 + np.exp(v)), np.ones_like(v)
+        c = 2.0 * math.sqrt(2.0 / math.pi)
+        t = c * (v + 0.044715 * v ** 3)
+        return 1.0 / (1.0 + np.exp(-t)), 1.0 / (1.0 + np.exp(t)), c * (1.0 + 3 * 0.044715 * v * v)
+
+
+def activation(v, name):
+    v = np.asarray(v, dtype=np.float64)
+    if name == "none":
+        return v
+    if name == "relu":
+        return np.maximum(v, 0.0)
+    if name == "gelu":
+        return 0.5 * v * _erfc(-v / math.sqrt(2.0))
+    if name in ("silu", "gelu_tanh"):
+        return v * _factor(v, name)[0]
+    raise ValueError(name)
+
+
+def activation_slope(v, name):
+    """(slope, sum of the absolute values of its terms)."""
+    v = np.asarray(v, dtype=np.float64)
+    if name == "none":
+        return np.ones_like(v), np.ones_like(v)
+    if name == "relu":
+        return (v > 0).astype(np.float64), np.ones_like(v)
+    if name == "gelu":
+        p, b = 0.5 * _erfc(-v / math.sqrt(2.0)), v * np.exp(-0.5 * v * v) / math.sqrt(2.0 * math.pi)
+    elif name in ("silu", "gelu_tanh"):
+        p, q, s = _factor(v, name)
+        b = v * p * q * s
+    else:
+        raise ValueError(name)
+    return p + b, p + np.abs(b)
+
+
 def gated(x, w, bias=None, act="silu"):
     """(h, g, u) from the operands' values; w: gate columns, then up columns."""
     v = x @ w
@@ -51,3 +96,10 @@ def gated(x, w, bias=None, act="silu"):
         v = v + bias
     g, u = np.split(v, 2, axis=1)
     return activation(g, act) * u, g, u
+
+
+def gated_backward(dh, g, u, act):
+    """(dgu, magnitude) before the rounding to bf16."""
+    s, smag = activation_slope(g, act)
+    a = activation(g, act)
+    return np.concatenate([dh * u * s, dh * a], 1), np.concatenate([np.abs(dh * u) * smag, np.abs(dh * a)], 1)

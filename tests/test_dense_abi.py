@@ -44,7 +44,8 @@ def test_add_layernorm_backward_refuses(over, code, needle):
     assert needle in M.moe_last_error() and "moe_add_layernorm_backward" in M.moe_last_error()
 
 
-@pytest.mark.parametrize("name", ["moe_add_layernorm", "moe_add_layernorm_backward", "moe_gated_linear"])
+@pytest.mark.parametrize("name", ["moe_add_layernorm", "moe_add_layernorm_backward", "moe_gated_linear",
+                                  "moe_gated_linear_backward"])
 def test_null_arguments(name):
     assert getattr(M.lib(), name)(None) == B.MOE_ERR_INVALID
     assert name in M.moe_last_error()
@@ -68,3 +69,25 @@ GATED = dict(T=4, K=256, I=96, xq=at(0), xs=at(1), w=at(2), w_scale=at(3), bias=
 def test_gated_linear_refuses(over, code, needle):
     assert call("moe_gated_linear", L.GatedLinearArgs, GATED, **over) == code
     assert needle in M.moe_last_error() and "moe_gated_linear" in M.moe_last_error()
+
+
+GBWD = dict(T=4, K=256, I=96, dh=at(0), gu=at(1), activation=2, xq=at(2), xs=at(3), w=at(4), w_scale=at(5), quant=0, dgu=at(6),
+            dx=at(7), dw=at(8), dw_dtype=0, dbias=at(9), workspace=at(10), workspace_bytes=1 << 30)
+
+
+@pytest.mark.parametrize("over,code,needle", [
+    (dict(T=0), B.MOE_ERR_INVALID, "T, K, I"), (dict(K=200), B.MOE_ERR_UNSUPPORTED, "multiple of 128"),
+    (dict(I=48), B.MOE_ERR_UNSUPPORTED, "multiple of 32"), (dict(T=1 << 22), B.MOE_ERR_UNSUPPORTED, "2^30"),
+    (dict(quant=3), B.MOE_ERR_UNSUPPORTED, "quant"), (dict(activation=7), B.MOE_ERR_INVALID, "activation"),
+    (dict(dgu=None), B.MOE_ERR_INVALID, "dgu"), (dict(gu=None), B.MOE_ERR_INVALID, "gu"),
+    (dict(w=None), B.MOE_ERR_INVALID, "dx needs"), (dict(xs=None), B.MOE_ERR_INVALID, "dw needs"),
+    (dict(dw_dtype=2), B.MOE_ERR_INVALID, "dw_dtype"), (dict(dx=at(7, 8)), B.MOE_ERR_UNSUPPORTED, "16-byte"),
+    (dict(dbias=at(9, 2)), B.MOE_ERR_INVALID, "dbias"), (dict(workspace=None), B.MOE_ERR_WORKSPACE, "workspace"),
+    (dict(workspace_bytes=1000), B.MOE_ERR_WORKSPACE, "need"), (dict(workspace=at(10, 128)), B.MOE_ERR_INVALID, "256-byte"),
+    (dict(dgu=at(0)), B.MOE_ERR_INVALID, "dgu must not overlap dh"), (dict(dgu=at(1, 256)), B.MOE_ERR_INVALID, "dgu must not overlap gu"),
+    (dict(dx=at(1)), B.MOE_ERR_INVALID, "dx must not overlap gu"), (dict(dw=at(7)), B.MOE_ERR_INVALID, "dx and dw"),
+    (dict(dw=at(4)), B.MOE_ERR_INVALID, "dw must not overlap w"), (dict(workspace=at(2)), B.MOE_ERR_INVALID, "workspace must not overlap xq"),
+])
+def test_gated_linear_backward_refuses(over, code, needle):
+    assert call("moe_gated_linear_backward", L.GatedLinearBackwardArgs, GBWD, **over) == code
+    assert needle in M.moe_last_error() and "moe_gated_linear_backward" in M.moe_last_error()
