@@ -13,8 +13,9 @@ from .binding import (  # noqa: F401
     QUANT_SCHEMES, MOE_FUSED_EXPERT_OUT_BF16, MOE_FUSED_SHARED_EXPERT, moe_fused_static, MOE_STATIC_SCRATCH_BYTES,
 )
 from .layer import (  # noqa: F401
-    ACTIVATIONS, LinearWeights, MoeAddLayerNorm, MoeAddLayerNormBackward, MoeAddRmsNorm, MoeAddRmsNormBackward,
-    MoeBalanceLoss, MoeCombineBackward, MoeGatedLinear, MoeGatedLinearBackward, MoeLinear, MoeRouteBackward,
-    moe_add_layernorm, moe_add_layernorm_backward, moe_add_rmsnorm, moe_add_rmsnorm_backward, moe_balance_loss,
-    moe_combine_backward, moe_gated_linear, moe_gated_linear_backward, moe_linear, moe_route_backward,
+    ACTIVATIONS, LinearWeights, LoraWeights, MoeAddLayerNorm, MoeAddLayerNormBackward, MoeAddRmsNorm,
+    MoeAddRmsNormBackward, MoeBalanceLoss, MoeCombineBackward, MoeGatedLinear, MoeGatedLinearBackward, MoeLinear, MoeLora,
+    MoeRouteBackward, moe_add_layernorm, moe_add_layernorm_backward, moe_add_rmsnorm, moe_add_rmsnorm_backward,
+    moe_balance_loss, moe_combine_backward, moe_gated_linear, moe_gated_linear_backward, moe_linear, moe_lora,
+    moe_route_backward,
 )

@@ -36,7 +36,7 @@ EXPORTED = ["moe_route", "moe_route_workspace_size", "moe_quant_act", "moe_quant
             "moe_add_rmsnorm_backward_workspace_size", "moe_linear", "moe_linear_workspace_size", "moe_balance_loss",
             "moe_balance_loss_workspace_size", "moe_route_backward", "moe_combine_backward", "moe_add_layernorm",
             "moe_add_layernorm_backward", "moe_add_layernorm_backward_workspace_size", "moe_gated_linear",
-            "moe_gated_linear_backward", "moe_gated_linear_backward_workspace_size"]
+            "moe_gated_linear_backward", "moe_gated_linear_backward_workspace_size", "moe_lora", "moe_lora_workspace_size"]
 MOE_STATIC_SCRATCH_BYTES = 64 << 20
 
 
@@ -129,12 +129,13 @@ def lib() -> ctypes.CDLL:
         L.moe_prepack_weights_mx.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp, vp]
         for name in ("moe_add_rmsnorm", "moe_add_rmsnorm_backward", "moe_linear", "moe_balance_loss",
                      "moe_route_backward", "moe_combine_backward", "moe_add_layernorm",
-                     "moe_add_layernorm_backward", "moe_gated_linear", "moe_gated_linear_backward"):   # one argument struct each (layer.py)
+                     "moe_add_layernorm_backward", "moe_gated_linear", "moe_gated_linear_backward", "moe_lora"):   # one argument struct each (layer.py)
             getattr(L, name).restype = ctypes.c_int
             getattr(L, name).argtypes = [vp]
         for name, n in (("moe_add_rmsnorm_backward_workspace_size", 2),
                         ("moe_add_layernorm_backward_workspace_size", 2), ("moe_linear_workspace_size", 4),
-                        ("moe_balance_loss_workspace_size", 3), ("moe_gated_linear_backward_workspace_size", 6)):
+                        ("moe_balance_loss_workspace_size", 3), ("moe_gated_linear_backward_workspace_size", 6),
+                        ("moe_lora_workspace_size", 5)):
             getattr(L, name).restype = sz
             getattr(L, name).argtypes = [i32] * n
         _lib = L

@@ -115,6 +115,21 @@ hipError_t launch_gated_backward(const GatedBwdArgs& a, hipStream_t st);
 // out[c] = sum of the np rows of part [np][n], in a fixed order
 hipError_t launch_column_sums(const float* part, int np, int n, float* out, hipStream_t st);
 
+struct LoraArgs {
+    int T, K, R, n, S;    // n adapters, S sequences
+    const uint16_t* x;
+    int64_t ldx;
+    const uint16_t* a;    // [n][R][K]
+    const uint16_t* b;    // [n][N][R]
+    const float* scale;   // [n] or NULL: 1
+    const int32_t* ids;   // [S]
+    const int32_t* off;   // [S + 1] or NULL: a sequence per row
+    float* v;             // workspace: [parts][T][ldv]
+    LinArgs out;          // N, residual, y
+    int ldv = 0, parts = 0, chunks = 0;   // set by launch_lora
+};
+hipError_t launch_lora(const LoraArgs& a, hipStream_t st);
+
 struct BalanceArgs {
     int T, E, k, S, scoring;
     const float* logits;

@@ -702,22 +702,27 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_tile(LinArgs a, int 
     else tile_finish<MI>(a, acc, bias, res, row0, col0);
 }
 
-// Launches a tiled kernel.  More than 64 KB of LDS has to be asked for, once per kernel and device.
+// More than 64 KB of LDS has to be asked for, once per kernel and device.
 constexpr int kLdsBytes = 160 * 1024;
 template <auto Kern>
-static hipError_t launch_tiles(const LinArgs& a, int tm, int tn, int threads, size_t lds, hipStream_t st) {
-    if (lds > 64 * 1024) {
-        static std::atomic<uint64_t> asked{0};   // a bit per device
-        int dev = 0;
-        hipError_t e = hipGetDevice(&dev);
+static hipError_t ask_for_lds(size_t lds) {
+    if (lds <= 64 * 1024) return hipSuccess;
+    static std::atomic<uint64_t> asked{0};   // a bit per device
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev > 63 || !(asked.load(std::memory_order_relaxed) & bit)) {
+        e = hipFuncSetAttribute(reinterpret_cast<const void*>(Kern), hipFuncAttributeMaxDynamicSharedMemorySize, kLdsBytes);
         if (e != hipSuccess) return e;
-        const uint64_t bit = 1ull << (dev & 63);
-        if (dev > 63 || !(asked.load(std::memory_order_relaxed) & bit)) {
-            e = hipFuncSetAttribute(reinterpret_cast<const void*>(Kern), hipFuncAttributeMaxDynamicSharedMemorySize, kLdsBytes);
-            if (e != hipSuccess) return e;
-            asked.fetch_or(bit, std::memory_order_relaxed);
-        }
+        asked.fetch_or(bit, std::memory_order_relaxed);
     }
+    return hipSuccess;
+}
+// Launches a tiled kernel.
+template <auto Kern>
+static hipError_t launch_tiles(const LinArgs& a, int tm, int tn, int threads, size_t lds, hipStream_t st) {
+    if (const hipError_t e = ask_for_lds<Kern>(lds); e != hipSuccess) return e;
     hipLaunchKernelGGL(Kern, dim3((unsigned)(ceil_div((int64_t)tm * tn, 8) * 8)), dim3(threads), lds, st, a, tm, tn);
     return hipGetLastError();
 }

@@ -64,6 +64,17 @@ GatedBwdPlan gated_bwd_plan(int T, int K, int I, bool dx, bool dw, bool dbias) {
     return p;
 }
 
+LoraPlan lora_plan(int T, int K, int R, int S) {
+    LoraPlan p;
+    p.window = S && T / S >= 32 ? 64 : 16;
+    p.slots = S ? cdiv(T, p.window) + S : T;
+    p.ldv = (int)cdiv(R, 16) * 16;
+    const int64_t groups = p.slots * cdiv(R, 64);
+    p.parts = (int)std::max<int64_t>(1, std::min<int64_t>(256 / groups, K / 64 / 16));
+    p.end = align256((size_t)p.parts * T * p.ldv * 4);
+    return p;
+}
+
 namespace host {
 namespace {
 
@@ -137,6 +148,18 @@ int check_router(const char* op, const moe_route_params* p, int T, int S, const 
     if (!std::isfinite(ca) || !std::isfinite(cz))
         return fail(MOE_ERR_INVALID, "%s: balance_coef and z_coef must be finite", op);
     return MOE_OK;
+}
+
+// y [.., N] may be the residual itself, or other columns of one matrix's rows: side by side their spans meet,
+// they do not.
+int check_residual(const char* op, const Span& y, const Span& res, int64_t ld_y, int64_t ld_res, int N, int size) {
+    if (res.p && ld_res == ld_y) {
+        const uint64_t row = (uint64_t)ld_y * size, used = (uint64_t)N * size;
+        const uintptr_t p = (uintptr_t)y.p, q = (uintptr_t)res.p;
+        const uint64_t d = (p > q ? p - q : q - p) % row;
+        if (p != q && d >= used && row - d >= used) return MOE_OK;
+    }
+    return check_io(op, y, res, ld_res == ld_y);
 }
 
 // Scheme, depth and activation of a gated block's products of T rows, N = 2I wide.
@@ -291,15 +314,7 @@ int check_linear(const moe_linear_args* a) {
                         {"residual", a->residual, a->residual ? span2(T, N, a->ld_residual, size) : 0}};
     for (int i = 0; i < 5; ++i)
         if (int rc = check_io(op, y, in[i])) return rc;
-    // y and residual may be columns side by side in the rows of one matrix: their spans meet, they do not
-    if (a->residual && a->ld_residual == a->ld_y) {
-        const uint64_t row = (uint64_t)a->ld_y * size, used = (uint64_t)N * size;
-        const uint64_t d = ((uintptr_t)a->y > (uintptr_t)a->residual ? (uintptr_t)a->y - (uintptr_t)a->residual
-                                                                     : (uintptr_t)a->residual - (uintptr_t)a->y) % row;
-        if (a->y != a->residual && d >= used && row - d >= used) return MOE_OK;
-    }
-    if (int rc = check_io(op, y, in[5], a->ld_residual == a->ld_y)) return rc;
-    return MOE_OK;
+    return check_residual(op, y, in[5], a->ld_y, a->ld_residual, N, size);
 }
 
 int check_gated_linear(const moe_gated_linear_args* a) {
@@ -375,6 +390,55 @@ int check_gated_linear_backward(const moe_gated_linear_backward_args* a) {
         for (int j = 0; j < 6; ++j)
             if ((rc = check_io(op, out[i], in[j], i == 0 && j == 0))) return rc;
     return MOE_OK;
+}
+
+int check_lora(const moe_lora_args* a) {
+    const char* op = "moe_lora";
+    if (!a) return fail(MOE_ERR_INVALID, "%s: args must not be NULL", op);
+    const int T = a->T, K = a->K, N = a->N, R = a->R, S = a->num_seqs;
+    if (T < 1 || K < 1 || N < 1 || R < 1)
+        return fail(MOE_ERR_INVALID, "%s: T, K, N, R (%d, %d, %d, %d) must be > 0", op, T, K, N, R);
+    if (a->num_adapters < 1) return fail(MOE_ERR_INVALID, "%s: num_adapters (%d) must be > 0", op, a->num_adapters);
+    if (K % 8 || R % 8 || N % 16)
+        return fail(MOE_ERR_UNSUPPORTED, "%s: K (%d) and R (%d) must be multiples of 8, N (%d) of 16", op, K, R, N);
+    if (R > 256) return fail(MOE_ERR_UNSUPPORTED, "%s: R (%d) must not exceed 256", op, R);
+    if (K > 65536 || N > (1 << 20))
+        return fail(MOE_ERR_UNSUPPORTED, "%s: K (%d) must not exceed 65536, N (%d) %d", op, K, N, 1 << 20);
+    if (S < 1) return fail(MOE_ERR_INVALID, "%s: num_seqs (%d) must be > 0", op, S);
+    if (!a->seq_offsets && S != T)
+        return fail(MOE_ERR_INVALID, "%s: num_seqs (%d) must be T (%d) without seq_offsets", op, S, T);
+    if (S > (1 << 20) || T > (1 << 23))
+        return fail(MOE_ERR_UNSUPPORTED, "%s: num_seqs (%d) must not exceed %d, T (%d) %d", op, S, 1 << 20, T, 1 << 23);
+    if (!a->x || !a->a || !a->b || !a->adapter_ids || !a->y)
+        return fail(MOE_ERR_INVALID, "%s: x, a, b, adapter_ids and y must not be NULL", op);
+    if (a->out_dtype != MOE_DTYPE_F32 && a->out_dtype != MOE_DTYPE_BF16)
+        return fail(MOE_ERR_INVALID, "%s: out_dtype (%d) must be MOE_DTYPE_F32 or MOE_DTYPE_BF16", op, a->out_dtype);
+    if (a->ld_x < K) return fail(MOE_ERR_INVALID, "%s: ld_x (%lld) must be >= K (%d)", op, (long long)a->ld_x, K);
+    if (a->ld_y < N || (a->residual && a->ld_residual < N))
+        return fail(MOE_ERR_INVALID, "%s: ld_y (%lld) and ld_residual (%lld) must be >= N (%d)", op, (long long)a->ld_y,
+                    (long long)a->ld_residual, N);
+    if (a->ld_x % 8 || a->ld_y % 8 || (a->residual && a->ld_residual % 8) || !aligned(a->x, 16) || !aligned(a->y, 16) ||
+        !aligned(a->residual, 16) || !aligned(a->a, 16) || !aligned(a->b, 16))
+        return fail(MOE_ERR_UNSUPPORTED, "%s: x, a, b, residual and y must be 16-byte aligned, rows a multiple of 8 "
+                    "elements apart", op);
+    const size_t need = lora_plan(T, K, R, a->seq_offsets ? S : 0).end;
+    int rc = check_ws(op, a->workspace, a->workspace_bytes, need);
+    if (rc) return rc;
+    const int size = a->out_dtype == MOE_DTYPE_BF16 ? 2 : 4;
+    const uint64_t n = a->num_adapters;
+    const Span out[2] = {{"y", a->y, span2(T, N, a->ld_y, size)}, {"workspace", a->workspace, need}};
+    const Span in[6] = {{"scale", a->scale, n * 4},
+                        {"adapter_ids", a->adapter_ids, (uint64_t)S * 4},
+                        {"seq_offsets", a->seq_offsets, (uint64_t)(S + 1) * 4},
+                        {"x", a->x, span2(T, K, a->ld_x, 2)},
+                        {"a", a->a, n * R * K * 2},
+                        {"b", a->b, n * N * R * 2}};
+    const Span res{"residual", a->residual, a->residual ? span2(T, N, a->ld_residual, size) : 0};
+    if ((rc = check_words(op, in, 3)) || (rc = check_outputs(op, out, 2)) || (rc = check_io(op, out[1], res))) return rc;
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 6; ++j)
+            if ((rc = check_io(op, out[i], in[j]))) return rc;
+    return check_residual(op, out[0], res, a->ld_y, a->ld_residual, N, size);
 }
 
 int check_balance_loss(const moe_balance_loss_args* a) {

@@ -26,6 +26,14 @@ struct GatedBwdPlan {
 };
 GatedBwdPlan gated_bwd_plan(int T, int K, int I, bool dx, bool dw, bool dbias);
 
+// ---- adapters: rows of one sequence in one window are a slot; a slot's sum over K may be split
+struct LoraPlan {
+    int window, parts, ldv;   // rows of a window; partial sums; floats of a row of them
+    int64_t slots;
+    size_t end;               // workspace bytes
+};
+LoraPlan lora_plan(int T, int K, int R, int S);   // S = 0: a sequence per row
+
 namespace host {
 int check_add_rmsnorm(const moe_add_rmsnorm_args* a);
 int check_add_rmsnorm_backward(const moe_add_rmsnorm_backward_args* a);
@@ -34,6 +42,7 @@ int check_add_layernorm_backward(const moe_add_layernorm_backward_args* a);
 int check_linear(const moe_linear_args* a);
 int check_gated_linear(const moe_gated_linear_args* a);
 int check_gated_linear_backward(const moe_gated_linear_backward_args* a);
+int check_lora(const moe_lora_args* a);
 int check_balance_loss(const moe_balance_loss_args* a);
 int check_route_backward(const moe_route_backward_args* a);
 int check_combine_backward(const moe_combine_backward_args* a);

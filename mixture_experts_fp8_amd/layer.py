@@ -65,6 +65,13 @@ class GatedLinearBackwardArgs(ctypes.Structure):
                 ("dw_dtype", _i32), ("dbias", _vp), ("workspace", _vp), ("workspace_bytes", _sz), ("stream", _vp)]
 
 
+class LoraArgs(ctypes.Structure):
+    _fields_ = [("T", _i32), ("K", _i32), ("N", _i32), ("R", _i32), ("num_adapters", _i32), ("num_seqs", _i32), ("x", _vp),
+                ("ld_x", _i64), ("a", _vp), ("b", _vp), ("scale", _vp), ("adapter_ids", _vp), ("seq_offsets", _vp),
+                ("residual", _vp), ("ld_residual", _i64), ("y", _vp), ("ld_y", _i64), ("out_dtype", _i32),
+                ("workspace", _vp), ("workspace_bytes", _sz), ("stream", _vp)]
+
+
 class BalanceLossArgs(ctypes.Structure):
     _fields_ = [("route", ctypes.POINTER(RouteParams)), ("T", _i32), ("num_seqs", _i32), ("router_logits", _vp),
                 ("topk_ids", _vp), ("seq_offsets", _vp), ("balance_coef", _f32), ("z_coef", _f32), ("losses", _vp),
@@ -486,6 +493,65 @@ def moe_gated_linear_backward(dh: torch.Tensor, gu: torch.Tensor, w: LinearWeigh
                               dw_dtype=torch.float32) -> dict:
     """One call of MoeGatedLinearBackward."""
     return MoeGatedLinearBackward(dh, gu, w, xq, xs, activation, want_dx, want_dw, want_dbias, dw_dtype)()
+
+
+@dataclass
+class LoraWeights:
+    """Adapters of one projection: a [num_adapters, R, K] and b [num_adapters, N, R] bf16 (smaller ranks padded
+    with zeros), scale float32 [num_adapters] or None for 1."""
+    a: torch.Tensor
+    b: torch.Tensor
+    scale: Optional[torch.Tensor] = None
+
+
+class MoeLora(_Call):
+    """y = residual + scale * (x @ A^T) @ B^T with the adapter of each row's sequence.
+
+    x bf16 [T, K]; adapter_ids int32 [num_seqs], a sequence without an adapter has one outside the range;
+    seq_offsets int32 [num_seqs + 1] on the GPU, or None for one row per sequence.  residual and y [T, N] of
+    out_dtype (bfloat16 or float32); rows of x, residual and y may be strided; y may be residual itself.
+    Rows outside the sequences are not written (0 in a y that the object makes)."""
+
+    def __init__(self, x: torch.Tensor, w: LoraWeights, adapter_ids: torch.Tensor,
+                 seq_offsets: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                 out_dtype=torch.bfloat16, y: Optional[torch.Tensor] = None):
+        if w.a.dim() != 3 or w.b.dim() != 3:
+            raise ValueError("a, b: expected shapes [num_adapters, R, K] and [num_adapters, N, R]")
+        n, R, K = w.a.shape
+        T, N = x.shape[0], w.b.shape[1]
+        ldx = _rows(x, "x", torch.bfloat16, (T, K))
+        _need(w.a, "a", torch.bfloat16)
+        _need(w.b, "b", torch.bfloat16, (n, N, R))
+        if w.scale is not None:
+            _need(w.scale, "scale", torch.float32, (n,))
+        if out_dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"out_dtype: expected float32 or bfloat16, got {out_dtype}")
+        S = adapter_ids.numel()
+        _need(adapter_ids, "adapter_ids", torch.int32, (S if seq_offsets is not None else T,))
+        if seq_offsets is not None:
+            _need(seq_offsets, "seq_offsets", torch.int32, (S + 1,))
+        ldr = _rows(residual, "residual", out_dtype, (T, N)) if residual is not None else N
+        if y is None:
+            y = torch.zeros(T, N, dtype=out_dtype, device=x.device)
+        ldy = _rows(y, "y", out_dtype, (T, N))
+        ws = workspace(lib().moe_lora_workspace_size(T, K, R, S, int(seq_offsets is not None)), x.device)
+        dt = B.MOE_DTYPE_F32 if out_dtype == torch.float32 else B.MOE_DTYPE_BF16
+        self.y = y
+        self._hold("moe_lora",
+                   LoraArgs(T, K, N, R, n, S, _ptr(x), ldx, _ptr(w.a), _ptr(w.b), _ptr(w.scale), _ptr(adapter_ids),
+                            _ptr(seq_offsets), _ptr(residual), ldr, _ptr(y), ldy, dt, _ptr(ws), ws.numel(), None),
+                   (x, w.a, w.b, w.scale, adapter_ids, seq_offsets, residual, y, ws))
+
+    def __call__(self, stream: Optional[int] = None) -> torch.Tensor:
+        self._run(stream)
+        return self.y
+
+
+def moe_lora(x: torch.Tensor, w: LoraWeights, adapter_ids: torch.Tensor, seq_offsets: Optional[torch.Tensor] = None,
+             residual: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16,
+             y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One call of MoeLora."""
+    return MoeLora(x, w, adapter_ids, seq_offsets, residual, out_dtype, y)()
 
 
 def _router_inputs(params: RouteParams, logits: torch.Tensor, ids: Optional[torch.Tensor],

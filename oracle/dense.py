@@ -103,3 +103,20 @@ def gated_backward(dh, g, u, act):
     s, smag = activation_slope(g, act)
     a = activation(g, act)
     return np.concatenate([dh * u * s, dh * a], 1), np.concatenate([np.abs(dh * u) * smag, np.abs(dh * a)], 1)
+
+
+# ---- adapters of many requests -----------------------------------------------------------
+def lora(x, a, b, scale, ids, offsets, residual, y):
+    """(y, magnitude): y's rows of the sequences are overwritten, the others stay; magnitude: the sum of the
+    absolute values of the adapters' terms."""
+    T, n = x.shape[0], a.shape[0]
+    y, mag = y.copy(), np.zeros_like(y)
+    off = np.arange(T + 1) if offsets is None else np.clip(offsets, 0, T)
+    for i, lo, hi in zip(ids, off, off[1:]):
+        if hi <= lo:
+            continue
+        y[lo:hi] = 0 if residual is None else residual[lo:hi]
+        if 0 <= i < n:
+            y[lo:hi] += scale[i] * ((x[lo:hi] @ a[i].T) @ b[i].T)
+            mag[lo:hi] = np.abs(scale[i]) * ((np.abs(x[lo:hi]) @ np.abs(a[i]).T) @ np.abs(b[i]).T)
+    return y, mag

@@ -45,7 +45,7 @@ def test_add_layernorm_backward_refuses(over, code, needle):
 
 
 @pytest.mark.parametrize("name", ["moe_add_layernorm", "moe_add_layernorm_backward", "moe_gated_linear",
-                                  "moe_gated_linear_backward"])
+                                  "moe_gated_linear_backward", "moe_lora"])
 def test_null_arguments(name):
     assert getattr(M.lib(), name)(None) == B.MOE_ERR_INVALID
     assert name in M.moe_last_error()
@@ -91,3 +91,28 @@ GBWD = dict(T=4, K=256, I=96, dh=at(0), gu=at(1), activation=2, xq=at(2), xs=at(
 def test_gated_linear_backward_refuses(over, code, needle):
     assert call("moe_gated_linear_backward", L.GatedLinearBackwardArgs, GBWD, **over) == code
     assert needle in M.moe_last_error() and "moe_gated_linear_backward" in M.moe_last_error()
+
+
+LORA = dict(T=6, K=72, N=48, R=24, num_adapters=3, num_seqs=2, x=at(0), ld_x=80, a=at(1), b=at(2), scale=at(3), adapter_ids=at(4),
+            seq_offsets=at(5), residual=at(6), ld_residual=48, y=at(7), ld_y=48, out_dtype=1, workspace=at(8), workspace_bytes=1 << 20)
+
+
+@pytest.mark.parametrize("over,code,needle", [
+    (dict(T=0), B.MOE_ERR_INVALID, "T, K, N, R"), (dict(R=0), B.MOE_ERR_INVALID, "T, K, N, R"), (dict(K=70), B.MOE_ERR_UNSUPPORTED, "multiples of 8"),
+    (dict(R=12), B.MOE_ERR_UNSUPPORTED, "multiples of 8"), (dict(N=40), B.MOE_ERR_UNSUPPORTED, "of 16"), (dict(R=264), B.MOE_ERR_UNSUPPORTED, "256"),
+    (dict(K=65544, ld_x=65544), B.MOE_ERR_UNSUPPORTED, "65536"), (dict(num_adapters=0), B.MOE_ERR_INVALID, "num_adapters"),
+    (dict(num_seqs=0), B.MOE_ERR_INVALID, "num_seqs"), (dict(seq_offsets=None), B.MOE_ERR_INVALID, "must be T"),
+    (dict(num_seqs=(1 << 20) + 1), B.MOE_ERR_UNSUPPORTED, "num_seqs"), (dict(T=(1 << 23) + 1), B.MOE_ERR_UNSUPPORTED, "T ("),
+    (dict(adapter_ids=None), B.MOE_ERR_INVALID, "adapter_ids"), (dict(out_dtype=3), B.MOE_ERR_INVALID, "out_dtype"),
+    (dict(ld_x=64), B.MOE_ERR_INVALID, "ld_x"), (dict(ld_y=40), B.MOE_ERR_INVALID, "ld_y"), (dict(ld_residual=8), B.MOE_ERR_INVALID, "ld_residual"),
+    (dict(ld_x=76), B.MOE_ERR_UNSUPPORTED, "aligned"), (dict(b=at(2, 8)), B.MOE_ERR_UNSUPPORTED, "aligned"), (dict(y=at(7, 2)), B.MOE_ERR_UNSUPPORTED, "aligned"),
+    (dict(scale=at(3, 2)), B.MOE_ERR_INVALID, "scale"), (dict(adapter_ids=at(4, 1)), B.MOE_ERR_INVALID, "adapter_ids"), (dict(seq_offsets=at(5, 2)), B.MOE_ERR_INVALID, "seq_offsets"),
+    (dict(workspace=None), B.MOE_ERR_WORKSPACE, "workspace"), (dict(workspace_bytes=100), B.MOE_ERR_WORKSPACE, "need"),
+    (dict(workspace=at(8, 64)), B.MOE_ERR_INVALID, "256-byte"), (dict(y=at(0)), B.MOE_ERR_INVALID, "y must not overlap x"),
+    (dict(y=at(2)), B.MOE_ERR_INVALID, "y must not overlap b"), (dict(y=at(6, 16)), B.MOE_ERR_INVALID, "residual"),
+    (dict(y=at(6), ld_y=56), B.MOE_ERR_INVALID, "residual"), (dict(workspace=at(6)), B.MOE_ERR_INVALID, "workspace must not overlap residual"),
+    (dict(workspace=at(7)), B.MOE_ERR_INVALID, "y and workspace"), (dict(workspace=at(1)), B.MOE_ERR_INVALID, "workspace must not overlap a"),
+])
+def test_lora_refuses(over, code, needle):
+    assert call("moe_lora", L.LoraArgs, LORA, **over) == code
+    assert needle in M.moe_last_error() and "moe_lora" in M.moe_last_error()
