@@ -627,10 +627,10 @@ size_t moe_gated_linear_backward_workspace_size(int32_t T, int32_t K, int32_t I,
  * wrote (moe_linear without activation) as y and residual at once, the adapters are added to it; given another
  * y, that can be moe_linear's residual.
  * The inner product is a float32 sum; it goes to the matrix cores as two bf16 values (three for float32 y)
- * whose sum is within 2^-17 (2^-25) of it, and y is rounded once.
+ * whose sum is within 2^-17 (2^-25) of it times the scale, and y is rounded once.
  *   T, K, N, R  K % 8 == 0, K <= 65536; N % 16 == 0, N <= 2^20; R % 8 == 0, R <= 256 (a smaller rank is
  *               padded with zeros); T <= 2^23, num_seqs <= 2^20.
- *   x           [T, ld_x] bf16, the first K columns used.
+ *   x           [T, ld_x] bf16, the first K columns used; ld_x <= 2^24.
  *   a, b        [num_adapters, R, K] and [num_adapters, N, R] bf16.   scale [num_adapters] float32 or NULL (1).
  *   adapter_ids [num_seqs] int32, seq_offsets [num_seqs + 1] int32 (non-decreasing within [0, T]; values
  *               outside are taken as the nearest ones inside), both on the device.
@@ -638,7 +638,8 @@ size_t moe_gated_linear_backward_workspace_size(int32_t T, int32_t K, int32_t I,
  *               of the matrix that y's columns are part of (same ld).
  *   y           [T, ld_y] of out_dtype (MOE_DTYPE_*), the first N columns written.
  *               x, a, b, residual, y 16-byte aligned, leading dimensions % 8 == 0.
- *   workspace   >= moe_lora_workspace_size(T, K, R, num_seqs, seq_offsets != NULL) bytes, 256-byte aligned.
+ *   workspace   >= moe_lora_workspace_size(T, R, num_seqs, seq_offsets != NULL, out_dtype) bytes, 256-byte
+ *               aligned.
  * Deterministic. */
 typedef struct moe_lora_args {
     int32_t T, K, N, R, num_adapters, num_seqs;
@@ -659,7 +660,7 @@ typedef struct moe_lora_args {
     void*           stream;
 } moe_lora_args;
 int moe_lora(const moe_lora_args* a);
-size_t moe_lora_workspace_size(int32_t T, int32_t K, int32_t R, int32_t num_seqs, int32_t with_offsets);
+size_t moe_lora_workspace_size(int32_t T, int32_t R, int32_t num_seqs, int32_t with_offsets, int32_t out_dtype);
 
 /* moe_balance_loss: load-balance and z losses of a router, with per-expert counts.  The rows are
  * num_seqs packed sequences, sequence s in rows [seq_offsets[s], seq_offsets[s+1]); seq_offsets

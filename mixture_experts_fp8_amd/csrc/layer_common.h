@@ -124,9 +124,9 @@ struct LoraArgs {
     const float* scale;   // [n] or NULL: 1
     const int32_t* ids;   // [S]
     const int32_t* off;   // [S + 1] or NULL: a sequence per row
-    float* v;             // workspace: [parts][T][ldv]
+    void* v;              // workspace: x A^T as operands (v_operand)
     LinArgs out;          // N, residual, y
-    int ldv = 0, parts = 0, chunks = 0;   // set by launch_lora
+    int steps = 0, split = 0, col_blocks = 0, slot0 = 0;   // set by launch_lora
 };
 hipError_t launch_lora(const LoraArgs& a, hipStream_t st);
 

@@ -303,49 +303,37 @@ __device__ __forceinline__ int column_fragment(const LinArgs& a, int tn, int col
 template <bool GATED>
 constexpr int tile_scales(int cols) { return GATED ? cols / 32 : (cols + 127) / 128; }
 
-// 4 x 4 transpose between the registers r[0..3] and the four groups of 16 lanes: r[i] of group g
-// becomes what r[g] of group i was.
-__device__ __forceinline__ void transpose_groups(uint32_t (&r)[4]) {
-    auto swap32 = [](uint32_t& a, uint32_t& b) {
-        auto v = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-        a = v[0];
-        b = v[1];
-    };
-    auto swap16 = [](uint32_t& a, uint32_t& b) {
-        auto v = __builtin_amdgcn_permlane16_swap(a, b, false, false);
-        a = v[0];
-        b = v[1];
-    };
-    swap32(r[0], r[2]);
-    swap32(r[1], r[3]);
-    swap16(r[0], r[1]);
-    swap16(r[2], r[3]);
-}
-
 __device__ __forceinline__ void store16(v4u_t* d, v4u_t v, int nt) {
     if (nt) __builtin_nontemporal_store(v, d);
     else *d = v;
 }
 
+// Exchange between neighbouring groups of 16 lanes, its own inverse: of two column fragments' values, a and b,
+// lane group G then holds those of fragment G % 2, a the ones of group G & 2 and b the ones of the next.
+__device__ __forceinline__ void swap_groups(uint32_t& a, uint32_t& b) {
+    auto v = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = v[0];
+    b = v[1];
+}
+
 // Epilogue of a wave's 64 columns col0 .. (of which those below N exist; N is a multiple of 16).
 // acc[mi][j]: columns col0 + 16 j + 4 G .. +3 of row row0 + 16 mi.
-//   bf16: the four groups of 16 lanes are transposed against the four column fragments, so that lane
-//   group G holds the 16 columns of fragment G, 32 bytes: residual and output move as 16-byte vectors.
+//   bf16: after an exchange between neighbouring lane groups, lane group G holds the 8 columns from
+//   16 (G % 2) + 8 (G / 2) of 32: residual and output move as 16-byte vectors, and one instruction covers
+//   64 bytes of a row.
 //   float32: a lane's four columns are 16 bytes already.
 // The residual of all rows is requested before the first one is used.
 template <int MI>
 __device__ __forceinline__ void tile_residual(const LinArgs& a, uint4 (&q)[MI][2], int row0, int col0) {
-    const int G = (threadIdx.x & 63) >> 4;
-    const bool on = col0 + 16 * G < a.N;
+    const int G = (threadIdx.x & 63) >> 4, col = col0 + 16 * (G & 1) + 8 * (G >> 1);
     if (a.out_bf16 && a.res) {
 #pragma unroll
         for (int mi = 0; mi < MI; ++mi) {
-            q[mi][0] = q[mi][1] = make_uint4(0, 0, 0, 0);
-            if (on && row0 + 16 * mi < a.T) {
-                const uint4* s = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.res) +
-                                                                (row0 + 16 * mi) * a.ldr + col0 + 16 * G);
-                q[mi][0] = s[0];
-                q[mi][1] = s[1];
+            const uint16_t* s = reinterpret_cast<const uint16_t*>(a.res) + (row0 + 16 * mi) * a.ldr + col;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                q[mi][h] = make_uint4(0, 0, 0, 0);
+                if (col + 32 * h < a.N && row0 + 16 * mi < a.T) q[mi][h] = *reinterpret_cast<const uint4*>(s + 32 * h);
             }
         }
     }
@@ -354,7 +342,6 @@ template <int MI, int ACT>
 __device__ __forceinline__ void tile_epilogue(const LinArgs& a, v4f (&acc)[MI][4], const v4f (&b)[4], uint4 (&q)[MI][2],
                                               int row0, int col0) {
     const int G = (threadIdx.x & 63) >> 4;
-    const bool bf = a.out_bf16, on = col0 + 16 * G < a.N;
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi) {
         const int64_t row = row0 + 16 * mi;
@@ -364,13 +351,15 @@ __device__ __forceinline__ void tile_epilogue(const LinArgs& a, v4f (&acc)[MI][4
         for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[j][i] = act_fn(v[j][i] + b[j][i], ACT);
-        if (bf) {
+        if (a.out_bf16) {
             uint32_t lo[4], hi[4];
             if (a.res) {
-                lo[0] = q[mi][0].x, hi[0] = q[mi][0].y, lo[1] = q[mi][0].z, hi[1] = q[mi][0].w;
-                lo[2] = q[mi][1].x, hi[2] = q[mi][1].y, lo[3] = q[mi][1].z, hi[3] = q[mi][1].w;
-                transpose_groups(lo);
-                transpose_groups(hi);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    lo[2 * h] = q[mi][h].x, hi[2 * h] = q[mi][h].y, lo[2 * h + 1] = q[mi][h].z, hi[2 * h + 1] = q[mi][h].w;
+                    swap_groups(lo[2 * h], lo[2 * h + 1]);
+                    swap_groups(hi[2 * h], hi[2 * h + 1]);
+                }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     v[j][0] += __uint_as_float(lo[j] << 16);
@@ -384,12 +373,14 @@ __device__ __forceinline__ void tile_epilogue(const LinArgs& a, v4f (&acc)[MI][4
                 lo[j] = pack_bf16(v[j][0], v[j][1]);
                 hi[j] = pack_bf16(v[j][2], v[j][3]);
             }
-            transpose_groups(lo);
-            transpose_groups(hi);
-            if (on && live) {
-                v4u_t* d = reinterpret_cast<v4u_t*>(reinterpret_cast<uint16_t*>(a.y) + row * a.ldy + col0 + 16 * G);
-                store16(d, v4u_t{lo[0], hi[0], lo[1], hi[1]}, a.nt);
-                store16(d + 1, v4u_t{lo[2], hi[2], lo[3], hi[3]}, a.nt);
+            const int col = col0 + 16 * (G & 1) + 8 * (G >> 1);
+            uint16_t* d = reinterpret_cast<uint16_t*>(a.y) + row * a.ldy + col;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                swap_groups(lo[2 * h], lo[2 * h + 1]);
+                swap_groups(hi[2 * h], hi[2 * h + 1]);
+                if (live && col + 32 * h < a.N)
+                    store16(reinterpret_cast<v4u_t*>(d + 32 * h), v4u_t{lo[2 * h], hi[2 * h], lo[2 * h + 1], hi[2 * h + 1]}, a.nt);
             }
         } else {
 #pragma unroll
@@ -418,18 +409,12 @@ __device__ __forceinline__ void tile_finish(const LinArgs& a, v4f (&acc)[MI][4],
 }
 
 // Epilogue of the gated block: acc[mi][0..1] gate and acc[mi][2..3] up, columns col0 + 16 j + 4 G .. +3 of row
-// row0 + 16 mi; the wave's 32 columns exist together (N / 2 is a multiple of 32).  The kept sums move as the
-// linear layer's output does, h after an exchange between neighbouring groups of 16 lanes, which leaves
-// lane group G the columns 8 (G / 2) .. +7 of fragment G % 2: 16-byte vectors.
+// row0 + 16 mi; the wave's 32 columns exist together (N / 2 is a multiple of 32).  Kept sums and h
+// move as the linear layer's output does.
 template <int MI, int ACT>
 __device__ __forceinline__ void gated_epilogue(const LinArgs& a, v4f (&acc)[MI][4], const v4f (&b)[4], int row0, int col0) {
     const int G = (threadIdx.x & 63) >> 4, I = a.N / 2;
     const bool on = col0 < I;
-    auto swap16 = [](uint32_t& x, uint32_t& y) __attribute__((always_inline)) {
-        auto v = __builtin_amdgcn_permlane16_swap(x, y, false, false);
-        x = v[0];
-        y = v[1];
-    };
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi) {
         const int64_t row = row0 + 16 * mi;
@@ -437,19 +422,19 @@ __device__ __forceinline__ void gated_epilogue(const LinArgs& a, v4f (&acc)[MI][
         v4f (&v)[4] = acc[mi];
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] += b[j];
+        const int col = col0 + 16 * (G & 1) + 8 * (G >> 1);
         if (a.gu) {
-            uint32_t lo[4], hi[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                lo[j] = pack_bf16(v[j][0], v[j][1]);
-                hi[j] = pack_bf16(v[j][2], v[j][3]);
-            }
-            transpose_groups(lo);
-            transpose_groups(hi);
-            if (live) {
-                v4u_t* d = reinterpret_cast<v4u_t*>(a.gu + row * a.N + (G >> 1) * I + col0 + 16 * (G & 1));
-                store16(d, v4u_t{lo[0], hi[0], lo[1], hi[1]}, a.nt);
-                store16(d + 1, v4u_t{lo[2], hi[2], lo[3], hi[3]}, a.nt);
+            for (int h = 0; h < 2; ++h) {
+                uint32_t lo[2], hi[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    lo[j] = pack_bf16(v[2 * h + j][0], v[2 * h + j][1]);
+                    hi[j] = pack_bf16(v[2 * h + j][2], v[2 * h + j][3]);
+                }
+                swap_groups(lo[0], lo[1]);
+                swap_groups(hi[0], hi[1]);
+                if (live) store16(reinterpret_cast<v4u_t*>(a.gu + row * a.N + h * I + col), v4u_t{lo[0], hi[0], lo[1], hi[1]}, a.nt);
             }
         }
         uint32_t lo[2], hi[2];
@@ -461,11 +446,10 @@ __device__ __forceinline__ void gated_epilogue(const LinArgs& a, v4f (&acc)[MI][
             lo[j] = pack_bf16(h[0], h[1]);
             hi[j] = pack_bf16(h[2], h[3]);
         }
-        swap16(lo[0], lo[1]);
-        swap16(hi[0], hi[1]);
+        swap_groups(lo[0], lo[1]);
+        swap_groups(hi[0], hi[1]);
         if (live)
-            store16(reinterpret_cast<v4u_t*>(reinterpret_cast<uint16_t*>(a.y) + row * I + col0 + 16 * (G & 1) + 8 * (G >> 1)),
-                    v4u_t{lo[0], hi[0], lo[1], hi[1]}, a.nt);
+            store16(reinterpret_cast<v4u_t*>(reinterpret_cast<uint16_t*>(a.y) + row * I + col), v4u_t{lo[0], hi[0], lo[1], hi[1]}, a.nt);
     }
 }
 template <int MI>

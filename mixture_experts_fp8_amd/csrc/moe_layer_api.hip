@@ -87,14 +87,14 @@ int moe_gated_linear_backward(const moe_gated_linear_backward_args* a) {
     return done("moe_gated_linear_backward", moe::launch_gated_backward(g, static_cast<hipStream_t>(a->stream)));
 }
 
-size_t moe_lora_workspace_size(int32_t T, int32_t K, int32_t R, int32_t num_seqs, int32_t with_offsets) {
-    return T < 1 || K < 1 || R < 1 || num_seqs < 1 ? 0 : moe::lora_plan(T, K, R, with_offsets ? num_seqs : 0).end;
+size_t moe_lora_workspace_size(int32_t T, int32_t R, int32_t num_seqs, int32_t with_offsets, int32_t out_dtype) {
+    return T < 1 || R < 1 || num_seqs < 1 ? 0 : moe::lora_plan(T, R, with_offsets ? num_seqs : 0, out_dtype == MOE_DTYPE_BF16).end;
 }
 
 int moe_lora(const moe_lora_args* a) {
     if (int rc = moe::host::check_lora(a)) return rc;
     moe::LoraArgs l{a->T, a->K, a->R, a->num_adapters, a->num_seqs, a->x, a->ld_x, a->a, a->b, a->scale,
-                    a->adapter_ids, a->seq_offsets, static_cast<float*>(a->workspace), {}};
+                    a->adapter_ids, a->seq_offsets, a->workspace, {}};
     l.out.N = a->N, l.out.res = a->residual, l.out.ldr = a->ld_residual;
     l.out.y = a->y, l.out.ldy = a->ld_y, l.out.out_bf16 = a->out_dtype == MOE_DTYPE_BF16;
     return done("moe_lora", moe::launch_lora(l, static_cast<hipStream_t>(a->stream)));

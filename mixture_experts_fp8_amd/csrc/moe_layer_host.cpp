@@ -64,14 +64,13 @@ GatedBwdPlan gated_bwd_plan(int T, int K, int I, bool dx, bool dw, bool dbias) {
     return p;
 }
 
-LoraPlan lora_plan(int T, int K, int R, int S) {
+LoraPlan lora_plan(int T, int R, int S, bool bf16) {
     LoraPlan p;
     p.window = S && T / S >= 32 ? 64 : 16;
     p.slots = S ? cdiv(T, p.window) + S : T;
-    p.ldv = (int)cdiv(R, 16) * 16;
-    const int64_t groups = p.slots * cdiv(R, 64);
-    p.parts = (int)std::max<int64_t>(1, std::min<int64_t>(256 / groups, K / 64 / 16));
-    p.end = align256((size_t)p.parts * T * p.ldv * 4);
+    p.steps = (int)cdiv(R, 32);
+    p.split = bf16 ? 2 : 3;
+    p.end = (size_t)p.slots * (p.window / 16) * p.steps * p.split * 1024;
     return p;
 }
 
@@ -414,6 +413,8 @@ int check_lora(const moe_lora_args* a) {
     if (a->out_dtype != MOE_DTYPE_F32 && a->out_dtype != MOE_DTYPE_BF16)
         return fail(MOE_ERR_INVALID, "%s: out_dtype (%d) must be MOE_DTYPE_F32 or MOE_DTYPE_BF16", op, a->out_dtype);
     if (a->ld_x < K) return fail(MOE_ERR_INVALID, "%s: ld_x (%lld) must be >= K (%d)", op, (long long)a->ld_x, K);
+    if (a->ld_x > (1 << 24))   // 64 rows within 32-bit offsets
+        return fail(MOE_ERR_UNSUPPORTED, "%s: ld_x (%lld) must not exceed %d", op, (long long)a->ld_x, 1 << 24);
     if (a->ld_y < N || (a->residual && a->ld_residual < N))
         return fail(MOE_ERR_INVALID, "%s: ld_y (%lld) and ld_residual (%lld) must be >= N (%d)", op, (long long)a->ld_y,
                     (long long)a->ld_residual, N);
@@ -421,7 +422,7 @@ int check_lora(const moe_lora_args* a) {
         !aligned(a->residual, 16) || !aligned(a->a, 16) || !aligned(a->b, 16))
         return fail(MOE_ERR_UNSUPPORTED, "%s: x, a, b, residual and y must be 16-byte aligned, rows a multiple of 8 "
                     "elements apart", op);
-    const size_t need = lora_plan(T, K, R, a->seq_offsets ? S : 0).end;
+    const size_t need = lora_plan(T, R, a->seq_offsets ? S : 0, a->out_dtype == MOE_DTYPE_BF16).end;
     int rc = check_ws(op, a->workspace, a->workspace_bytes, need);
     if (rc) return rc;
     const int size = a->out_dtype == MOE_DTYPE_BF16 ? 2 : 4;

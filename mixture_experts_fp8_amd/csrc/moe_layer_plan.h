@@ -26,13 +26,14 @@ struct GatedBwdPlan {
 };
 GatedBwdPlan gated_bwd_plan(int T, int K, int I, bool dx, bool dw, bool dbias);
 
-// ---- adapters: rows of one sequence in one window are a slot; a slot's sum over K may be split
+// ---- adapters: rows of one sequence in one window are a slot, which has operands of 16 rows x 32 ranks in
+// the workspace, each as `split` bf16 parts
 struct LoraPlan {
-    int window, parts, ldv;   // rows of a window; partial sums; floats of a row of them
+    int window, steps, split;   // rows of a window; operands along the rank; parts
     int64_t slots;
-    size_t end;               // workspace bytes
+    size_t end;                 // workspace bytes
 };
-LoraPlan lora_plan(int T, int K, int R, int S);   // S = 0: a sequence per row
+LoraPlan lora_plan(int T, int R, int S, bool bf16);   // S = 0: a sequence per row
 
 namespace host {
 int check_add_rmsnorm(const moe_add_rmsnorm_args* a);

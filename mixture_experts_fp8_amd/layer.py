@@ -534,8 +534,8 @@ class MoeLora(_Call):
         if y is None:
             y = torch.zeros(T, N, dtype=out_dtype, device=x.device)
         ldy = _rows(y, "y", out_dtype, (T, N))
-        ws = workspace(lib().moe_lora_workspace_size(T, K, R, S, int(seq_offsets is not None)), x.device)
         dt = B.MOE_DTYPE_F32 if out_dtype == torch.float32 else B.MOE_DTYPE_BF16
+        ws = workspace(lib().moe_lora_workspace_size(T, R, S, int(seq_offsets is not None), dt), x.device)
         self.y = y
         self._hold("moe_lora",
                    LoraArgs(T, K, N, R, n, S, _ptr(x), ldx, _ptr(w.a), _ptr(w.b), _ptr(w.scale), _ptr(adapter_ids),

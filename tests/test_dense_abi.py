@@ -104,7 +104,7 @@ LORA = dict(T=6, K=72, N=48, R=24, num_adapters=3, num_seqs=2, x=at(0), ld_x=80,
     (dict(num_seqs=0), B.MOE_ERR_INVALID, "num_seqs"), (dict(seq_offsets=None), B.MOE_ERR_INVALID, "must be T"),
     (dict(num_seqs=(1 << 20) + 1), B.MOE_ERR_UNSUPPORTED, "num_seqs"), (dict(T=(1 << 23) + 1), B.MOE_ERR_UNSUPPORTED, "T ("),
     (dict(adapter_ids=None), B.MOE_ERR_INVALID, "adapter_ids"), (dict(out_dtype=3), B.MOE_ERR_INVALID, "out_dtype"),
-    (dict(ld_x=64), B.MOE_ERR_INVALID, "ld_x"), (dict(ld_y=40), B.MOE_ERR_INVALID, "ld_y"), (dict(ld_residual=8), B.MOE_ERR_INVALID, "ld_residual"),
+    (dict(ld_x=64), B.MOE_ERR_INVALID, "ld_x"), (dict(ld_x=(1 << 24) + 8), B.MOE_ERR_UNSUPPORTED, "ld_x"), (dict(ld_y=40), B.MOE_ERR_INVALID, "ld_y"), (dict(ld_residual=8), B.MOE_ERR_INVALID, "ld_residual"),
     (dict(ld_x=76), B.MOE_ERR_UNSUPPORTED, "aligned"), (dict(b=at(2, 8)), B.MOE_ERR_UNSUPPORTED, "aligned"), (dict(y=at(7, 2)), B.MOE_ERR_UNSUPPORTED, "aligned"),
     (dict(scale=at(3, 2)), B.MOE_ERR_INVALID, "scale"), (dict(adapter_ids=at(4, 1)), B.MOE_ERR_INVALID, "adapter_ids"), (dict(seq_offsets=at(5, 2)), B.MOE_ERR_INVALID, "seq_offsets"),
     (dict(workspace=None), B.MOE_ERR_WORKSPACE, "workspace"), (dict(workspace_bytes=100), B.MOE_ERR_WORKSPACE, "need"),

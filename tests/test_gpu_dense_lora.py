@@ -140,7 +140,7 @@ def test_lora_stays_inside_its_buffers(T, K, N, R, n, seqs, out):
     dt = torch.bfloat16 if out == "bf16" else torch.float32
     args = (x, w, _i32(ids), None if off is None else _i32(off), r, dt)
     want = M.moe_lora(*args, y=torch.zeros_like(r))
-    need = B.lib().moe_lora_workspace_size(T, K, R, len(ids), int(off is not None))
+    need = B.lib().moe_lora_workspace_size(T, R, len(ids), int(off is not None), int(out == "bf16"))
     ar = Arena([T * N * r.element_size(), need])
     call = M.MoeLora(*args)
     ar.view(0, dt, (T, N)).zero_()
