@@ -480,7 +480,8 @@ int moe_add_layernorm(const moe_add_layernorm_args* a);
 /* moe_add_layernorm_backward: as moe_add_rmsnorm_backward, with xhat = (h - m) * r and g = dy * weight:
  *   dx[t, :]   = bf16_RNE( r * (g - mean_c(g) - xhat * mean_c(g * xhat)) + dh );
  *   dweight[c] = sum_t dy[t, c] * xhat[t, c],  dbias[c] = sum_t dy[t, c]   (float32, each optional).
- * dx is formed in double, the two gradients' sums in float32.  Buffers as there; workspace >=
+ * The rows' sums and xhat are formed in double, products and the two gradients' sums in float32.  Buffers as there;
+ * workspace >=
  * moe_add_layernorm_backward_workspace_size(T, H) bytes, used for dweight and dbias only (may be NULL
  * without both).  Deterministic. */
 typedef struct moe_add_layernorm_backward_args {

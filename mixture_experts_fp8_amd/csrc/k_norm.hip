@@ -98,16 +98,24 @@ __device__ __forceinline__ double rsqrt_f64(double x) {
     return x > 0.0 && x < __builtin_inf() ? n : r;
 }
 
-// A double as a float that rounds to the same bf16: rounded to odd (towards zero, the last bit set where
-// anything was cut off).  Rounded to nearest it could land on the middle of two bf16 values and be
-// rounded the other way then, which happens to one value in 2^17.  Infinities (of an infinite weight) and NaN
-// have no remainder that compares with 0 and stay as they are.
-__device__ __forceinline__ float round_odd(double d) {
-    const float f = (float)d;
-    const double r = d - (double)f;
-    uint32_t u = __float_as_uint(f);
-    if (r < 0.0 || r > 0.0) u = (u - ((r > 0.0) != (d > 0.0) ? 1u : 0u)) | 1u;
-    return __uint_as_float(u);
+// Doubles as floats that round to the same bf16.  A float beside the double does, unless it lands on the middle
+// of two bf16 values (one in 2^16 does) and the double does not: then the next float towards the double.
+// Infinities (of an infinite weight) and NaN are no such middle.
+__device__ __forceinline__ void round_towards(const double (&d)[8], float (&f)[8]) {
+    bool middle = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        f[j] = (float)d[j];
+        middle |= (__float_as_uint(f[j]) & 0xFFFFu) == 0x8000u;
+    }
+    if (middle) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t u = __float_as_uint(f[j]);
+            const double r = d[j] - (double)f[j];
+            if ((u & 0xFFFFu) == 0x8000u && (r < 0.0 || r > 0.0)) f[j] = __uint_as_float((r > 0.0) == (d[j] > 0.0) ? u + 1 : u - 1);
+        }
+    }
 }
 
 // E4M3 codes of 8 values in each of LANES consecutive lanes sharing one scale (LANES * 8 columns):
@@ -142,7 +150,7 @@ __device__ __forceinline__ uint2 group_codes(const float (&f)[8], int& e) {
 // of at most H, and a constant row's variance is 0.
 template <int G, int VPT, bool ST, bool LN>
 __device__ __forceinline__ void add_norm(const NormArgs& a) {
-    constexpr int RPB = G < 256 ? 256 / G : 1;
+    constexpr int RPB = G == 64 ? 4 : 1;
     __shared__ double s_sum[LN ? 2 : 1][G / 64];
     const int sub = threadIdx.x % G, nv = a.H >> 3;
     const int64_t t = (int64_t)blockIdx.x * RPB + threadIdx.x / G;
@@ -150,7 +158,16 @@ __device__ __forceinline__ void add_norm(const NormArgs& a) {
     const uint16_t* xr = a.x + t * a.ldx;
     const uint16_t* rr = a.res ? a.res + t * a.ldr : nullptr;
     uint4 vx[VPT], vr[VPT];
-    float4 w0[VPT], w1[VPT], b0[LN ? VPT : 1], b1[LN ? VPT : 1];
+    auto load_bias = [&](int v, float4& lo, float4& hi) __attribute__((always_inline)) {
+        lo = hi = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (a.b && v < nv) {
+            lo = *reinterpret_cast<const float4*>(a.b + v * 8);
+            hi = *reinterpret_cast<const float4*>(a.b + v * 8 + 4);
+        }
+    };
+    // Weight and bias before the sums, where the registers hold them (4096 x 7168: 62 us, the bias behind them 68).
+    constexpr bool EARLY = LN && G < 1024, EARLY_W = !LN || G * VPT < 4096;
+    float4 w0[VPT], w1[VPT], b0[EARLY ? VPT : 1], b1[EARLY ? VPT : 1];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int v = sub + i * G;
@@ -165,20 +182,17 @@ __device__ __forceinline__ void add_norm(const NormArgs& a) {
             else vr[i] = make_uint4(0, 0, 0, 0);
         }
     }
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
+    auto load_weight = [&](int i) __attribute__((always_inline)) {
         const int v = sub + i * G;
         if (v < nv) {
             w0[i] = *reinterpret_cast<const float4*>(a.w + v * 8);
             w1[i] = *reinterpret_cast<const float4*>(a.w + v * 8 + 4);
         }
-        if constexpr (LN) {
-            b0[i] = b1[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (a.b && v < nv) {
-                b0[i] = *reinterpret_cast<const float4*>(a.b + v * 8);
-                b1[i] = *reinterpret_cast<const float4*>(a.b + v * 8 + 4);
-            }
-        }
+    };
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        if constexpr (EARLY_W) load_weight(i);
+        if constexpr (EARLY) load_bias(sub + i * G, b0[i], b1[i]);
     }
     double ss = 0.0, sd = 0.0, h0 = 0.0;
     if constexpr (LN) {   // h[0]
@@ -237,17 +251,22 @@ __device__ __forceinline__ void add_norm(const NormArgs& a) {
         const int v = sub + i * G;
         float f[8];
         unpack8(vx[i], f);
+        if constexpr (!EARLY_W) load_weight(i);
         const float w[8] = {w0[i].x, w0[i].y, w0[i].z, w0[i].w, w1[i].x, w1[i].y, w1[i].z, w1[i].w};
         float b[8] = {};
+        double d[8];
         if constexpr (LN) {
-            const float4 lo = b0[i], hi = b1[i];
+            float4 lo, hi;
+            if constexpr (EARLY) lo = b0[i], hi = b1[i];
+            else load_bias(v, lo, hi);
             b[0] = lo.x, b[1] = lo.y, b[2] = lo.z, b[3] = lo.w, b[4] = hi.x, b[5] = hi.y, b[6] = hi.z, b[7] = hi.w;
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            if constexpr (LN) f[j] = round_odd(fma(((double)f[j] - mean) * r, (double)w[j], (double)b[j]));
-            else f[j] = round_odd((double)f[j] * r * (double)w[j]);
+            if constexpr (LN) d[j] = fma(((double)f[j] - mean) * r, (double)w[j], (double)b[j]);
+            else d[j] = (double)f[j] * r * (double)w[j];
         }
+        round_towards(d, f);
         const uint4 o = pack8(f);
         if (v < nv) {   // a scale's lanes are all in or all out: H is a multiple of its columns
             if (a.y) st16<ST>(a.y + t * a.H + v * 8, o);
@@ -267,18 +286,18 @@ __device__ __forceinline__ void add_norm(const NormArgs& a) {
 }
 
 template <int G, int VPT, bool ST>
-__global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_rmsnorm(NormArgs a) {
+__global__ __launch_bounds__(G == 64 ? 256 : G) void k_add_rmsnorm(NormArgs a) {
     add_norm<G, VPT, ST, false>(a);
 }
 template <int G, int VPT, bool ST>
-__global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_layernorm(NormArgs a) {
+__global__ __launch_bounds__(G == 64 ? 256 : G) void k_add_layernorm(NormArgs a) {
     add_norm<G, VPT, ST, true>(a);
 }
 
 template <int G, int VPT, bool LN>
 static void run_norm(const NormArgs& args, hipStream_t st) {
-    constexpr int RPB = G < 256 ? 256 / G : 1;
-    const dim3 block(G < 256 ? 256 : G);
+    constexpr int RPB = G == 64 ? 4 : 1;
+    const dim3 block(G == 64 ? 256 : G);
     NormArgs a = args;
     for (int64_t t = 0; t < args.T; t += launch_rows(G)) {
         a.T = (int)std::min<int64_t>(args.T - t, launch_rows(G));
@@ -328,20 +347,29 @@ hipError_t launch_add_layernorm(const NormArgs& a, hipStream_t st) { return laun
 //
 // LN: xhat = (h - m) r and dx = r (g - mean(g) - xhat mean(g xhat)) + dh; the bias's gradient sum_t dy takes
 // its place beside the weight's, in registers and in a second set of parts.  With d = h - h[0] (as in the
-// forward pass) the four sums of d, d^2, g and g d need one exchange: sum g (h - m) = sum g d - mean(d) sum g.
+// forward pass, here rounded to float32, which leaves 2^-24 of d) the four sums of d, d^2, g and g d need one
+// exchange: sum g (h - m) = sum g d - mean(d) sum g.
 template <int G, int VPT, bool ST, bool LN>
 __device__ __forceinline__ void add_norm_bwd(const NormBwdArgs& a) {
-    constexpr int RPB = G < 256 ? 256 / G : 1;
-    constexpr bool AHEAD = VPT <= (LN ? 2 : 4);   // else the registers hold no second row and no weights
+    constexpr int RPB = G == 64 ? 4 : 1;
+    constexpr bool AHEAD = VPT <= 4;   // else the registers hold no second row and no weights
     constexpr int NS = LN ? 4 : 2;
     __shared__ double s_sum[2][NS][G / 64];
     __shared__ __align__(16) float s_dw[RPB][RPB > 1 ? VPT * G * 8 : 4];
+    // The bias's sums: in registers, or, where those do not hold them beside the rest, in LDS, each thread its own.
+    constexpr bool DB_LDS = LN && VPT > 4;
+    extern __shared__ __align__(16) float s_db[];   // [VPT][2][G] vectors of four
     float db[LN ? VPT : 1][8];
     if constexpr (LN) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
 #pragma unroll
             for (int j = 0; j < 8; ++j) db[i][j] = 0.f;
+    }
+    auto db_slot = [&](int i, int h) __attribute__((always_inline)) { return reinterpret_cast<v4f*>(s_db) + (2 * i + h) * G + (threadIdx.x % G); };
+    if constexpr (DB_LDS) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) *db_slot(i, 0) = *db_slot(i, 1) = v4f{0.f, 0.f, 0.f, 0.f};
     }
     const int sub = RPB > 1 ? threadIdx.x % G : threadIdx.x, rw = RPB > 1 ? threadIdx.x / G : 0, nv = a.H >> 3;
     const int64_t step = (int64_t)gridDim.x * RPB;
@@ -386,8 +414,9 @@ __device__ __forceinline__ void add_norm_bwd(const NormBwdArgs& a) {
         for (int i = 0; i < VPT; ++i) vh[i] = nx.h[i], vd[i] = nx.d[i], vr[i] = nx.r[i];
         if (AHEAD && t + step < a.T) load(t + step, nx);   // in flight over this row's sums
         // sum h^2 and sum g h in one exchange: mean(g xhat) = r sum(g h) / H
-        double ss = 0.0, gh = 0.0, sd = 0.0, sg = 0.0, h0 = 0.0;
-        if constexpr (LN) h0 = (double)bf16_to_f32(a.h[t * a.H]);
+        double ss = 0.0, gh = 0.0, sd = 0.0, sg = 0.0;
+        float h0 = 0.f;
+        if constexpr (LN) h0 = bf16_to_f32(a.h[t * a.H]);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             float h[8], d[8], wt[8];
@@ -398,8 +427,8 @@ __device__ __forceinline__ void add_norm_bwd(const NormBwdArgs& a) {
             for (int j = 0; j < 8; ++j) {
                 if constexpr (LN) {
                     // (no weight, and no gradient, behind the row's end: only d has to be left out there)
-                    const double x = sub + i * G < nv ? (double)h[j] - h0 : 0.0;
-                    const double g = (double)d[j] * (double)(AHEAD ? wk[AHEAD ? i : 0][j] : wt[j]);
+                    const double x = (double)(sub + i * G < nv ? h[j] - h0 : 0.f);
+                    const double g = (double)(d[j] * (AHEAD ? wk[AHEAD ? i : 0][j] : wt[j]));
                     sd += x;
                     sg += g;
                     ss = fma(x, x, ss);
@@ -438,13 +467,13 @@ __device__ __forceinline__ void add_norm_bwd(const NormBwdArgs& a) {
                 }
             }
         }
-        double rd, mean = 0.0, mg = 0.0, mx = 0.0;   // LN: mean(h), mean(g), mean(g xhat)
+        double rd, md = 0.0;   // LN: mean(d)
+        float mg = 0.f;        // LN: mean(g)
         if constexpr (LN) {
-            const double md = sd * a.inv_h;
+            md = sd * a.inv_h;
             rd = rsqrt_f64(fma(-md, md, ss * a.inv_h) + (double)a.eps);
-            mean = h0 + md;
-            mg = sg * a.inv_h;
-            mx = (gh * a.inv_h - md * mg) * rd;
+            mg = (float)(sg * a.inv_h);
+            gh -= md * sg;
         } else {
             rd = rsqrt_f64(fma(ss, a.inv_h, (double)a.eps));
         }
@@ -463,18 +492,16 @@ __device__ __forceinline__ void add_norm_bwd(const NormBwdArgs& a) {
             if constexpr (!AHEAD) weights(i, wt);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                if constexpr (LN) {
-                    const double x = ((double)h[j] - mean) * rd, gw = (double)d[j] * (double)(AHEAD ? wk[AHEAD ? i : 0][j] : wt[j]);
-                    dw[i][j] = fmaf(d[j], (float)x, dw[i][j]);
-                    db[i][j] += d[j];
-                    const float g = (float)(rd * fma(-x, mx, gw - mg));
-                    e[j] = a.dh ? g + e[j] : g;
-                } else {
-                    const float x = (float)((double)h[j] * rd);
-                    dw[i][j] = fmaf(d[j], x, dw[i][j]);
-                    const float g = r * (d[j] * (AHEAD ? wk[AHEAD ? i : 0][j] : wt[j]) - x * m);
-                    e[j] = a.dh ? g + e[j] : g;
-                }
+                const float x = LN ? (float)(((double)(h[j] - h0) - md) * rd) : (float)((double)h[j] * rd);
+                dw[i][j] = fmaf(d[j], x, dw[i][j]);
+                if constexpr (LN && !DB_LDS) db[i][j] += d[j];
+                const float gw = d[j] * (AHEAD ? wk[AHEAD ? i : 0][j] : wt[j]);
+                const float g = r * ((LN ? gw - mg : gw) - x * m);
+                e[j] = a.dh ? g + e[j] : g;
+            }
+            if constexpr (DB_LDS) {
+                *db_slot(i, 0) += v4f{d[0], d[1], d[2], d[3]};
+                *db_slot(i, 1) += v4f{d[4], d[5], d[6], d[7]};
             }
             if (v < nv) st16<ST>(a.dx + t * a.H + v * 8, pack8(e));
             if constexpr (VPT > 2) __builtin_amdgcn_sched_barrier(0);
@@ -509,6 +536,12 @@ __device__ __forceinline__ void add_norm_bwd(const NormBwdArgs& a) {
     };
     if (a.dw) part(dw, a.part);
     if constexpr (LN) {
+        if constexpr (DB_LDS) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) db[i][j] = (*db_slot(i, j / 4))[j % 4];
+        }
         if (a.db) {
             if (RPB > 1 && a.dw) __syncthreads();   // s_dw has been read
             part(db, a.part_b);
@@ -517,11 +550,11 @@ __device__ __forceinline__ void add_norm_bwd(const NormBwdArgs& a) {
 }
 
 template <int G, int VPT, bool ST>
-__global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_rmsnorm_bwd(NormBwdArgs a) {
+__global__ __launch_bounds__(G == 64 ? 256 : G) void k_add_rmsnorm_bwd(NormBwdArgs a) {
     add_norm_bwd<G, VPT, ST, false>(a);
 }
 template <int G, int VPT, bool ST>
-__global__ __launch_bounds__(G < 256 ? 256 : G) void k_add_layernorm_bwd(NormBwdArgs a) {
+__global__ __launch_bounds__(G == 64 ? 256 : G) void k_add_layernorm_bwd(NormBwdArgs a) {
     add_norm_bwd<G, VPT, ST, true>(a);
 }
 
@@ -550,34 +583,42 @@ __global__ __launch_bounds__(256) void k_norm_dw(const float* part, int np, int 
     }
 }
 
+template <auto Kern, size_t LDS>
+static hipError_t run_layernorm_bwd(const NormBwdArgs& a, int grid, dim3 block, hipStream_t st) {
+    if (const hipError_t e = ask_for_lds<Kern, LDS>(LDS); e != hipSuccess) return e;
+    hipLaunchKernelGGL(Kern, dim3(grid), block, LDS, st, a);
+    return hipGetLastError();
+}
 template <int G, int VPT, bool LN>
-static void run_norm_bwd(const NormBwdArgs& a, int grid, hipStream_t st) {
-    const dim3 block(G < 256 ? 256 : G);
+static hipError_t run_norm_bwd(const NormBwdArgs& a, int grid, hipStream_t st) {
+    const dim3 block(G == 64 ? 256 : G);
     const bool far = streamed(a.T, a.H);
     if constexpr (LN) {
-        if (far) hipLaunchKernelGGL((k_add_layernorm_bwd<G, VPT, true>), dim3(grid), block, 0, st, a);
-        else hipLaunchKernelGGL((k_add_layernorm_bwd<G, VPT, false>), dim3(grid), block, 0, st, a);
+        constexpr size_t lds = VPT > 4 ? (size_t)VPT * G * 32 : 0;
+        return far ? run_layernorm_bwd<k_add_layernorm_bwd<G, VPT, true>, lds>(a, grid, block, st)
+                   : run_layernorm_bwd<k_add_layernorm_bwd<G, VPT, false>, lds>(a, grid, block, st);
     } else {
         if (far) hipLaunchKernelGGL((k_add_rmsnorm_bwd<G, VPT, true>), dim3(grid), block, 0, st, a);
         else hipLaunchKernelGGL((k_add_rmsnorm_bwd<G, VPT, false>), dim3(grid), block, 0, st, a);
+        return hipGetLastError();
     }
 }
 
 template <bool LN>
 static hipError_t launch_norm_backward(const NormBwdArgs& args, hipStream_t st) {
     NormBwdArgs a = args;
-    const int nv = a.H / 8, grid = norm_bwd_parts(a.T, a.H);
+    const int nv = a.H / 8, grid = LN ? layernorm_bwd_parts(a.T, a.H) : norm_bwd_parts(a.T, a.H);
     const auto odd = [](const float* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; };
     const bool one = grid == 1 && !odd(a.dw) && !odd(a.db);   // the only part is the sum
     if (one) a.part = a.dw, a.part_b = a.db;
-    if (nv <= 64) run_norm_bwd<64, 1, LN>(a, grid, st);
-    else if (nv <= 128) run_norm_bwd<64, 2, LN>(a, grid, st);
-    else if (nv <= 256) run_norm_bwd<256, 1, LN>(a, grid, st);
-    else if (nv <= 512) run_norm_bwd<512, 1, LN>(a, grid, st);
-    else if (nv <= 1024) run_norm_bwd<512, 2, LN>(a, grid, st);
-    else if (nv <= 2048) run_norm_bwd<512, 4, LN>(a, grid, st);
-    else run_norm_bwd<512, 8, LN>(a, grid, st);
-    hipError_t e = hipGetLastError();
+    hipError_t e;
+    if (nv <= 64) e = run_norm_bwd<64, 1, LN>(a, grid, st);
+    else if (nv <= 128) e = run_norm_bwd<64, 2, LN>(a, grid, st);
+    else if (nv <= 256) e = run_norm_bwd<LN ? 128 : 256, LN ? 2 : 1, LN>(a, grid, st);
+    else if (nv <= 512) e = run_norm_bwd<LN ? 256 : 512, LN ? 2 : 1, LN>(a, grid, st);
+    else if (nv <= 1024) e = run_norm_bwd<512, 2, LN>(a, grid, st);
+    else if (nv <= 2048) e = run_norm_bwd<512, 4, LN>(a, grid, st);
+    else e = run_norm_bwd<512, 8, LN>(a, grid, st);
     if (e != hipSuccess || (!a.dw && !a.db) || one) return e;
     const float* first = a.dw ? a.part : a.part_b;
     hipLaunchKernelGGL(k_norm_dw, dim3((unsigned)ceil_div(a.H, 32), a.dw && a.db ? 2 : 1), dim3(256), 0, st, first, grid, a.H,

@@ -4,6 +4,8 @@
 #include "moe_common.h"
 #include "moe_layer_plan.h"
 
+#include <atomic>
+
 namespace moe {
 
 typedef float v2f_t __attribute__((ext_vector_type(2)));
@@ -40,6 +42,25 @@ __device__ __forceinline__ float sum16(float v) {
 // HIP takes fewer than 2^32 threads in a launch: operators with a fixed number of threads per row launch
 // this many rows at a time.
 constexpr int64_t launch_rows(int threads_per_row) { return ((int64_t)1 << 31) / threads_per_row; }
+
+// More than 64 KB of LDS has to be asked for, once per kernel and device.  MOST: the largest request, less than
+// all of it by what the kernel holds in static arrays.
+constexpr int kLdsBytes = 160 * 1024;
+template <auto Kern, size_t MOST = kLdsBytes>
+static hipError_t ask_for_lds(size_t lds) {
+    if (lds <= 64 * 1024) return hipSuccess;
+    static std::atomic<uint64_t> asked{0};   // a bit per device
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev > 63 || !(asked.load(std::memory_order_relaxed) & bit)) {
+        e = hipFuncSetAttribute(reinterpret_cast<const void*>(Kern), hipFuncAttributeMaxDynamicSharedMemorySize, (int)MOST);
+        if (e != hipSuccess) return e;
+        asked.fetch_or(bit, std::memory_order_relaxed);
+    }
+    return hipSuccess;
+}
 
 struct NormArgs {
     int T, H;

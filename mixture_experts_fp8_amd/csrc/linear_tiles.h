@@ -16,7 +16,6 @@
 #include "layer_common.h"
 
 #include <algorithm>
-#include <atomic>
 
 namespace moe {
 
@@ -686,23 +685,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_tile(LinArgs a, int 
     else tile_finish<MI>(a, acc, bias, res, row0, col0);
 }
 
-// More than 64 KB of LDS has to be asked for, once per kernel and device.
-constexpr int kLdsBytes = 160 * 1024;
-template <auto Kern>
-static hipError_t ask_for_lds(size_t lds) {
-    if (lds <= 64 * 1024) return hipSuccess;
-    static std::atomic<uint64_t> asked{0};   // a bit per device
-    int dev = 0;
-    hipError_t e = hipGetDevice(&dev);
-    if (e != hipSuccess) return e;
-    const uint64_t bit = 1ull << (dev & 63);
-    if (dev > 63 || !(asked.load(std::memory_order_relaxed) & bit)) {
-        e = hipFuncSetAttribute(reinterpret_cast<const void*>(Kern), hipFuncAttributeMaxDynamicSharedMemorySize, kLdsBytes);
-        if (e != hipSuccess) return e;
-        asked.fetch_or(bit, std::memory_order_relaxed);
-    }
-    return hipSuccess;
-}
 // Launches a tiled kernel.
 template <auto Kern>
 static hipError_t launch_tiles(const LinArgs& a, int tm, int tn, int threads, size_t lds, hipStream_t st) {

@@ -43,14 +43,14 @@ int moe_add_layernorm(const moe_add_layernorm_args* a) {
 }
 
 size_t moe_add_layernorm_backward_workspace_size(int32_t T, int32_t H) {
-    return T < 1 || H < 1 ? 0 : 2 * moe::norm_bwd_ws_bytes(T, H);
+    return T < 1 || H < 1 ? 0 : moe::layernorm_bwd_ws_bytes(T, H);
 }
 
 int moe_add_layernorm_backward(const moe_add_layernorm_backward_args* a) {
     if (int rc = moe::host::check_add_layernorm_backward(a)) return rc;
     float* part = static_cast<float*>(a->workspace);
     const moe::NormBwdArgs n{a->T, a->H, a->dy, a->h, a->weight, a->eps, a->dh, a->dx, a->dweight,
-                             part, 1.0 / a->H, a->dbias, part ? part + moe::norm_bwd_ws_bytes(a->T, a->H) / 4 : nullptr};
+                             part, 1.0 / a->H, a->dbias, part ? part + moe::layernorm_bwd_ws_bytes(a->T, a->H) / 8 : nullptr};
     return done("moe_add_layernorm_backward", moe::launch_add_layernorm_backward(n, static_cast<hipStream_t>(a->stream)));
 }
 

@@ -15,7 +15,15 @@ int norm_bwd_parts(int T, int H) {
     if (H <= 1024) return (int)std::min<int64_t>(cdiv(T, 4), H <= 512 && T >= 32768 ? 512 : 256);
     return std::min(T, H <= 2048 && T >= 4096 ? 512 : 256);
 }
+// The layer norm forms more sums per row, which more workgroups hide where a thread has two vectors (16384 x 4096:
+// 107 us with 512, 143 with 512 threads and 256; 16384 x 2048: 68 with 1024, 74 with 512 and one vector per thread),
+// once each has several rows (1000 x 4096: 17.1 us with 256, 19.8 with 512).
+int layernorm_bwd_parts(int T, int H) {
+    if (H <= 1024 || H > 4096) return norm_bwd_parts(T, H);
+    return std::min(T, T < 4096 ? 256 : H <= 2048 ? 1024 : 512);
+}
 size_t norm_bwd_ws_bytes(int T, int H) { return (size_t)norm_bwd_parts(T, H) * H * 4; }
+size_t layernorm_bwd_ws_bytes(int T, int H) { return 2 * (size_t)layernorm_bwd_parts(T, H) * H * 4; }
 
 // A workgroup takes 32 rows at once (8 above 256 experts) and the sequences in its rows one after the
 // other.  Up to four rounds in at most four sequences, one workgroup does everything; beyond that one
@@ -265,7 +273,7 @@ int check_add_rmsnorm_backward(const moe_add_rmsnorm_backward_args* a) {
 int check_add_layernorm_backward(const moe_add_layernorm_backward_args* a) {
     const char* op = "moe_add_layernorm_backward";
     if (!a) return fail(MOE_ERR_INVALID, "%s: args must not be NULL", op);
-    return check_norm_backward(op, a, a->dbias, a->T < 1 || a->H < 1 ? 0 : 2 * norm_bwd_ws_bytes(a->T, a->H));
+    return check_norm_backward(op, a, a->dbias, a->T < 1 || a->H < 1 ? 0 : layernorm_bwd_ws_bytes(a->T, a->H));
 }
 
 int check_linear(const moe_linear_args* a) {

@@ -8,6 +8,8 @@ namespace moe {
 // ---- RMS norm backward: weight-gradient partials, one row of H floats per workgroup
 int norm_bwd_parts(int T, int H);   // workgroups (= partial rows) of the backward kernel
 size_t norm_bwd_ws_bytes(int T, int H);
+int layernorm_bwd_parts(int T, int H);            // the same for the layer norm,
+size_t layernorm_bwd_ws_bytes(int T, int H);      // which has a second set of parts for the bias
 
 // ---- balance loss: workgroup b takes rows [b * chunk, (b + 1) * chunk); the part of sequence s
 // in it writes its sums to slot b + s (increasing along the rows, so no two parts share one).

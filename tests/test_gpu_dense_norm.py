@@ -110,12 +110,15 @@ def test_add_layernorm_backward(T, H, with_dh):
     dy, dyf = bf16(0.1 * rng(19, T, H).standard_normal((T, H)))
     out = M.moe_add_layernorm_backward(dy, x, w, 1e-5, dh=r if with_dh else None)
     dx, dw, db, mag, dwmag, dbmag = OD.layernorm_backward(dyf, xf, wf, 1e-5, rf if with_dh else None)
-    # dx: double up to one rounding to float32, the addition of dh and the rounding to bf16
-    within(host(out["dx"]), dx, UB * np.abs(dx) + 4 * U * (1 + UB) * mag + TINY, "dx")
-    # the sums over rows: a workgroup's rows in turn, then the partial rows (a 32nd of them in a chain, 32 chains)
+    # dx: means and xhat in double, of h - h[0] and g in float32 (1 u each).  In float32: mean(g), xhat and
+    # mean(g xhat) rounded (1 u each), xhat mean(g xhat) and two subtractions, the product with r and r itself, the addition of
+    # dh: no term of `mag` passes more than 10 roundings.  Then the rounding to bf16.
+    within(host(out["dx"]), dx, UB * np.abs(dx) + 10 * U * (1 + UB) * mag + TINY, "dx")
+    # the sums over rows, of xhat off by 3 u (h - h[0], which is at most 2 (|xhat| + 1) standard deviations for these h[0],
+    # and its rounding): a workgroup's rows in turn, then the partial rows (a 32nd of them in a chain, 32 chains)
     parts = B.lib().moe_add_layernorm_backward_workspace_size(T, H) // (8 * H)
     chain = -(-T // parts) + 4 + -(-parts // 32) + 32
-    within(host(out["dweight"]), dw, (chain + 4) * U * dwmag + 1e-38, "dweight")
+    within(host(out["dweight"]), dw, (chain + 8) * U * dwmag + 8 * U * dbmag + 1e-38, "dweight")
     within(host(out["dbias"]), db, (chain + 4) * U * dbmag + 1e-38, "dbias")
     again = M.moe_add_layernorm_backward(dy, x, w, 1e-5, dh=r if with_dh else None)
     assert all(torch.equal(again[n], out[n]) for n in out)
@@ -146,12 +149,12 @@ def test_add_layernorm_backward_special_rows(H):
     w, wf = f32(1 + 0.1 * g.standard_normal(H))
     out = M.moe_add_layernorm_backward(dy, h, w, 1e-5)
     dx, _, _, mag, _, _ = OD.layernorm_backward(dyf, hf, wf, 1e-5)
-    within(host(out["dx"]), dx, UB * np.abs(dx) + 4 * U * (1 + UB) * mag + TINY, "dx")
+    within(host(out["dx"]), dx, UB * np.abs(dx) + 10 * U * (1 + UB) * mag + TINY, "dx")
     for row in range(8):
         one = M.moe_add_layernorm_backward(dy[row:row + 1], h[row:row + 1], w, 1e-5)
         assert torch.equal(one["dx"], out["dx"][row:row + 1])
         _, dw, db, _, dwmag, _ = OD.layernorm_backward(dyf[row:row + 1], hf[row:row + 1], wf, 1e-5)
-        within(host(one["dweight"]), dw, 6 * U * dwmag + 1e-38, "dweight")
+        within(host(one["dweight"]), dw, 8 * U * (dwmag + np.abs(dyf[row])) + 1e-38, "dweight")
         assert np.array_equal(host(one["dbias"]), db)
     bad = h.clone()
     bad[0, 3], bad[1, 5] = float("inf"), float("nan")
