@@ -595,7 +595,7 @@ int moe_gated_linear(const moe_gated_linear_args* a);
  *   All but dbias, xs and w_scale 16-byte aligned.
  *   workspace  >= moe_gated_linear_backward_workspace_size(T, K, I, dx != NULL, dw != NULL, dbias != NULL)
  *              bytes, 256-byte aligned (NULL where that is 0).
- * Deterministic. */
+ * Deterministic; the order of the sums depends on the sizes and on which outputs are asked for. */
 typedef struct moe_gated_linear_backward_args {
     int32_t T, K, I;
     const uint16_t* dh;

@@ -61,12 +61,12 @@ __device__ __forceinline__ v4u_t column_of(const uint4 (&r)[8], int c) {
 }
 
 struct DguArgs {
-    int T, I, NT;           // NT: blocks of 64 rows
+    int T, I, NT, parts;    // blocks of 64 rows; block b is of part b % parts
     const uint16_t* dh;
     const uint16_t* gu;
     uint16_t* dgu;
     uint8_t* packed;        // or NULL: dgu as column fragments whose K is the row, rows past T 0
-    float* part;            // or NULL: [gridDim.x][2I] column sums
+    float* part;            // or NULL: [parts][2I] column sums
 };
 
 // A wave takes 64 columns of g and u and blocks of 64 rows, a grid apart; lane (t = l / 8, c = l % 8) the rows
@@ -74,15 +74,15 @@ struct DguArgs {
 // registers.  The fragments of the transposed result go through LDS, so that they leave in whole kilobytes;
 // slots are swizzled by t, which spreads the lanes' 16-byte writes over the banks.
 template <int ACT, bool PACK>
-__global__ __launch_bounds__(256) void k_gated_dgu(DguArgs a) {
-    __shared__ __align__(16) uint8_t s_frag[4][PACK ? 8192 : 16];
+__device__ __forceinline__ void gated_dgu(const DguArgs& a, int unit, uint8_t* smem) {
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int t8 = lane >> 3, c8 = lane & 7, col = (blockIdx.y * 4 + wv) * 64 + 8 * c8;
+    const int cols = (unit / a.parts * 4 + wv) * 64, first = unit % a.parts;
+    const int t8 = lane >> 3, c8 = lane & 7, col = cols + 8 * c8;
     const bool on = col < a.I;
-    if ((blockIdx.y * 4 + wv) * 64 >= a.I) return;   // (uniform; no barrier follows)
+    if (cols >= a.I) return;   // (uniform; no barrier follows)
     const int64_t N = 2 * (int64_t)a.I;
     float sg[8] = {}, su[8] = {};
-    for (int b = blockIdx.x; b < a.NT; b += gridDim.x) {
+    for (int b = first; b < a.NT; b += a.parts) {
         uint4 g[8], u[8], d[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -118,7 +118,7 @@ __global__ __launch_bounds__(256) void k_gated_dgu(DguArgs a) {
             }
         }
         if constexpr (PACK) {
-            v4u_t* s = reinterpret_cast<v4u_t*>(s_frag[wv]);
+            v4u_t* s = reinterpret_cast<v4u_t*>(smem + wv * 8192);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
 #pragma unroll
@@ -126,12 +126,12 @@ __global__ __launch_bounds__(256) void k_gated_dgu(DguArgs a) {
                     s[(c8 >> 1) * 128 + t8 * 16 + ((8 * (c8 & 1) + c) ^ t8)] = column_of(half ? u : g, c);
                 asm volatile("" ::: "memory");   // (a wave's LDS accesses stay in order)
                 __builtin_amdgcn_wave_barrier();
-                const int n0 = (half ? a.I : 0) / 16 + (blockIdx.y * 4 + wv) * 4;
+                const int n0 = ((half ? a.I : 0) + cols) / 16;
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {    // fragment q / 2, its lower and upper kilobyte
                     const int p = (q & 1) * 64 + lane, r = p >> 4;
                     const v4u_t v = s[(q >> 1) * 128 + r * 16 + ((p & 15) ^ r)];
-                    if ((blockIdx.y * 4 + wv) * 64 + 16 * (q >> 1) < a.I)
+                    if (cols + 16 * (q >> 1) < a.I)
                         *reinterpret_cast<v4u_t*>(a.packed + ((int64_t)(n0 + (q >> 1)) * a.NT + b) * kFragBytes + p * 16) = v;
                 }
                 asm volatile("" ::: "memory");
@@ -149,7 +149,7 @@ __global__ __launch_bounds__(256) void k_gated_dgu(DguArgs a) {
             }
         }
         if (t8 == 0 && on) {
-            float* p = a.part + (int64_t)blockIdx.x * N + col;
+            float* p = a.part + (int64_t)first * N + col;
 #pragma unroll
             for (int j = 0; j < 8; ++j) p[j] = sg[j], p[a.I + j] = su[j];
         }
@@ -159,9 +159,9 @@ __global__ __launch_bounds__(256) void k_gated_dgu(DguArgs a) {
 // x^T as bf16 [K][64 NT], 0 behind row T.  A wave takes 64 rows and 64 columns, a lane 8 x 8 of them; its
 // 16-byte vectors of 8 rows make 128 bytes of a row of the result.
 template <bool MX>
-__global__ __launch_bounds__(256) void k_rows_transposed(const uint8_t* xq, const uint8_t* xs, int T, int K, int NT, uint16_t* xt) {
+__device__ __forceinline__ void rows_transposed(const uint8_t* xq, const uint8_t* xs, int T, int K, int NT, uint16_t* xt, int unit) {
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    const int t0 = blockIdx.x * 64 + 8 * (lane & 7), k0 = (blockIdx.y * 4 + wv) * 64 + 8 * (lane >> 3);
+    const int t0 = unit % NT * 64 + 8 * (lane & 7), k0 = (unit / NT * 4 + wv) * 64 + 8 * (lane >> 3);
     if (k0 >= K) return;
     constexpr int gs = MX ? 32 : 128;
     uint2 q[8];
@@ -193,10 +193,10 @@ __global__ __launch_bounds__(256) void k_rows_transposed(const uint8_t* xq, cons
 // The packed FP8 weights [K][N] as bf16 fragments of 16 rows of w whose K is the column: a workgroup turns 4
 // fragments of 16 columns x 128 rows into 8 of 16 rows x 64 columns.
 template <bool MX>
-__global__ __launch_bounds__(256) void k_weights_transposed(const uint8_t* w, const uint8_t* ws, int K, int N, uint8_t* out) {
-    __shared__ __align__(16) uint8_t s_w[4 * kFragBytes];
-    __shared__ uint8_t s_s[4 * 64];
-    const int tid = threadIdx.x, jb = blockIdx.x, kb = blockIdx.y, KB = K / kGroup, NJ = N / 64;
+__device__ __forceinline__ void weights_transposed(const uint8_t* w, const uint8_t* ws, int K, int N, uint8_t* out, int unit,
+                                                   uint8_t* s_w) {
+    uint8_t* s_s = s_w + 4 * kFragBytes;
+    const int tid = threadIdx.x, KB = K / kGroup, NJ = N / 64, jb = unit % NJ, kb = unit / NJ;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int p = i * 256 + tid, f = p >> 7;
@@ -226,27 +226,148 @@ __global__ __launch_bounds__(256) void k_weights_transposed(const uint8_t* w, co
     }
 }
 
-template <bool PACK>
-void run_dgu(const DguArgs& a, int act, dim3 grid, hipStream_t st) {
-    switch (act) {
-        case MOE_ACT_RELU: hipLaunchKernelGGL((k_gated_dgu<MOE_ACT_RELU, PACK>), grid, dim3(256), 0, st, a); break;
-        case MOE_ACT_SILU: hipLaunchKernelGGL((k_gated_dgu<MOE_ACT_SILU, PACK>), grid, dim3(256), 0, st, a); break;
-        case MOE_ACT_GELU: hipLaunchKernelGGL((k_gated_dgu<MOE_ACT_GELU, PACK>), grid, dim3(256), 0, st, a); break;
-        case MOE_ACT_GELU_TANH: hipLaunchKernelGGL((k_gated_dgu<MOE_ACT_GELU_TANH, PACK>), grid, dim3(256), 0, st, a); break;
-        default: hipLaunchKernelGGL((k_gated_dgu<MOE_ACT_NONE, PACK>), grid, dim3(256), 0, st, a);
+// The operands of both products in one launch: workgroups of dgu, of x^T and of the weights.  (One after the other
+// the three took 13.3, 4.6 and 4.2 us at 2047 x 768 x 1152, where neither fills the chip.)
+struct PrepareArgs {
+    DguArgs d;
+    int K, dgu_units, row_units;          // workgroups of each, the rest the weights'
+    const uint8_t *xq, *xs, *w, *ws;
+    uint16_t* xt;
+    uint8_t* wt;
+};
+template <int ACT, bool MX, bool PACK>
+__global__ __launch_bounds__(256) void k_gated_prepare(PrepareArgs a) {
+    __shared__ __align__(16) uint8_t smem[PACK ? 32768 : 4 * kFragBytes + 256];
+    int unit = blockIdx.x;
+    if (unit < a.dgu_units) return gated_dgu<ACT, PACK>(a.d, unit, smem);
+    unit -= a.dgu_units;
+    if (unit < a.row_units) return rows_transposed<MX>(a.xq, a.xs, a.d.T, a.K, a.d.NT, a.xt, unit);
+    weights_transposed<MX>(a.w, a.ws, a.K, 2 * a.d.I, a.wt, unit - a.row_units, smem);
+}
+
+template <int ACT>
+void run_prepare(const PrepareArgs& a, bool mx, unsigned grid, hipStream_t st) {
+    if (a.xt) {
+        if (mx) hipLaunchKernelGGL((k_gated_prepare<ACT, true, true>), dim3(grid), dim3(256), 0, st, a);
+        else hipLaunchKernelGGL((k_gated_prepare<ACT, false, true>), dim3(grid), dim3(256), 0, st, a);
+    } else {
+        if (mx) hipLaunchKernelGGL((k_gated_prepare<ACT, true, false>), dim3(grid), dim3(256), 0, st, a);
+        else hipLaunchKernelGGL((k_gated_prepare<ACT, false, false>), dim3(grid), dim3(256), 0, st, a);
     }
 }
 
-// Tile by the number of workgroups, as launch_linear's.
-hipError_t launch_product(const LinArgs& args, hipStream_t st) {
-    LinArgs a = args;
-    a.nt = (int64_t)a.T * a.N * (a.out_bf16 ? 2 : 4) >= (32 << 20);
-    auto fits = [&](int rows, int cols, int64_t most) { return ceil_div(a.T, rows) * ceil_div(a.N, cols) <= most; };
-    if (fits(64, 64, 256)) return run_deep_t<kBf16, false, 1, 4, 4, 1, 4, 2>(a, st);
-    if (fits(64, 128, 256)) return run_deep_t<kBf16, false, 2, 4, 2, 2, 4, 1>(a, st);
-    if (fits(64, 128, 512)) return run_deep_t<kBf16, false, 2, 4, 2, 2, 3, 1>(a, st);
-    if (fits(128, 256, 256)) return run_deep_t<kBf16, false, 4, 4, 2, 4, 3, 1>(a, st);
-    return run_tile_t<kBf16, false, 8, 4, 1, 4>(a, st);
+// Both products in one launch: workgroups [0, first_units) compute the tiles of p[0], the next ones those of p[1], the
+// last ones the bias's gradient from its parts.  One launch fills the chip where either product alone leaves it half
+// empty, and has one last round.
+struct ProductsArgs {
+    LinArgs p[2];
+    int tm[2], tn[2];
+    int units[2], parts[2], per[2];   // workgroups of a part, parts of the sum (0: not asked for), K blocks of one
+    float* join[2];              // more than one part: [parts][rows][columns]
+    const float* sums;           // the bias's parts, [sum_parts][n]
+    int sum_parts, n;
+    float* dbias;
+};
+// 32 columns of the parts' sum, as k_norm_dw adds them.
+__device__ __forceinline__ void column_sums(const float* part, int np, int n, float* out, int unit, float* s) {
+    const int c = threadIdx.x & 7, g = threadIdx.x >> 3, col = unit * 32 + 4 * c;   // (256 threads, or the first 256)
+    if (g < 32) {
+        v4f v = {0.f, 0.f, 0.f, 0.f};
+        if (col < n) {
+#pragma unroll 8
+            for (int p = g; p < np; p += 32) v += *reinterpret_cast<const v4f*>(part + (int64_t)p * n + col);
+        }
+        *reinterpret_cast<v4f*>(s + g * 32 + 4 * c) = v;
+    }
+    __syncthreads();
+    const int o = unit * 32 + threadIdx.x;
+    if (threadIdx.x < 32 && o < n) {
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) t += s[i * 32 + threadIdx.x];
+        out[o] = t;
+    }
+}
+template <int MI, int WM, int WN, int S, int KS, bool TILE>
+__global__ __launch_bounds__(64 * WM * WN * KS, TILE ? 2 : 1) void k_gated_products(ProductsArgs a) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    int unit = blockIdx.x;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if (unit < a.units[i] * a.parts[i]) {
+            LinArgs l = a.p[i];
+            const int KB = l.K / kGroup;
+            Blocks b{0, KB};
+            if (a.parts[i] > 1) {
+                int z = 0;   // (few parts: no division)
+                while (unit >= a.units[i]) unit -= a.units[i], ++z;
+                b = {z * a.per[i], min(a.per[i], KB - z * a.per[i])};   // (no part is empty: product_plan)
+                l.y = a.join[i] + (int64_t)z * l.T * l.N;
+                l.ldy = l.N, l.out_bf16 = 0;
+            }
+            if constexpr (TILE) return linear_tile<kBf16, false, MI, 4, WM, WN>(l, unit, a.tm[i], a.tn[i], b);
+            else return linear_deep<kBf16, false, MI, 4, WM, WN, S, KS>(l, unit, a.tm[i], a.tn[i], b);
+        }
+        unit -= a.units[i] * a.parts[i];
+    }
+    column_sums(a.sums, a.sum_parts, a.n, a.dbias, unit, reinterpret_cast<float*>(smem));
+}
+
+// The sum of a product's parts, eight values per thread.
+struct JoinArgs {
+    const float* join[2];
+    void* y[2];
+    int parts[2], bf16[2];
+    int64_t n[2];            // values; 0: not in parts
+};
+__global__ __launch_bounds__(256) void k_gated_join(JoinArgs a) {
+    int64_t v = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+    int i = 0;
+    if (v >= a.n[0]) v -= a.n[0], i = 1;
+    if (v >= a.n[i]) return;
+    v4f s[2] = {};
+#pragma unroll 4
+    for (int z = 0; z < a.parts[i]; ++z) {
+        const v4f* p = reinterpret_cast<const v4f*>(a.join[i] + z * a.n[i] + v);
+        s[0] += p[0];
+        s[1] += p[1];
+    }
+    if (a.bf16[i]) {
+        const float f[8] = {s[0][0], s[0][1], s[0][2], s[0][3], s[1][0], s[1][1], s[1][2], s[1][3]};
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y[i]) + v) = pack8(f);
+    } else {
+        v4f* d = reinterpret_cast<v4f*>(static_cast<float*>(a.y[i]) + v);
+        d[0] = s[0];
+        d[1] = s[1];
+    }
+}
+
+template <int MI, int WM, int WN, int S, int KS, bool TILE>
+hipError_t run_products(ProductsArgs a, int bias_units, hipStream_t st) {
+    constexpr int ROWS = 16 * MI * WM, COLS = 64 * WN;
+    unsigned grid = bias_units;
+    for (int i = 0; i < 2; ++i) {
+        if (!a.parts[i]) continue;
+        a.tm[i] = (int)ceil_div(a.p[i].T, ROWS);
+        a.tn[i] = (int)ceil_div(a.p[i].N, COLS);
+        a.units[i] = (int)(ceil_div((int64_t)a.tm[i] * a.tn[i], 8) * 8);
+        a.per[i] = (int)ceil_div(a.p[i].K / kGroup, a.parts[i]);
+        grid += a.units[i] * a.parts[i];
+    }
+    constexpr size_t lds = TILE ? 3 * ROWS * kGroup + scales_lds<kBf16, false>(ROWS, COLS, 0, 0) : deep_lds<kBf16, false>(ROWS, COLS, KS * S, 1);
+    if (const hipError_t e = ask_for_lds<k_gated_products<MI, WM, WN, S, KS, TILE>>(lds); e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_gated_products<MI, WM, WN, S, KS, TILE>), dim3(grid), dim3(64 * WM * WN * KS), lds, st, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_products(const ProductsArgs& a, int tile, int bias_units, hipStream_t st) {
+    switch (tile) {   // (product_plan's table)
+        case 0: return run_products<1, 4, 1, 4, 2, false>(a, bias_units, st);
+        case 1: return run_products<2, 2, 2, 4, 1, false>(a, bias_units, st);
+        case 2: return run_products<2, 2, 2, 3, 1, false>(a, bias_units, st);
+        case 3: return run_products<4, 2, 4, 3, 1, false>(a, bias_units, st);
+        default: return run_products<8, 1, 4, 1, 1, true>(a, bias_units, st);
+    }
 }
 
 }  // namespace
@@ -256,35 +377,46 @@ hipError_t launch_gated_backward(const GatedBwdArgs& a, hipStream_t st) {
     const int N = 2 * a.I, NT = p.row_blocks;
     uint8_t* ws = a.ws;
     float* part = a.dbias ? reinterpret_cast<float*>(ws + p.part) : nullptr;
-    const DguArgs d{a.T, a.I, NT, a.dh, a.gu, a.dgu, a.dw ? ws + p.dgu_packed : nullptr, part};
-    const dim3 grid((unsigned)(a.dbias ? p.parts : NT), (unsigned)ceil_div(a.I, 256));
-    if (a.dw) run_dgu<true>(d, a.act, grid, st);
-    else run_dgu<false>(d, a.act, grid, st);
-    hipError_t e = hipGetLastError();
-    if (e == hipSuccess && a.dbias) e = launch_column_sums(part, p.parts, N, a.dbias, st);
-    if (e != hipSuccess) return e;
-    if (a.dx) {
-        const dim3 g((unsigned)(N / 64), (unsigned)(a.K / kGroup));
-        if (a.mx) hipLaunchKernelGGL(k_weights_transposed<true>, g, dim3(256), 0, st, a.w, a.wsc, a.K, N, ws + p.weights);
-        else hipLaunchKernelGGL(k_weights_transposed<false>, g, dim3(256), 0, st, a.w, a.wsc, a.K, N, ws + p.weights);
-        LinArgs l{};
-        l.T = a.T, l.K = 2 * N, l.N = a.K;
-        l.xq = reinterpret_cast<const uint8_t*>(a.dgu), l.w = ws + p.weights;
-        l.y = a.dx, l.ldy = a.K, l.out_bf16 = 1;
-        if ((e = hipGetLastError()) != hipSuccess || (e = launch_product(l, st)) != hipSuccess) return e;
+    PrepareArgs r{{a.T, a.I, NT, a.dbias ? p.parts : NT, a.dh, a.gu, a.dgu, a.dw ? ws + p.dgu_packed : nullptr, part},
+                  a.K, 0, 0, a.xq, a.xs, a.w, a.wsc, a.dw ? reinterpret_cast<uint16_t*>(ws + p.rows) : nullptr,
+                  a.dx ? ws + p.weights : nullptr};
+    r.dgu_units = r.d.parts * (int)ceil_div(a.I, 256);
+    r.row_units = a.dw ? NT * (int)ceil_div(a.K, 256) : 0;
+    const unsigned grid = r.dgu_units + r.row_units + (a.dx ? N / 64 * (a.K / kGroup) : 0);
+    switch (a.act) {
+        case MOE_ACT_RELU: run_prepare<MOE_ACT_RELU>(r, a.mx, grid, st); break;
+        case MOE_ACT_SILU: run_prepare<MOE_ACT_SILU>(r, a.mx, grid, st); break;
+        case MOE_ACT_GELU: run_prepare<MOE_ACT_GELU>(r, a.mx, grid, st); break;
+        case MOE_ACT_GELU_TANH: run_prepare<MOE_ACT_GELU_TANH>(r, a.mx, grid, st); break;
+        default: run_prepare<MOE_ACT_NONE>(r, a.mx, grid, st);
     }
-    if (a.dw) {
-        const dim3 g((unsigned)NT, (unsigned)ceil_div(a.K, 256));
-        uint16_t* xt = reinterpret_cast<uint16_t*>(ws + p.rows);
-        if (a.mx) hipLaunchKernelGGL(k_rows_transposed<true>, g, dim3(256), 0, st, a.xq, a.xs, a.T, a.K, NT, xt);
-        else hipLaunchKernelGGL(k_rows_transposed<false>, g, dim3(256), 0, st, a.xq, a.xs, a.T, a.K, NT, xt);
-        LinArgs l{};
-        l.T = a.K, l.K = 128 * NT, l.N = N;
-        l.xq = ws + p.rows, l.w = ws + p.dgu_packed;
-        l.y = a.dw, l.ldy = N, l.out_bf16 = a.dw_bf16;
-        if ((e = hipGetLastError()) != hipSuccess || (e = launch_product(l, st)) != hipSuccess) return e;
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    if (!a.dx && !a.dw) return a.dbias ? launch_column_sums(part, p.parts, N, a.dbias, st) : hipSuccess;
+    ProductsArgs q{};
+    const int kw = p.product.first;   // the product with the longer sums first
+    LinArgs &dw = q.p[kw], &dx = q.p[!kw];
+    dx.T = a.T, dx.K = 2 * N, dx.N = a.K;
+    dx.xq = reinterpret_cast<const uint8_t*>(a.dgu), dx.w = ws + p.weights;
+    dx.y = a.dx, dx.ldy = a.K, dx.out_bf16 = 1, dx.nt = (int64_t)a.T * a.K * 2 >= (32 << 20);
+    dw.T = a.K, dw.K = 128 * NT, dw.N = N;
+    dw.xq = ws + p.rows, dw.w = ws + p.dgu_packed;
+    dw.y = a.dw, dw.ldy = N, dw.out_bf16 = a.dw_bf16, dw.nt = (int64_t)a.K * N * (a.dw_bf16 ? 2 : 4) >= (32 << 20);
+    JoinArgs j{};
+    int64_t joined = 0;
+    for (int i = 0; i < 2; ++i) {
+        const int which = i == kw ? 1 : 0;   // the plan's order: dx, dw
+        q.parts[i] = p.product.parts[which];
+        if (q.parts[i] < 2) continue;
+        q.join[i] = reinterpret_cast<float*>(ws + p.join[which]);
+        q.p[i].nt = 0;                       // read again at once
+        j.join[i] = q.join[i], j.y[i] = q.p[i].y, j.parts[i] = q.parts[i], j.bf16[i] = q.p[i].out_bf16;
+        j.n[i] = (int64_t)q.p[i].T * q.p[i].N;
+        joined += j.n[i];
     }
-    return hipSuccess;
+    q.n = N, q.sums = part, q.sum_parts = p.parts, q.dbias = a.dbias;
+    if (const hipError_t e = launch_products(q, p.product.tile, a.dbias ? (int)ceil_div(N, 32) : 0, st); e != hipSuccess || !joined) return e;
+    hipLaunchKernelGGL(k_gated_join, dim3((unsigned)ceil_div(joined, 2048)), dim3(256), 0, st, j);
+    return hipGetLastError();
 }
 
 }  // namespace moe

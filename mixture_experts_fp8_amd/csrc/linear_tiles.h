@@ -465,8 +465,8 @@ __device__ __forceinline__ void gated_finish(const LinArgs& a, v4f (&acc)[MI][4]
 // Work order: workgroup L runs on XCD L % 8; XCD x takes a contiguous share of the list, which walks the
 // row tiles in groups of 8 with the column tile outside, so that one XCD's workgroups share both
 // operands through its L2.  False for the holes behind the last tile.
-__device__ __forceinline__ bool tile_of(int tiles_m, int tiles_n, int& tm, int& tn) {
-    const int total = tiles_m * tiles_n, per = (total + 7) / 8, L = blockIdx.x;
+__device__ __forceinline__ bool tile_of(int L, int tiles_m, int tiles_n, int& tm, int& tn) {
+    const int total = tiles_m * tiles_n, per = (total + 7) / 8;
     const int w = (L & 7) * per + (L >> 3);
     if ((L >> 3) >= per || w >= total) return false;
     const int sb = w / (8 * tiles_n), r = w - sb * 8 * tiles_n, g = min(8, tiles_m - sb * 8);
@@ -517,8 +517,13 @@ __device__ __forceinline__ void load_bias(const LinArgs& a, float* s_bias, int t
     }
 }
 
+// The K blocks that a workgroup sums (kBf16; with FP8 always all of them).
+struct Blocks {
+    int first, n;
+};
+
 template <Format F, bool GATED, int MI, int NJ, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_tile(LinArgs a, int tiles_m, int tiles_n) {
+__device__ __forceinline__ void linear_tile(const LinArgs& a, int L, int tiles_m, int tiles_n, Blocks part = {}) {
     static_assert(NJ == 4, "the epilogue takes 64 columns");
     constexpr bool MX = F == kMicro;
     constexpr int NW = WM * WN, ROWS = 16 * MI * WM, NTH = 64 * NW, DMA = ROWS * 8 / NTH;
@@ -527,13 +532,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_tile(LinArgs a, int 
     extern __shared__ __align__(16) uint8_t smem[];
     uint8_t* s_a = smem;                       // [3][ROWS][128]
     uint8_t* s_x = smem + 3 * STAGE;           // MX: [3][WM][16][MI] dwords; else [KB][WM][16][MI] bytes
-    const int KB = a.K / kGroup, nbs = (a.N + kGroup - 1) / kGroup;
+    const int KB = a.K / kGroup, K0 = F == kBf16 ? part.first : 0, KN = F == kBf16 ? part.n : KB, nbs = (a.N + kGroup - 1) / kGroup;
     constexpr int COLS = 16 * NJ * WN, NBW = tile_scales<GATED>(COLS);
     uint8_t* s_w = s_x + KB * ROWS;            // (128-element scales) [KB][scales of the tile]
     float* s_bias = reinterpret_cast<float*>(F != kBlock ? s_x + 3 * SCST : s_w + (KB * NBW + 15) / 16 * 16);   // [COLS]
 
     int tm, tn;
-    if (!tile_of(tiles_m, tiles_n, tm, tn)) return;
+    if (!tile_of(L, tiles_m, tiles_n, tm, tn)) return;
     // Two workgroups share a CU.  The one that was dealt second runs ahead at equal work, so that their
     // epilogues (memory) and K loops (matrix cores) fall apart: 4 us of 267 at 16384 x 4096 x 4096.
     if (MI > 4 && ((blockIdx.x >> 8) & 1)) __builtin_amdgcn_s_setprio(1);
@@ -553,7 +558,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_tile(LinArgs a, int 
     for (int i = 0; i < DMA; ++i) {
         const int row = min(m0 + 8 * (wv + NW * i) + (lane >> 3), a.T - 1), slot = (lane & 7) ^ (lane >> 3);
         const int chunk = F != kBlock ? slot : (slot < 4 ? 2 * slot : 2 * slot - 7);
-        aoff[i] = (uint32_t)row * (uint32_t)a.K + 16 * chunk;
+        aoff[i] = (uint32_t)row * (uint32_t)a.K + 16 * chunk + K0 * kGroup;
     }
     const uint32_t lds_w = lds_addr(s_a) + wv * 1024;
     uint32_t xoff = 0, lds_x = 0;   // MX: the row scales' dwords (waves past ROWS / 64 copy the last 64 again)
@@ -576,7 +581,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_tile(LinArgs a, int 
     uint32_t wfrag[NJ];
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
-        wfrag[j] = __builtin_amdgcn_readfirstlane((uint32_t)column_fragment<GATED>(a, tn, COLS, wn * NJ + j) * (uint32_t)KB);
+        wfrag[j] = __builtin_amdgcn_readfirstlane((uint32_t)column_fragment<GATED>(a, tn, COLS, wn * NJ + j) * (uint32_t)KB + K0);
     const uint32_t l16 = 16 * lane;
     struct Wt {
         v8i w[NJ];
@@ -603,7 +608,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_tile(LinArgs a, int 
     };
     Wt W0, W1;
     issue(0, 0);
-    issue(min(1, KB - 1), 1);
+    issue(min(1, KN - 1), 1);
     load_w(0, W0);
     load_bias<GATED, COLS, NTH>(a, s_bias, tn);
     if constexpr (F == kBlock) load_scale_tables<GATED, MI, ROWS, COLS, NTH>(a, s_x, s_w, KB, nbs, m0, tn);
@@ -637,8 +642,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_tile(LinArgs a, int 
     auto step = [&](int kb, Wt& W, Wt& N) __attribute__((always_inline)) {
         const int s1 = st == 2 ? 0 : st + 1, s2 = s1 == 2 ? 0 : s1 + 1;
         // (past the end the last block again, unused: the loop has no branches)
-        load_w(min(kb + 1, KB - 1), N);
-        issue(min(kb + 2, KB - 1), s2);
+        load_w(min(kb + 1, KN - 1), N);
+        issue(min(kb + 2, KN - 1), s2);
         int sx[(MI + 3) / 4] = {}, sw[2] = {};   // 128-element scales: byte mi % 4 of sx[mi / 4]; gate's and up's
         if constexpr (F == kBlock) {
             const int* p = reinterpret_cast<const int*>(s_x + kb * ROWS + (wm * 16 + r16) * MI);
@@ -671,11 +676,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_tile(LinArgs a, int 
         st = s1;
     };
     int kb = 0;
-    for (; kb + 2 <= KB; kb += 2) {
+    for (; kb + 2 <= KN; kb += 2) {
         step(kb, W0, W1);
         step(kb + 1, W1, W0);
     }
-    if (kb < KB) step(kb, W0, W1);
+    if (kb < KN) step(kb, W0, W1);
 
     if constexpr (MI > 4 && !GATED) tile_residual<MI>(a, res, row0, col0);
     v4f bias[4];
@@ -683,6 +688,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_tile(LinArgs a, int 
     for (int j = 0; j < 4; ++j) bias[j] = *reinterpret_cast<const v4f*>(s_bias + wn * NJ * 16 + 16 * j + 4 * G);
     if constexpr (GATED) gated_finish<MI>(a, acc, bias, row0, col0);
     else tile_finish<MI>(a, acc, bias, res, row0, col0);
+}
+
+template <Format F, bool GATED, int MI, int NJ, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_tile(LinArgs a, int tiles_m, int tiles_n) {
+    linear_tile<F, GATED, MI, NJ, WM, WN>(a, blockIdx.x, tiles_m, tiles_n);
 }
 
 // Launches a tiled kernel.
@@ -722,7 +732,7 @@ __device__ __forceinline__ void wait_vm() {
 }
 
 template <Format F, bool GATED, int MI, int NJ, int WM, int WN, int S, int KS>
-__global__ __launch_bounds__(64 * WM * WN * KS, 1) void k_linear_deep(LinArgs a, int tiles_m, int tiles_n) {
+__device__ __forceinline__ void linear_deep(const LinArgs& a, int L, int tiles_m, int tiles_n, Blocks part = {}) {
     constexpr bool MX = F == kMicro;
     constexpr int NW = WM * WN, ROWS = 16 * MI * WM, COLS = 16 * NJ * WN, NTH = 64 * NW * KS;
     constexpr int DX = ROWS / 8 / NW, DW = COLS / 8 / NW;            // 1 KB copies of a wave and block
@@ -732,13 +742,13 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 1) void k_linear_deep(LinArgs a,
     constexpr int STAGE = XB + WB + XS + WS, OPS = DX + DW + DS;
     static_assert(ROWS / 8 % NW == 0 && COLS / 8 % NW == 0 && ROWS % 64 == 0 && COLS % 64 == 0 && S >= 3, "whole copies");
     extern __shared__ __align__(16) uint8_t smem[];
-    const int KB = a.K / kGroup, nbs = (a.N + kGroup - 1) / kGroup;
+    const int KB = a.K / kGroup, K0 = F == kBf16 ? part.first : 0, KN = F == kBf16 ? part.n : KB, nbs = (a.N + kGroup - 1) / kGroup;
     constexpr int NBW = tile_scales<GATED>(COLS), gpb = MX ? 4 : 1;
     uint8_t* s_x = smem + KS * S * STAGE;            // (128-element scales) [KB][WM][16][MI] bytes
     uint8_t* s_w = s_x + KB * ROWS;             // (128-element scales) [KB][scales of the tile]
     float* s_bias = reinterpret_cast<float*>(F != kBlock ? s_x : s_w + (KB * NBW + 15) / 16 * 16);   // [COLS]
     int tm, tn;
-    if (!tile_of(tiles_m, tiles_n, tm, tn)) return;
+    if (!tile_of(L, tiles_m, tiles_n, tm, tn)) return;
     const int tid = threadIdx.x, lane = tid & 63, w0 = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int ks = w0 / NW, wv = w0 % NW;       // set of waves, wave of the set
     const int wm = wv / WN, wn = wv % WN, r16 = lane & 15, G = lane >> 4, x8 = r16 & 7;
@@ -758,12 +768,12 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 1) void k_linear_deep(LinArgs a,
     for (int i = 0; i < DX; ++i) {
         const int row = min(m0 + 8 * (wv + NW * i) + (lane >> 3), a.T - 1), slot = (lane & 7) ^ (lane >> 3);
         const int chunk = F != kBlock ? slot : (slot < 4 ? 2 * slot : 2 * slot - 7);
-        xoff[i] = (uint32_t)row * (uint32_t)a.K + 16 * chunk;
+        xoff[i] = (uint32_t)row * (uint32_t)a.K + 16 * chunk + K0 * kGroup;
     }
 #pragma unroll
     for (int i = 0; i < DW; ++i) {
         const int g = wv + NW * i;
-        wsrc[i] = __builtin_amdgcn_readfirstlane((uint32_t)column_fragment<GATED>(a, tn, COLS, g >> 1) * (uint32_t)KB * kFragBytes + (g & 1) * 1024);
+        wsrc[i] = __builtin_amdgcn_readfirstlane((uint32_t)column_fragment<GATED>(a, tn, COLS, g >> 1) * (uint32_t)KB * kFragBytes + (g & 1) * 1024 + K0 * kFragBytes);
     }
     const uint32_t l16 = 16 * lane, lds0 = lds_addr(ring);
     uint32_t soff[DS ? DS : 1], sdst[DS ? DS : 1];
@@ -785,7 +795,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 1) void k_linear_deep(LinArgs a,
         }
     }
     auto issue = [&](int blk, int st) __attribute__((always_inline)) {   // the set's block: K block blk KS + ks
-        const int kb = min(blk * KS + ks, KB - 1);   // (past the end the last block again: the count per step stays)
+        const int kb = min(blk * KS + ks, KN - 1);   // (past the end the last block again: the count per step stays)
         const uint32_t base = __builtin_amdgcn_readfirstlane(lds0 + st * STAGE + wv * 1024);
 #pragma unroll
         for (int i = 0; i < DX; ++i) dma16(rx, base + i * NW * 1024, xoff[i], kb * kGroup);
@@ -811,7 +821,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 1) void k_linear_deep(LinArgs a,
     };
     auto read = [&](int blk, int st, Ops& o) __attribute__((always_inline)) {
         const uint8_t* cur = ring + st * STAGE;
-        const int kb = min(blk * KS + ks, KB - 1);
+        const int kb = min(blk * KS + ks, KN - 1);
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
             const uint8_t* rowp = cur + ((wm * MI + i) * 16 + r16) * kGroup;
@@ -855,7 +865,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 1) void k_linear_deep(LinArgs a,
 #pragma unroll
             for (int j = 0; j < NJ; ++j) acc[i][j] = products_of<F>(C.w[j], C.x[i], acc[i][j], C.sw[j], C.sx[i], 0);
     };
-    const int n = (KB + KS - 1) / KS;   // blocks of a set; the last may lie past the end
+    const int n = (KN + KS - 1) / KS;   // blocks of a set; the last may lie past the end
     int i = 0;
     for (; i + 2 < n; i += 2) {
         step(i, A, B);
@@ -867,8 +877,8 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 1) void k_linear_deep(LinArgs a,
         step(i, A, B);
         products(A);
         ++i;
-        if (KS == 1 || i * KS + ks < KB) products(B);
-    } else if (KS == 1 || i * KS + ks < KB) {
+        if (KS == 1 || i * KS + ks < KN) products(B);
+    } else if (KS == 1 || i * KS + ks < KN) {
         products(A);
     }
     wait_all();
@@ -897,6 +907,10 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 1) void k_linear_deep(LinArgs a,
 template <Format F, bool GATED>
 static constexpr size_t deep_lds(int rows, int cols, int stages, int KB) {
     return (size_t)stages * (rows + cols) * kGroup + scales_lds<F, GATED>(rows, cols, stages * (rows + cols), KB);
+}
+template <Format F, bool GATED, int MI, int NJ, int WM, int WN, int S, int KS>
+__global__ __launch_bounds__(64 * WM * WN * KS, 1) void k_linear_deep(LinArgs a, int tiles_m, int tiles_n) {
+    linear_deep<F, GATED, MI, NJ, WM, WN, S, KS>(a, blockIdx.x, tiles_m, tiles_n);
 }
 template <Format F, bool GATED, int MI, int NJ, int WM, int WN, int S, int KS>
 static hipError_t run_deep_t(const LinArgs& a, hipStream_t st) {

@@ -53,10 +53,58 @@ BalancePlan balance_plan(int T, int E, int S) {
     return p;
 }
 
+// Tile and parts of the gated block's two products by the time that they are estimated to take.  A workgroup
+// takes `busy` us per K block of 64 where all `slots` of the chip have one, `alone` us at least, and `fixed` us per
+// tile; the launch takes the longer of the work shared by the slots and of the longest chain, and a quarter of the
+// other.  The table is fitted to 16 shapes from 16 x 4096 x 1536 to 16384 x 2048 x 1024 with every tile: 7 to
+// 9% off in the mean, and never more than 9% from the fastest of the five (4096 x 7168 x 2048: 408 us with the last
+// row's tiles, 518, 632, 761 and 867 with the others'; 300 x 768 x 1152: 21 us with the first's, 43 with the last's).
+// Parts: a long sum over few tiles is split over workgroups, whose float32 parts a third launch joins (3 us
+// and their bytes at 4 TB/s), where the estimate gains by it: 16384 x 768 x 256 has 256 blocks per tile of dw.
+ProductPlan product_plan(int T, int K, int I, bool dx, bool dw) {
+    static const struct {
+        int rows, cols, slots;
+        double busy, alone, fixed;
+    } tiles[5] = {{64, 64, 256, 0.147, 0.199, 2.0},    // two sets of waves over the K blocks
+                  {64, 128, 256, 0.286, 0.286, 2.0},   // four stages, one workgroup per CU
+                  {64, 128, 512, 0.434, 0.367, 3.6},   // three, two
+                  {128, 256, 256, 0.70, 0.61, 4.8},    // eight waves
+                  {128, 256, 512, 1.16, 0.73, 4.8}};   // weights straight to registers
+    const int rows[2] = {T, K}, cols[2] = {K, 2 * I}, blocks[2] = {I / 32, (int)cdiv(T, 64)};
+    const bool on[2] = {dx, dw};
+    ProductPlan best{0, {dx, dw}, blocks[0] > blocks[1]};
+    double least = 1e30;
+    for (int t = 0; t < 5; ++t)
+        for (int a = 1; a <= (dx ? 16 : 1); a *= 2)
+            for (int b = 1; b <= (dw ? 16 : 1); b *= 2) {
+                const int parts[2] = {a, b};
+                double work = 0, chain = 0, join = 0;
+                bool fits = true;
+                for (int i = 0; i < 2; ++i) {
+                    if (!on[i]) continue;
+                    const int64_t per = cdiv(blocks[i], parts[i]);
+                    if (parts[i] > 1 && (per < 4 || per * (parts[i] - 1) >= blocks[i])) fits = false;
+                    const double n = (double)(cdiv(rows[i], tiles[t].rows) * cdiv(cols[i], tiles[t].cols)) * parts[i];
+                    work += n * (per * tiles[t].busy + tiles[t].fixed) / tiles[t].slots;
+                    chain = std::max(chain, per * tiles[t].alone + tiles[t].fixed);
+                    if (parts[i] > 1) join += (double)rows[i] * cols[i] * parts[i] * 8 / 4e6 + (join == 0 ? 3 : 0);
+                }
+                const double us = std::max(work, chain) + 0.25 * std::min(work, chain) + join;
+                if (fits && us < least) {
+                    least = us;
+                    best.tile = t;
+                    best.parts[0] = dx ? a : 0;
+                    best.parts[1] = dw ? b : 0;
+                }
+            }
+    return best;
+}
+
 GatedBwdPlan gated_bwd_plan(int T, int K, int I, bool dx, bool dw, bool dbias) {
     GatedBwdPlan p;
     p.row_blocks = (int)cdiv(T, 64);
     p.parts = std::min(p.row_blocks, 256);
+    p.product = product_plan(T, K, I, dx, dw);
     const size_t N = 2 * (size_t)I, rows = 64 * (size_t)p.row_blocks;
     size_t o = 0;
     auto take = [&](bool on, size_t n) {
@@ -68,6 +116,8 @@ GatedBwdPlan gated_bwd_plan(int T, int K, int I, bool dx, bool dw, bool dbias) {
     p.weights = take(dx, K * N * 2);
     p.rows = take(dw, K * rows * 2);
     p.dgu_packed = take(dw, N * rows * 2);
+    p.join[0] = take(p.product.parts[0] > 1, (size_t)p.product.parts[0] * T * K * 4);
+    p.join[1] = take(p.product.parts[1] > 1, (size_t)p.product.parts[1] * K * N * 4);
     p.end = o;
     return p;
 }

@@ -21,10 +21,18 @@ struct BalancePlan {
 };
 BalancePlan balance_plan(int T, int E, int S);
 
-// ---- gated block backward: operands of its bf16 products, and partial rows of the bias's gradient
+// ---- gated block backward: its two bf16 products in one launch
+struct ProductPlan {
+    int tile;       // of product_plan's table
+    int parts[2];   // parts that the sums of dx and dw are split into; 0: not asked for
+    int first;      // the product that goes first: 0 dw, 1 dx
+};
+ProductPlan product_plan(int T, int K, int I, bool dx, bool dw);
+// operands of the products, their parts, and partial rows of the bias's gradient
 struct GatedBwdPlan {
     int row_blocks, parts;                             // blocks of 64 rows; partial rows [parts][2I] floats
-    size_t part, weights, rows, dgu_packed, end;       // byte offsets; a part that is not needed takes nothing
+    ProductPlan product;
+    size_t part, weights, rows, dgu_packed, join[2], end;   // byte offsets; what is not needed takes nothing
 };
 GatedBwdPlan gated_bwd_plan(int T, int K, int I, bool dx, bool dw, bool dbias);
 

@@ -121,22 +121,32 @@ def test_gated_linear_backward(T, K, I, scheme, act, bias):
     def product(got, a, b, rounding, what):
         ref, m = a @ b, np.abs(a) @ np.abs(b)
         t = (a.shape[1] + 8) * U * m
-        within(got, ref, t + rounding * (np.abs(ref) + t) + (TINY if rounding else 0), what)
-    product(host(out["dx"]), d, wv.T, UB, "dx")
-    product(host(out["dw"]), xv.T, d, 0, "dw")
+        within(host(got), ref, t + rounding * (np.abs(ref) + t) + (TINY if rounding else 0), what)
+    product(out["dx"], d, wv.T, UB, "dx")
+    product(out["dw"], xv.T, d, 0, "dw")
+    def bias_sums(got):
+        within(host(got), v.sum(0), tol.sum(0) + (T / 256 + 64) * U * mag.sum(0) + 1e-38, "dbias")
     if bias:
-        within(host(out["dbias"]), v.sum(0), tol.sum(0) + (T / 256 + 64) * U * mag.sum(0) + 1e-38, "dbias")
+        bias_sums(out["dbias"])
     else:
         assert out["dbias"] is None
-    # the same bits in parts, with bf16 weights' gradients, and over gu
-    half = M.moe_gated_linear_backward(dh, gu, w, xq, xs, act, want_dx=False, want_dbias=False, dw_dtype=torch.bfloat16)
-    assert half["dx"] is None and torch.equal(half["dw"], out["dw"].to(torch.bfloat16)) and torch.equal(half["dgu"], out["dgu"])
+    # the same bits again, and over gu
     over = gu.clone()
-    rest = M.MoeGatedLinearBackward(dh, over, w, activation=act, want_dbias=bias, dgu=over)()
-    assert rest["dw"] is None and torch.equal(over, out["dgu"]) and torch.equal(rest["dx"], out["dx"])
-    assert not bias or torch.equal(rest["dbias"], out["dbias"])
-    only = M.moe_gated_linear_backward(dh, gu, w, activation=act, want_dx=False, want_dbias=False)
-    assert torch.equal(only["dgu"], out["dgu"]) and only["dx"] is only["dw"] is only["dbias"] is None
+    again = M.MoeGatedLinearBackward(dh, over, w, xq, xs, act, want_dbias=bias, dgu=over)()
+    assert torch.equal(over, out["dgu"])
+    assert all(torch.equal(again[n], out[n]) for n in out if out[n] is not None)
+    # parts of it (the order of the sums is chosen for the outputs that are asked for), weights' gradients in bf16
+    half = M.moe_gated_linear_backward(dh, gu, w, xq, xs, act, want_dx=False, want_dbias=False, dw_dtype=torch.bfloat16)
+    assert half["dx"] is half["dbias"] is None and torch.equal(half["dgu"], out["dgu"])
+    product(half["dw"], xv.T, d, UB, "dw in bf16")
+    rest = M.moe_gated_linear_backward(dh, gu, w, activation=act, want_dbias=bias)
+    assert rest["dw"] is None and torch.equal(rest["dgu"], out["dgu"])
+    product(rest["dx"], d, wv.T, UB, "dx alone")
+    only = M.moe_gated_linear_backward(dh, gu, w, activation=act, want_dx=False, want_dbias=bias)
+    assert torch.equal(only["dgu"], out["dgu"]) and only["dx"] is only["dw"] is None
+    if bias:
+        assert torch.equal(rest["dbias"], out["dbias"])
+        bias_sums(only["dbias"])
 
 
 @pytest.mark.parametrize("T,K,I,scheme", [(5, 128, 32, "fp8"), (77, 384, 96, "mxfp8"), (300, 256, 416, "fp8"), (1100, 512, 96, "mxfp8")])
