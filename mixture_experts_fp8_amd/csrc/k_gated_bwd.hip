@@ -10,6 +10,26 @@ namespace moe {
 
 namespace {
 
+// 1 / (1 + exp(-v)) and its complement q = 1 - p, both within 2 u of their value down to 2^-126.  act_fn's argument
+// of the base-2 instruction is |v| u off and its reciprocal another u; a gradient that is rounded to bf16 and
+// then summed shows that in the values beside the middle of two, so both are mended here: by the rest of the
+// argument's product, and by one Newton step.
+struct Logistic {
+    float p, q;
+};
+__device__ __forceinline__ Logistic logistic(float v) {
+    const float c = fminf(fmaxf(v, -100.f), 100.f);       // exp(100) is infinite, exp(-100) counts as 0
+    const float t = c * -1.44269502f;
+    float lo = fmaf(c, -1.44269502f, -t);
+    lo = fmaf(c, -1.92596303e-8f, lo);                    // log2(e) = 1.44269502 + 1.92596303e-8
+    float e = __builtin_amdgcn_exp2f(t);
+    e = e < 3e38f ? fmaf(e * lo, 0.693147182f, e) : e;
+    const float d = 1.0f + e;
+    float p = __builtin_amdgcn_rcpf(d);
+    if (d < 1e38f) p = fmaf(fmaf(-d, p, 1.0f), p, p);
+    return {v != v ? v : p, v < 0.f ? 1.0f - p : e * p};
+}
+
 // act(v) and its slope; the same functions as act_fn, and without cancellation where one of the two
 // factors of a logistic is small.
 struct Act {
@@ -19,10 +39,9 @@ template <int ACT>
 __device__ __forceinline__ Act act_slope(float v) {
     if constexpr (ACT == MOE_ACT_RELU) return {v < 0.f ? 0.f : v, v > 0.f ? 1.f : 0.f};
     if constexpr (ACT == MOE_ACT_SILU) {
-        const float e = exp_fast(-v), p = __builtin_amdgcn_rcpf(1.0f + e);
-        const float q = v < 0.f ? 1.0f - p : e * p;      // 1 - p
-        const float a = v * p;
-        return {a, fmaf(a, q, p)};
+        const Logistic l = logistic(v);
+        const float a = v * l.p;
+        return {a, fmaf(a, l.q, l.p)};
     }
     if constexpr (ACT == MOE_ACT_GELU) {
         const float c = normal_cdf(v), d = __builtin_amdgcn_exp2f(v * v * -0.72134752f);   // exp(-v^2 / 2)
@@ -30,10 +49,10 @@ __device__ __forceinline__ Act act_slope(float v) {
     }
     if constexpr (ACT == MOE_ACT_GELU_TANH) {
         const float w = v * v, u = 1.59576912f * fmaf(0.044715f * w, v, v);   // twice tanh's argument
-        const float e = exp_fast(-u), p = __builtin_amdgcn_rcpf(1.0f + e);
-        const float q = (u < 0.f ? 1.0f - p : e * p) * p;      // p (1 - p)
+        const Logistic l = logistic(u);
+        const float q = l.q * l.p;
         // (from |v| of 1e12 on the last factors would leave float32; q is 0 long before)
-        return {v * p, q == 0.f ? p : fmaf(v * q, 1.59576912f * fmaf(0.134145f, w, 1.0f), p)};
+        return {v * l.p, q == 0.f ? l.p : fmaf(v * q, 1.59576912f * fmaf(0.134145f, w, 1.0f), l.p)};
     }
     return {v, 1.0f};
 }
