@@ -46,10 +46,14 @@ __device__ __forceinline__ v4u_t* v_operand(const LoraArgs& p, int64_t slot, int
 // scale x A^T of a slot's rows and 16 NR columns.  Each of the NW waves takes every NW-th block of 64 K and
 // brings its operands through LDS stages of its own, S of them in flight, by LDS-DMA: eight neighbouring lanes
 // read 128 bytes of one row then.  (Straight to registers the operands' layout puts neighbouring lanes in
-// different rows, 64 requests of 16 bytes per instruction: 16384 x 4096 took 45 us for 134 MB.)  A row's 16-byte
-// chunk c stands at place c ^ (row % 8).  The waves' sums meet in LDS, in wave order, and leave as operands: a sum of
-// `split` bf16 values, each the rounding of what the ones before leave.  Two leave 2^-17 of it, under the rounding
-// of a bf16 y, three nothing of float32.  Columns from R on are 0.
+// different rows, 64 requests of 16 bytes per instruction: 16384 x 4096 took 45 us for 134 MB, now 33.)  A row's
+// 16-byte chunk c stands at place c ^ (row % 8).  The waves' sums meet in LDS, in wave order, and leave as operands: a
+// sum of `split` bf16 values, each the rounding of what the ones before leave.  Two leave 2^-17 of it, under the
+// rounding of a bf16 y, three nothing of float32.  Columns from R on are 0.
+//   Bound by HBM for many rows of few sequences, by the L2s for many slots, which all read their adapter (2047 rows in 40
+// sequences x 4096, rank 64: 12 us for 107 MB), and by the chain of a wave's blocks in a decode step.  Waves and
+// stages leave room for two workgroups per CU (16000 x 512 in 2000 sequences, rank 16: 37 us with its other half, with
+// one workgroup of twice the waves 53; 1 x 7168 10.7 and 10.5).
 template <int MT, int NR, int NW, int S>
 __global__ __launch_bounds__(64 * NW) void k_lora_down(LoraArgs p) {
     constexpr int STAGE = (MT + NR) * 2048, OPS = 2 * (MT + NR);
@@ -181,7 +185,9 @@ __global__ __launch_bounds__(64 * NW) void k_lora_down(LoraArgs p) {
 // y of a slot's rows, 16 MI of them and 128 columns per wave.  v is the first operand and B the second, so that a
 // lane of the accumulators holds rows 4 (l / 16) .. +3 and one column of each of eight fragments; which column of B
 // stands where in a fragment is free, and is chosen such that those eight are consecutive (float32: four and four):
-// 16 neighbouring lanes then move 256 bytes of a row.  The residual, B and v are requested at once.
+// 16 neighbouring lanes then move 256 bytes of a row.  The residual, B and v are requested at once.  Bound by HBM for many
+// rows (16384 x 4096, rank 32: 58 us, 4.6 TB/s of residual and y), by the reading of B for many slots (2047 rows in 40
+// sequences, rank 64: 19 us, 11 of them for ranks 8 to 64).
 template <int MT, int MI, bool BF16>
 __global__ __launch_bounds__(256, 3) void k_lora_up(LoraArgs p) {
     constexpr int SPLIT = BF16 ? 2 : 3, WR = MT / MI, WC = 4 / WR;   // waves along rows and columns
@@ -312,16 +318,16 @@ hipError_t launch_lora(const LoraArgs& args, hipStream_t st) {
     a.split = p.split;
     a.out.nt = (int64_t)a.T * a.out.N * (bf16 ? 2 : 4) >= (32 << 20);
     hipError_t e;
-    if (p.window == 64) {
-        if (a.R <= 16) e = run_down<4, 1, 4, 3>(a, p.slots, st);
-        else if (a.R <= 32) e = run_down<4, 2, 4, 3>(a, p.slots, st);
-        else e = run_down<4, 4, 4, 2>(a, p.slots, st);
+    if (p.window == 32) {
+        if (a.R <= 16) e = run_down<2, 1, 4, 3>(a, p.slots, st);
+        else if (a.R <= 32) e = run_down<2, 2, 4, 2>(a, p.slots, st);
+        else e = run_down<2, 4, 3, 2>(a, p.slots, st);
         if (e != hipSuccess) return e;
-        return bf16 ? run_up<4, 2, true>(a, p.slots, st) : run_up<4, 1, false>(a, p.slots, st);
+        return bf16 ? run_up<2, 2, true>(a, p.slots, st) : run_up<2, 1, false>(a, p.slots, st);
     }
-    if (a.R <= 16) e = run_down<1, 1, 8, 4>(a, p.slots, st);
-    else if (a.R <= 32) e = run_down<1, 2, 8, 3>(a, p.slots, st);
-    else e = run_down<1, 4, 4, 3>(a, p.slots, st);
+    if (a.R <= 16) e = run_down<1, 1, 4, 4>(a, p.slots, st);
+    else if (a.R <= 32) e = run_down<1, 2, 4, 3>(a, p.slots, st);
+    else e = run_down<1, 4, 4, 2>(a, p.slots, st);
     if (e != hipSuccess) return e;
     return bf16 ? run_up<1, 1, true>(a, p.slots, st) : run_up<1, 1, false>(a, p.slots, st);
 }

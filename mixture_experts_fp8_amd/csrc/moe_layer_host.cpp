@@ -122,13 +122,13 @@ GatedBwdPlan gated_bwd_plan(int T, int K, int I, bool dx, bool dw, bool dbias) {
     return p;
 }
 
-// Windows of 64 rows read an adapter's matrices a quarter as often, but leave CUs without a slot up to a few thousand
-// rows, and mostly empty where sequences are short (1000 rows in 3 sequences x 7168 x 2048, rank 64: 24.9 us with
-// windows of 16, 33.5 with 64; 3000 in 64 x 1000 x 4000, rank 24: 23.3 and 26.0; 4000 in 5 x 4096 x 4096, rank 128:
-// 55 and 51; 16384 in 9, rank 64: 151 and 126).
+// Windows of 32 rows read an adapter's matrices half as often as those of 16, but leave CUs without a slot up to about two
+// thousand rows, and half empty where sequences are short (1000 rows in 3 sequences x 7168 x 2048, rank 64: 22.9
+// us with windows of 16, 26.5 with 32; 1000 in 100 x 4096 x 4096, rank 16: 18.0 and 20.3; 2047 in 40, rank 64: 32.8 and
+// 30.5; 16384 in 9, rank 32: 112 and 99; 64 rows: 104, up to 6% less than 32 at many sequences, 18% more at 5000 rows).
 LoraPlan lora_plan(int T, int R, int S, bool bf16) {
     LoraPlan p;
-    p.window = S && T >= 4000 && T / S >= 32 ? 64 : 16;
+    p.window = S && T >= 2000 && T / S >= 24 ? 32 : 16;
     p.slots = S ? cdiv(T, p.window) + S : T;
     p.steps = (int)cdiv(R, 32);
     p.split = bf16 ? 2 : 3;

@@ -64,7 +64,7 @@ static void slots() {
             for (int j = i; j && off[j] < off[j - 1]; --j) std::swap(off[j], off[j - 1]);
         for (bool bf16 : {false, true}) {
             const LoraPlan p = lora_plan(T, R, S, bf16);
-            CHECK((p.window == 16 || p.window == 64) && p.steps * 32 >= R && p.split == (bf16 ? 2 : 3));
+            CHECK((p.window == 16 || p.window == 32) && p.steps * 32 >= R && p.split == (bf16 ? 2 : 3));
             CHECK(p.end == (size_t)p.slots * (p.window / 16) * p.steps * p.split * 1024);
             std::set<int> seen;
             for (int s = 0; s < S; ++s)

@@ -33,6 +33,9 @@ CASES = [  # T, K, N, R, adapters, sequences (None: one row each, a list: offset
     (2047, 1024, 512, 64, 12, 40, "bf16"), (5000, 64, 32, 16, 9, 4500, "bf16"), (3000, 128, 64, 48, 3, 3, "bf16"),
     (64, 4096, 256, 8, 2, [-5, 30, 90], "bf16"),     # offsets outside the rows
     (200, 448, 16, 200, 2, [150, 160, 190], "f32"), (4200, 320, 4112, 32, 4, 3, "bf16"),
+    # windows of 32 rows at each rank's tiles and both types
+    (2100, 136, 272, 24, 3, 5, "f32"), (2500, 520, 144, 64, 4, 60, "f32"), (2600, 320, 528, 16, 3, 20, "bf16"),
+    (2050, 256, 64, 200, 2, [1000, 1990, 2049], "bf16"), (2200, 1096, 1040, 8, 5, 40, "f32"),
 ]
 
 
