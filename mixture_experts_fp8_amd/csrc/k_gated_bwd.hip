@@ -70,13 +70,38 @@ __device__ __forceinline__ void decode4(uint32_t q, float (&f)[4]) {
 __device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
 __device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
 
-// 8 x 8 transpose of bf16 values: rows r[i] (8 columns each) -> the 8 rows' values of column c.
-__device__ __forceinline__ v4u_t column_of(const uint4 (&r)[8], int c) {
-    auto word = [&](int i) __attribute__((always_inline)) { return c < 2 ? r[i].x : c < 4 ? r[i].y : c < 6 ? r[i].z : r[i].w; };
+// The 8 rows' bf16 values of column c.
+template <int W>
+__device__ __forceinline__ v4u_t column_of(const uint32_t (&r)[8][W], int c) {
     v4u_t v;
 #pragma unroll
-    for (int p = 0; p < 4; ++p) v[p] = c % 2 ? high_halves(word(2 * p), word(2 * p + 1)) : low_halves(word(2 * p), word(2 * p + 1));
+    for (int p = 0; p < 4; ++p)
+        v[p] = c % 2 ? high_halves(r[2 * p][c / 2], r[2 * p + 1][c / 2]) : low_halves(r[2 * p][c / 2], r[2 * p + 1][c / 2]);
     return v;
+}
+// 2 W bf16 values (W 2 or 4) from and to memory, and as floats.
+template <int W>
+__device__ __forceinline__ void load_words(const uint16_t* p, uint32_t (&r)[W]) {
+    typedef uint32_t vec __attribute__((ext_vector_type(W)));
+    const vec v = *reinterpret_cast<const vec*>(p);
+#pragma unroll
+    for (int i = 0; i < W; ++i) r[i] = v[i];
+}
+template <int W>
+__device__ __forceinline__ void store_words(uint16_t* p, const uint32_t (&r)[W]) {
+    typedef uint32_t vec __attribute__((ext_vector_type(W)));
+    vec v;
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = r[i];
+    *reinterpret_cast<vec*>(p) = v;
+}
+template <int W>
+__device__ __forceinline__ void unpack_words(const uint32_t (&r)[W], float (&f)[2 * W]) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        f[2 * i] = __uint_as_float(r[i] << 16);
+        f[2 * i + 1] = __uint_as_float(r[i] & 0xFFFF0000u);
+    }
 }
 
 struct DguArgs {
@@ -88,40 +113,42 @@ struct DguArgs {
     float* part;            // or NULL: [parts][2I] column sums
 };
 
-// A wave takes 64 columns of g and u and blocks of 64 rows, a grid apart; lane (t = l / 8, c = l % 8) the rows
-// 8 t .. +7 and columns 8 c .. +7 of a block, all loads of which are in flight together.  Column sums stay in
+// A wave takes 8 CW columns of g and u and blocks of 64 rows, `parts` apart; lane (t = l / 8, c = l % 8) the rows
+// 8 t .. +7 and CW columns from CW c of a block, all loads of which are in flight together.  Column sums stay in
 // registers.  The fragments of the transposed result go through LDS, so that they leave in whole kilobytes;
-// slots are swizzled by t, which spreads the lanes' 16-byte writes over the banks.
-template <int ACT, bool PACK>
+// slots are swizzled by t, which spreads the lanes' 16-byte writes over the banks.  CW 8, or 4 where that leaves SIMDs
+// without a wave: a lane's 64 activations are one chain (the whole call at 512 x 2048 x 1024: 29.0 us, 32.5 with 8;
+// 4096 x 7168 x 2048: 419 with 4, 411 with 8).
+template <int ACT, bool PACK, int CW>
 __device__ __forceinline__ void gated_dgu(const DguArgs& a, int unit, uint8_t* smem) {
+    constexpr int W = CW / 2, WAVE = 8 * CW, FR = WAVE / 16;   // words of a lane's row; columns, fragments of a wave
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int cols = (unit / a.parts * 4 + wv) * 64, first = unit % a.parts;
-    const int t8 = lane >> 3, c8 = lane & 7, col = cols + 8 * c8;
+    const int cols = (unit / a.parts * 4 + wv) * WAVE, first = unit % a.parts;
+    const int t8 = lane >> 3, c8 = lane & 7, col = cols + CW * c8;
     const bool on = col < a.I;
     if (cols >= a.I) return;   // (uniform; no barrier follows)
     const int64_t N = 2 * (int64_t)a.I;
-    float sg[8] = {}, su[8] = {};
+    float sg[CW] = {}, su[CW] = {};
     for (int b = first; b < a.NT; b += a.parts) {
-        uint4 g[8], u[8], d[8];
+        uint32_t g[8][W] = {}, u[8][W] = {}, d[8][W] = {};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int64_t t = (int64_t)b * 64 + 8 * t8 + i;
-            g[i] = u[i] = d[i] = make_uint4(0, 0, 0, 0);
             if (on && t < a.T) {
-                g[i] = *reinterpret_cast<const uint4*>(a.gu + t * N + col);
-                u[i] = *reinterpret_cast<const uint4*>(a.gu + t * N + a.I + col);
-                d[i] = *reinterpret_cast<const uint4*>(a.dh + t * a.I + col);
+                load_words<W>(a.gu + t * N + col, g[i]);
+                load_words<W>(a.gu + t * N + a.I + col, u[i]);
+                load_words<W>(a.dh + t * a.I + col, d[i]);
             }
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int64_t t = (int64_t)b * 64 + 8 * t8 + i;
-            float x[8], y[8], z[8];
-            unpack8(g[i], x);
-            unpack8(u[i], y);
-            unpack8(d[i], z);
+            float x[CW], y[CW], z[CW];
+            unpack_words<W>(g[i], x);
+            unpack_words<W>(u[i], y);
+            unpack_words<W>(d[i], z);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < CW; ++j) {
                 const Act f = act_slope<ACT>(x[j]);
                 x[j] = z[j] * y[j] * f.s;
                 y[j] = z[j] * f.a;
@@ -129,25 +156,30 @@ __device__ __forceinline__ void gated_dgu(const DguArgs& a, int unit, uint8_t* s
                 sg[j] += x[j];
                 su[j] += y[j];
             }
-            g[i] = pack8(x);
-            u[i] = pack8(y);
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                g[i][j] = pack_bf16(x[2 * j], x[2 * j + 1]);
+                u[i][j] = pack_bf16(y[2 * j], y[2 * j + 1]);
+            }
             if (on && t < a.T) {
-                *reinterpret_cast<uint4*>(a.dgu + t * N + col) = g[i];
-                *reinterpret_cast<uint4*>(a.dgu + t * N + a.I + col) = u[i];
+                store_words<W>(a.dgu + t * N + col, g[i]);
+                store_words<W>(a.dgu + t * N + a.I + col, u[i]);
             }
         }
         if constexpr (PACK) {
-            v4u_t* s = reinterpret_cast<v4u_t*>(smem + wv * 8192);
+            v4u_t* s = reinterpret_cast<v4u_t*>(smem + wv * FR * kFragBytes);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    s[(c8 >> 1) * 128 + t8 * 16 + ((8 * (c8 & 1) + c) ^ t8)] = column_of(half ? u : g, c);
+                for (int c = 0; c < CW; ++c) {
+                    const int q = CW * c8 + c;   // column of the wave
+                    s[(q >> 4) * 128 + t8 * 16 + ((q & 15) ^ t8)] = column_of<W>(half ? u : g, c);
+                }
                 asm volatile("" ::: "memory");   // (a wave's LDS accesses stay in order)
                 __builtin_amdgcn_wave_barrier();
                 const int n0 = ((half ? a.I : 0) + cols) / 16;
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {    // fragment q / 2, its lower and upper kilobyte
+                for (int q = 0; q < 2 * FR; ++q) {    // fragment q / 2, its lower and upper kilobyte
                     const int p = (q & 1) * 64 + lane, r = p >> 4;
                     const v4u_t v = s[(q >> 1) * 128 + r * 16 + ((p & 15) ^ r)];
                     if (cols + 16 * (q >> 1) < a.I)
@@ -160,7 +192,7 @@ __device__ __forceinline__ void gated_dgu(const DguArgs& a, int unit, uint8_t* s
     }
     if (a.part) {   // over the lanes of a column, then one row of the parts
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < CW; ++j) {
 #pragma unroll
             for (int m = 8; m < 64; m *= 2) {
                 sg[j] += __shfl_xor(sg[j], m);
@@ -170,7 +202,7 @@ __device__ __forceinline__ void gated_dgu(const DguArgs& a, int unit, uint8_t* s
         if (t8 == 0 && on) {
             float* p = a.part + (int64_t)first * N + col;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) p[j] = sg[j], p[a.I + j] = su[j];
+            for (int j = 0; j < CW; ++j) p[j] = sg[j], p[a.I + j] = su[j];
         }
     }
 }
@@ -191,7 +223,7 @@ __device__ __forceinline__ void rows_transposed(const uint8_t* xq, const uint8_t
         q[i] = *reinterpret_cast<const uint2*>(xq + t * K + k0);
         s[i] = xs[t * (K / gs) + k0 / gs];
     }
-    uint4 r[8];
+    uint32_t r[8][4];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const float m = ue8m0(s[i]);
@@ -202,11 +234,12 @@ __device__ __forceinline__ void rows_transposed(const uint8_t* xq, const uint8_t
         decode4(q[i].y, f);
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[4 + j] = f[j] * m;
-        r[i] = t0 + i < T ? pack8(v) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r[i][j] = t0 + i < T ? pack_bf16(v[2 * j], v[2 * j + 1]) : 0;
     }
 #pragma unroll
     for (int c = 0; c < 8; ++c)
-        *reinterpret_cast<v4u_t*>(xt + (int64_t)(k0 + c) * (NT * 64) + t0) = column_of(r, c);
+        *reinterpret_cast<v4u_t*>(xt + (int64_t)(k0 + c) * (NT * 64) + t0) = column_of<4>(r, c);
 }
 
 // The packed FP8 weights [K][N] as bf16 fragments of 16 rows of w whose K is the column: a workgroup turns 4
@@ -254,25 +287,32 @@ struct PrepareArgs {
     uint16_t* xt;
     uint8_t* wt;
 };
-template <int ACT, bool MX, bool PACK>
+template <int ACT, bool MX, bool PACK, int CW>
 __global__ __launch_bounds__(256) void k_gated_prepare(PrepareArgs a) {
-    __shared__ __align__(16) uint8_t smem[PACK ? 32768 : 4 * kFragBytes + 256];
+    __shared__ __align__(16) uint8_t smem[PACK ? 2 * CW * kFragBytes : 4 * kFragBytes + 256];   // (CW 4: 16 KB, enough for both)
     int unit = blockIdx.x;
-    if (unit < a.dgu_units) return gated_dgu<ACT, PACK>(a.d, unit, smem);
+    if (unit < a.dgu_units) return gated_dgu<ACT, PACK, CW>(a.d, unit, smem);
     unit -= a.dgu_units;
     if (unit < a.row_units) return rows_transposed<MX>(a.xq, a.xs, a.d.T, a.K, a.d.NT, a.xt, unit);
     weights_transposed<MX>(a.w, a.ws, a.K, 2 * a.d.I, a.wt, unit - a.row_units, smem);
 }
 
-template <int ACT>
-void run_prepare(const PrepareArgs& a, bool mx, unsigned grid, hipStream_t st) {
+template <int ACT, int CW>
+void run_prepare_cw(PrepareArgs& a, bool mx, unsigned rest, hipStream_t st) {
+    a.dgu_units = a.d.parts * (int)ceil_div(a.d.I, 32 * CW);
+    const dim3 grid(a.dgu_units + rest);
     if (a.xt) {
-        if (mx) hipLaunchKernelGGL((k_gated_prepare<ACT, true, true>), dim3(grid), dim3(256), 0, st, a);
-        else hipLaunchKernelGGL((k_gated_prepare<ACT, false, true>), dim3(grid), dim3(256), 0, st, a);
+        if (mx) hipLaunchKernelGGL((k_gated_prepare<ACT, true, true, CW>), grid, dim3(256), 0, st, a);
+        else hipLaunchKernelGGL((k_gated_prepare<ACT, false, true, CW>), grid, dim3(256), 0, st, a);
     } else {
-        if (mx) hipLaunchKernelGGL((k_gated_prepare<ACT, true, false>), dim3(grid), dim3(256), 0, st, a);
-        else hipLaunchKernelGGL((k_gated_prepare<ACT, false, false>), dim3(grid), dim3(256), 0, st, a);
+        if (mx) hipLaunchKernelGGL((k_gated_prepare<ACT, true, false, CW>), grid, dim3(256), 0, st, a);
+        else hipLaunchKernelGGL((k_gated_prepare<ACT, false, false, CW>), grid, dim3(256), 0, st, a);
     }
+}
+template <int ACT>
+void run_prepare(PrepareArgs& a, bool mx, unsigned rest, hipStream_t st) {
+    if (a.d.parts * ceil_div(a.d.I, 64) < 1024) run_prepare_cw<ACT, 4>(a, mx, rest, st);
+    else run_prepare_cw<ACT, 8>(a, mx, rest, st);
 }
 
 // Both products in one launch: workgroups [0, first_units) compute the tiles of p[0], the next ones those of p[1], the
@@ -399,15 +439,14 @@ hipError_t launch_gated_backward(const GatedBwdArgs& a, hipStream_t st) {
     PrepareArgs r{{a.T, a.I, NT, a.dbias ? p.parts : NT, a.dh, a.gu, a.dgu, a.dw ? ws + p.dgu_packed : nullptr, part},
                   a.K, 0, 0, a.xq, a.xs, a.w, a.wsc, a.dw ? reinterpret_cast<uint16_t*>(ws + p.rows) : nullptr,
                   a.dx ? ws + p.weights : nullptr};
-    r.dgu_units = r.d.parts * (int)ceil_div(a.I, 256);
     r.row_units = a.dw ? NT * (int)ceil_div(a.K, 256) : 0;
-    const unsigned grid = r.dgu_units + r.row_units + (a.dx ? N / 64 * (a.K / kGroup) : 0);
+    const unsigned rest = r.row_units + (a.dx ? N / 64 * (a.K / kGroup) : 0);
     switch (a.act) {
-        case MOE_ACT_RELU: run_prepare<MOE_ACT_RELU>(r, a.mx, grid, st); break;
-        case MOE_ACT_SILU: run_prepare<MOE_ACT_SILU>(r, a.mx, grid, st); break;
-        case MOE_ACT_GELU: run_prepare<MOE_ACT_GELU>(r, a.mx, grid, st); break;
-        case MOE_ACT_GELU_TANH: run_prepare<MOE_ACT_GELU_TANH>(r, a.mx, grid, st); break;
-        default: run_prepare<MOE_ACT_NONE>(r, a.mx, grid, st);
+        case MOE_ACT_RELU: run_prepare<MOE_ACT_RELU>(r, a.mx, rest, st); break;
+        case MOE_ACT_SILU: run_prepare<MOE_ACT_SILU>(r, a.mx, rest, st); break;
+        case MOE_ACT_GELU: run_prepare<MOE_ACT_GELU>(r, a.mx, rest, st); break;
+        case MOE_ACT_GELU_TANH: run_prepare<MOE_ACT_GELU_TANH>(r, a.mx, rest, st); break;
+        default: run_prepare<MOE_ACT_NONE>(r, a.mx, rest, st);
     }
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     if (!a.dx && !a.dw) return a.dbias ? launch_column_sums(part, p.parts, N, a.dbias, st) : hipSuccess;
