@@ -128,8 +128,8 @@ def lib() -> ctypes.CDLL:
         L.moe_prepack_weights_mx.restype = ctypes.c_int
         L.moe_prepack_weights_mx.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp, vp]
         for name in ("moe_add_rmsnorm", "moe_add_rmsnorm_backward", "moe_linear", "moe_balance_loss",
-                     "moe_route_backward", "moe_combine_backward", "moe_add_layernorm",
-                     "moe_add_layernorm_backward", "moe_gated_linear", "moe_gated_linear_backward", "moe_lora"):   # one argument struct each (layer.py)
+                     "moe_route_backward", "moe_combine_backward", "moe_add_layernorm", "moe_add_layernorm_backward",
+                     "moe_gated_linear", "moe_gated_linear_backward", "moe_lora"):   # one argument struct each (layer.py)
             getattr(L, name).restype = ctypes.c_int
             getattr(L, name).argtypes = [vp]
         for name, n in (("moe_add_rmsnorm_backward_workspace_size", 2),

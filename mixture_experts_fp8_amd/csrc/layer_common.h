@@ -1,5 +1,5 @@
-// Device helpers and launchers of the operators around the expert step (k_norm.hip,
-// k_linear.hip, k_router_grad.hip).
+// Device helpers and launchers of the operators around the expert step (k_norm.hip, k_linear.hip,
+// k_gated.hip, k_gated_bwd.hip, k_lora.hip, k_router_grad.hip).
 #pragma once
 #include "moe_common.h"
 #include "moe_layer_plan.h"

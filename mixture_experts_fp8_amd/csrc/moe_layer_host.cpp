@@ -74,29 +74,37 @@ ProductPlan product_plan(int T, int K, int I, bool dx, bool dw) {
     const bool on[2] = {dx, dw};
     ProductPlan best{0, {dx, dw}, blocks[0] > blocks[1]};
     double least = 1e30;
-    for (int t = 0; t < 5; ++t)
-        for (int a = 1; a <= (dx ? 16 : 1); a *= 2)
-            for (int b = 1; b <= (dw ? 16 : 1); b *= 2) {
-                const int parts[2] = {a, b};
-                double work = 0, chain = 0, join = 0;
-                bool fits = true;
-                for (int i = 0; i < 2; ++i) {
-                    if (!on[i]) continue;
-                    const int64_t per = cdiv(blocks[i], parts[i]);
-                    if (parts[i] > 1 && (per < 4 || per * (parts[i] - 1) >= blocks[i])) fits = false;
-                    const double n = (double)(cdiv(rows[i], tiles[t].rows) * cdiv(cols[i], tiles[t].cols)) * parts[i];
-                    work += n * (per * tiles[t].busy + tiles[t].fixed) / tiles[t].slots;
-                    chain = std::max(chain, per * tiles[t].alone + tiles[t].fixed);
-                    if (parts[i] > 1) join += (double)rows[i] * cols[i] * parts[i] * 8 / 4e6 + (join == 0 ? 3 : 0);
-                }
-                const double us = std::max(work, chain) + 0.25 * std::min(work, chain) + join;
-                if (fits && us < least) {
+    for (int t = 0; t < 5; ++t) {
+        struct {
+            double work, chain, join;
+        } of[2][5] = {};   // of a product in 2^p parts
+        int most[2] = {0, 0};
+        for (int i = 0; i < 2; ++i) {
+            if (!on[i]) continue;
+            const double n = (double)(cdiv(rows[i], tiles[t].rows) * cdiv(cols[i], tiles[t].cols));
+            for (int p = 0; p < 5; ++p) {
+                const int parts = 1 << p;
+                const int64_t per = cdiv(blocks[i], parts);
+                if (p && per < 4) break;
+                most[i] = p;
+                of[i][p] = {n * parts * (per * tiles[t].busy + tiles[t].fixed) / tiles[t].slots,
+                            p && per * (parts - 1) >= blocks[i] ? 1e30 : per * tiles[t].alone + tiles[t].fixed,   // (an empty part)
+                            p ? (double)rows[i] * cols[i] * parts * 8 / 4e6 : 0};
+            }
+        }
+        for (int a = 0; a <= most[0]; ++a)
+            for (int b = 0; b <= most[1]; ++b) {
+                const auto &x = of[0][a], &w = of[1][b];
+                const double work = x.work + w.work, chain = std::max(x.chain, w.chain);
+                const double us = std::max(work, chain) + 0.25 * std::min(work, chain) + x.join + w.join + (a || b ? 3 : 0);
+                if (us < least) {
                     least = us;
                     best.tile = t;
-                    best.parts[0] = dx ? a : 0;
-                    best.parts[1] = dw ? b : 0;
+                    best.parts[0] = dx ? 1 << a : 0;
+                    best.parts[1] = dw ? 1 << b : 0;
                 }
             }
+    }
     return best;
 }
 

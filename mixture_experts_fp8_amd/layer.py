@@ -532,7 +532,8 @@ class MoeLora(_Call):
             _need(seq_offsets, "seq_offsets", torch.int32, (S + 1,))
         ldr = _rows(residual, "residual", out_dtype, (T, N)) if residual is not None else N
         if y is None:
-            y = torch.zeros(T, N, dtype=out_dtype, device=x.device)
+            make = torch.empty if seq_offsets is None else torch.zeros   # (a sequence per row: every row is written)
+            y = make(T, N, dtype=out_dtype, device=x.device)
         ldy = _rows(y, "y", out_dtype, (T, N))
         dt = B.MOE_DTYPE_F32 if out_dtype == torch.float32 else B.MOE_DTYPE_BF16
         ws = workspace(lib().moe_lora_workspace_size(T, R, S, int(seq_offsets is not None), dt), x.device)
