@@ -89,7 +89,7 @@ BWD = [  # T, K, I, scheme, act, bias: each variant of both products, ragged row
     (300, 1152, 64, "fp8", "gelu", False), (700, 2048, 288, "mxfp8", "silu", True), (1000, 640, 1056, "fp8", "gelu_tanh", True),
     (1900, 2176, 96, "fp8", "silu", False), (2047, 768, 1152, "fp8", "gelu", True), (130, 4096, 1184, "mxfp8", "relu", True),
     (2500, 4224, 128, "fp8", "none", False), (300, 2560, 2336, "fp8", "silu", True), (4100, 4096, 64, "mxfp8", "silu", True),
-    (17000, 128, 32, "fp8", "gelu", True),
+    (17000, 128, 32, "fp8", "gelu", True), (5, 32768, 32, "mxfp8", "silu", True), (70, 128, 16352, "fp8", "gelu_tanh", True),
 ]
 
 

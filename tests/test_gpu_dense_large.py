@@ -1,5 +1,6 @@
 """Operators of dense layers on buffers whose offsets pass 2^31 elements or bytes, against the same rows alone and
 against sums in 64 bits."""
+import numpy as np
 import pytest
 import torch
 
@@ -33,6 +34,27 @@ def test_lora_rows_far_apart():
     M.moe_lora(xw[:, 1024:1024 + K], w, ids, off, yw[:, :N], y=yw[:, :N])
     assert torch.equal(yw[:, :N], want)
     del xw, yw
+    _free()
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_lora_of_very_many_sequences(dt):
+    """2^20 sequences, nearly all of them empty: slots of several launches, two rounds of the search more."""
+    T, S, K, N, R, n = 300, 1 << 20, 72, 4624, 24, 5
+    g = rng(82)
+    x, _ = bf16(g.standard_normal((T, K)))
+    r = bf16(g.standard_normal((T, N)))[0].to(dt)
+    w = M.LoraWeights(bf16(g.standard_normal((n, R, K)) * 0.1)[0], bf16(g.standard_normal((n, N, R)) * 0.1)[0])
+    at = np.sort(np.concatenate([[0, 1, 63, 64, S - 1], g.choice(np.arange(65, S - 1), 20, replace=False)]))   # the others: empty
+    ends = np.concatenate([np.sort(g.choice(np.arange(4, T - 8), 24, replace=False)), [T - 5]])
+    off = np.full(S + 1, 3, np.int32)
+    for s, e in zip(at, ends):
+        off[s + 1:] = e
+    ids = g.integers(0, n, S).astype(np.int32)
+    i32 = lambda v: torch.tensor(np.asarray(v, np.int32), device=DEV)   # noqa: E731
+    want = M.moe_lora(x, w, i32(ids[at]), i32(np.concatenate([[3], ends])), r, dt, y=torch.full_like(r, 7))
+    got = M.moe_lora(x, w, i32(ids), i32(off), r, dt, y=torch.full_like(r, 7))
+    assert torch.equal(got, want) and (got[:3] == 7).all() and (got[T - 5:] == 7).all() and (got[3:T - 5] != 7).any(1).all()
     _free()
 
 

@@ -36,6 +36,8 @@ CASES = [  # T, K, N, R, adapters, sequences (None: one row each, a list: offset
     # windows of 32 rows at each rank's tiles and both types
     (2100, 136, 272, 24, 3, 5, "f32"), (2500, 520, 144, 64, 4, 60, "f32"), (2600, 320, 528, 16, 3, 20, "bf16"),
     (2050, 256, 64, 200, 2, [1000, 1990, 2049], "bf16"), (2200, 1096, 1040, 8, 5, 40, "f32"),
+    # the largest depth, rank and width
+    (3, 65536, 48, 256, 2, None, "f32"), (20, 65536, 16, 8, 2, [0, 3, 20], "bf16"), (2, 8, 1 << 20, 8, 2, None, "bf16"),
 ]
 
 
