@@ -346,9 +346,9 @@ hipError_t launch_add_layernorm(const NormArgs& a, hipStream_t st) { return laun
 // 1024 threads 69, with spills).
 //
 // LN: xhat = (h - m) r and dx = r (g - mean(g) - xhat mean(g xhat)) + dh; the bias's gradient sum_t dy takes
-// its place beside the weight's, in registers and in a second set of parts.  With d = h - h[0] (as in the
-// forward pass, here rounded to float32, which leaves 2^-24 of d) the four sums of d, d^2, g and g d need one
-// exchange: sum g (h - m) = sum g d - mean(d) sum g.
+// its place beside the weight's, in registers and in a second set of parts.  With d = h - h[0], in double as in the
+// forward pass (float32 would keep 2^-24 of h[0], not of d, and has no difference of two values of 3e38), the four
+// sums of d, d^2, g and g d need one exchange: sum g (h - m) = sum g d - mean(d) sum g.
 template <int G, int VPT, bool ST, bool LN>
 __device__ __forceinline__ void add_norm_bwd(const NormBwdArgs& a) {
     constexpr int RPB = G == 64 ? 4 : 1;
@@ -415,8 +415,8 @@ __device__ __forceinline__ void add_norm_bwd(const NormBwdArgs& a) {
         if (AHEAD && t + step < a.T) load(t + step, nx);   // in flight over this row's sums
         // sum h^2 and sum g h in one exchange: mean(g xhat) = r sum(g h) / H
         double ss = 0.0, gh = 0.0, sd = 0.0, sg = 0.0;
-        float h0 = 0.f;
-        if constexpr (LN) h0 = bf16_to_f32(a.h[t * a.H]);
+        double h0 = 0.0;
+        if constexpr (LN) h0 = (double)bf16_to_f32(a.h[t * a.H]);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             float h[8], d[8], wt[8];
@@ -427,7 +427,7 @@ __device__ __forceinline__ void add_norm_bwd(const NormBwdArgs& a) {
             for (int j = 0; j < 8; ++j) {
                 if constexpr (LN) {
                     // (no weight, and no gradient, behind the row's end: only d has to be left out there)
-                    const double x = (double)(sub + i * G < nv ? h[j] - h0 : 0.f);
+                    const double x = sub + i * G < nv ? (double)h[j] - h0 : 0.0;
                     const double g = (double)(d[j] * (AHEAD ? wk[AHEAD ? i : 0][j] : wt[j]));
                     sd += x;
                     sg += g;
@@ -467,10 +467,11 @@ __device__ __forceinline__ void add_norm_bwd(const NormBwdArgs& a) {
                 }
             }
         }
-        double rd, md = 0.0;   // LN: mean(d)
-        float mg = 0.f;        // LN: mean(g)
+        double rd, mean = 0.0;   // LN: mean(h)
+        float mg = 0.f;          // LN: mean(g)
         if constexpr (LN) {
-            md = sd * a.inv_h;
+            const double md = sd * a.inv_h;   // mean(d)
+            mean = h0 + md;
             rd = rsqrt_f64(fma(-md, md, ss * a.inv_h) + (double)a.eps);
             mg = (float)(sg * a.inv_h);
             gh -= md * sg;
@@ -492,7 +493,7 @@ __device__ __forceinline__ void add_norm_bwd(const NormBwdArgs& a) {
             if constexpr (!AHEAD) weights(i, wt);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float x = LN ? (float)(((double)(h[j] - h0) - md) * rd) : (float)((double)h[j] * rd);
+                const float x = LN ? (float)(((double)h[j] - mean) * rd) : (float)((double)h[j] * rd);
                 dw[i][j] = fmaf(d[j], x, dw[i][j]);
                 if constexpr (LN && !DB_LDS) db[i][j] += d[j];
                 const float gw = d[j] * (AHEAD ? wk[AHEAD ? i : 0][j] : wt[j]);

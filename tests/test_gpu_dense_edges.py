@@ -1,0 +1,54 @@
+"""Edges of the operators of a model's dense layers on the GPU: rows whose first column is far from the others and rows
+across the whole range in the layer norm's backward pass.
+
+Tolerances as in test_gpu_layer.py: u = 2^-24 is half a float32 step, 2^-8 half a bf16 step."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import dense as OD
+from test_gpu_layer import DEV, M, TINY, U, UB, bf16, f32, host, rng, within
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- layer norm, backward -----------------------------------------------------------------
+def _norm_gradients(h, hf, key):
+    """The backward pass of h against the oracle, with the bounds of test_add_layernorm_backward: dx's terms pass at
+    most 10 roundings, xhat is formed in double and rounded once, and a column's sums have one chain."""
+    T, H = hf.shape
+    dy, dyf = bf16(rng(51, T, H, key).standard_normal((T, H)))
+    w, wf = f32(1 + 0.1 * rng(52, H, key).standard_normal(H))
+    out = M.moe_add_layernorm_backward(dy, h, w, 1e-5)
+    dx, dw, db, mag, dwmag, dbmag = OD.layernorm_backward(dyf, hf, wf, 1e-5)
+    parts = M.binding.lib().moe_add_layernorm_backward_workspace_size(T, H) // (8 * H)
+    chain = -(-T // parts) + 4 + -(-parts // 32) + 32
+    within(host(out["dx"]), dx, UB * np.abs(dx) + 10 * U * (1 + UB) * mag + TINY, "dx")
+    within(host(out["dweight"]), dw, (chain + 4) * U * dwmag + 1e-38, "dweight")
+    within(host(out["dbias"]), db, (chain + 4) * U * dbmag + 1e-38, "dbias")
+
+
+@pytest.mark.parametrize("first", [1e3, -1e4])
+@pytest.mark.parametrize("H", [64, 1000, 2048, 4096, 8200, 20000])
+def test_layernorm_backward_of_a_large_first_column(H, first):
+    """A channel of 1000 to 10000 times the others' size: their deviations keep their digits."""
+    T = 64
+    h, hf = bf16(rng(50, H).standard_normal((T, H)) + np.where(np.arange(H) == 0, first, 0.0))
+    _norm_gradients(h, hf, 1)
+
+
+@pytest.mark.parametrize("H", [64, 1000, 2048, 4096, 8200, 20000])
+def test_layernorm_backward_across_the_range(H):
+    """Both signs near bf16's largest value, 3.39e38: differences of two values leave float32."""
+    g = rng(53, H)
+    v = g.uniform(-3.3e38, 3.3e38, (5, H))
+    v[0] = 3e38 * (-1.0) ** np.arange(H)
+    v[1] = 3e38
+    v[1, 0] = -3e38
+    v[2] = g.standard_normal(H)
+    v[2, 0] = 3e38
+    v[3] = g.standard_normal(H)
+    h, hf = bf16(v)
+    _norm_gradients(h, hf, 2)
+    one = M.moe_add_layernorm_backward(h[3:4], h[3:4], torch.ones(H, device=DEV), 1e-5)
+    assert all(torch.isfinite(t).all() for t in one.values())
