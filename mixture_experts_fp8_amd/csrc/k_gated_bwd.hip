@@ -10,10 +10,13 @@ namespace moe {
 
 namespace {
 
-// 1 / (1 + exp(-v)) and its complement q = 1 - p, both within 2 u of their value down to 2^-126.  act_fn's argument
-// of the base-2 instruction is |v| u off and its reciprocal another u; a gradient that is rounded to bf16 and
-// then summed shows that in the values beside the middle of two, so both are mended here: by the rest of the
-// argument's product, and by one Newton step.
+// 1 / (1 + exp(-v)) and its complement q = 1 - p.  With u = 2^-24 and the base-2 instruction's own error of up to 2 u
+// (1.4 u was the most seen): p is within 5 u of its value (its exponential's 3 u, where they count in full, 1 + e and
+// the last step of the reciprocal 1 u each) and q within 6 u (the product 1 u more), where those are 2^-126 or more.
+// Over all bf16 arguments the most seen was 2.1 and 2.7 u, over 4 million floats 3.3 and 4.0 u.  Below 2^-126,
+// where 1 + e is 1e38 or more, p has no Newton step and ends as 0.  act_fn's argument of the instruction is |v| u off
+// and its reciprocal 2 u; a gradient that is rounded to bf16 and then summed shows that in the values beside the middle
+// of two, so both are mended here: by the rest of the argument's product, and by one Newton step.
 struct Logistic {
     float p, q;
 };

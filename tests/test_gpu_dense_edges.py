@@ -1,5 +1,5 @@
 """Edges of the operators of a model's dense layers on the GPU: rows whose first column is far from the others and rows
-across the whole range in the layer norm's backward pass.
+across the whole range in the layer norm's backward pass, activations of every bf16 value.
 
 Tolerances as in test_gpu_layer.py: u = 2^-24 is half a float32 step, 2^-8 half a bf16 step."""
 import numpy as np
@@ -52,3 +52,26 @@ def test_layernorm_backward_across_the_range(H):
     _norm_gradients(h, hf, 2)
     one = M.moe_add_layernorm_backward(h[3:4], h[3:4], torch.ones(H, device=DEV), 1e-5)
     assert all(torch.isfinite(t).all() for t in one.values())
+
+
+# ---- gated block, backward ----------------------------------------------------------------
+def test_gated_backward_silu_of_every_value():
+    """One row with dh = u = 1, so dbias is silu' and silu themselves in float32, for every finite bf16 value."""
+    K, I = 128, 1 << 16
+    bits = np.arange(I, dtype=np.uint32) << 16
+    with np.errstate(invalid="ignore"):
+        v = bits.view(np.float32).astype(np.float64)
+    v[~np.isfinite(v)] = 0.0
+    q = torch.zeros(K, 2 * I, dtype=torch.uint8, device=DEV)
+    w = M.LinearWeights.from_logical(q, torch.full((1, 2 * I // 128), 127, dtype=torch.uint8, device=DEV), M.QUANT_SCHEMES["fp8"])
+    gu, _ = bf16(np.concatenate([v, np.ones(I)])[None])
+    dh, _ = bf16(np.ones((1, I)))
+    out = host(M.moe_gated_linear_backward(dh, gu, w, activation="silu", want_dx=False, want_dbias=True)["dbias"])
+    act, (slope, _) = OD.activation(v, "silu"), OD.activation_slope(v, "silu")
+    with np.errstate(over="ignore"):
+        p, n = 1 / (1 + np.exp(-v)), 1 / (1 + np.exp(v))
+    # p within 5 u and 1 - p within 6 u; v p one rounding more, then p + (v p)(1 - p) with one.  Where p is below 2^-126 it
+    # may be 0: v p is below 2^-119 there
+    far = 2.0 ** -118
+    within(out[I:], act, 6.1 * U * np.abs(act) + far, "silu")
+    within(out[:I], slope, 5.1 * U * p + 12.1 * U * np.abs(act) * n + U * np.abs(slope) + far, "slope")
