@@ -46,12 +46,13 @@ __device__ __forceinline__ v4u_t* v_operand(const LoraArgs& p, int64_t slot, int
 // scale x A^T of a slot's rows and 16 NR columns.  Each of the NW waves takes every NW-th block of 64 K and
 // brings its operands through LDS stages of its own, S of them in flight, by LDS-DMA: eight neighbouring lanes
 // read 128 bytes of one row then.  (Straight to registers the operands' layout puts neighbouring lanes in
-// different rows, 64 requests of 16 bytes per instruction: 16384 x 4096 took 45 us for 134 MB, now 33.)  A row's
-// 16-byte chunk c stands at place c ^ (row % 8).  The waves' sums meet in LDS, in wave order, and leave as operands: a
+// different rows, 64 requests of 16 bytes per instruction: 16384 x 4096, rank 32, took 45 us for 134 MB; this way 35 to
+// 39, traced.)  A row's 16-byte chunk c stands at place c ^ (row % 8).  The waves' sums meet in LDS, in wave order, and leave as operands: a
 // sum of `split` bf16 values, each the rounding of what the ones before leave.  Two leave 2^-17 of it, under the
 // rounding of a bf16 y, three nothing of float32.  Columns from R on are 0.
-//   Bound by HBM for many rows of few sequences, by the L2s for many slots, which all read their adapter (2047 rows in 40
-// sequences x 4096, rank 64: 12 us for 107 MB), and by the chain of a wave's blocks in a decode step.  Waves and
+//   Bound by HBM for many rows of few sequences, and by the chain of a wave's blocks where slots are few: in a decode
+// step, and also at 2047 rows in 40 sequences x 4096, rank 64 (12 us), where 104 workgroups leave 152 CUs idle and
+// bring 107 MB of rows and adapters, 86 bytes per ns and busy CU.  Waves and
 // stages leave room for two workgroups per CU (16000 x 512 in 2000 sequences, rank 16: 37 us with its other half, with
 // one workgroup of twice the waves 53; 1 x 7168 10.7 and 10.5).
 template <int MT, int NR, int NW, int S>
@@ -186,8 +187,10 @@ __global__ __launch_bounds__(64 * NW) void k_lora_down(LoraArgs p) {
 // lane of the accumulators holds rows 4 (l / 16) .. +3 and one column of each of eight fragments; which column of B
 // stands where in a fragment is free, and is chosen such that those eight are consecutive (float32: four and four):
 // 16 neighbouring lanes then move 256 bytes of a row.  The residual, B and v are requested at once.  Bound by HBM for many
-// rows (16384 x 4096, rank 32: 58 us, 4.6 TB/s of residual and y), by the reading of B for many slots (2047 rows in 40
-// sequences, rank 64: 19 us, 11 of them for ranks 8 to 64).
+// rows (16384 x 4096, rank 32: 58 us, 4.6 TB/s of residual and y), by the chain of a workgroup's loads and products where
+// slots are few: 2048 rows in 40 sequences take 18.7 us at rank 64, 12.8 at rank 8.  Three workgroups per CU make
+// 768 places, and a second round for the 832 workgroups there costs too: 31 sequences, 760 workgroups, take 15.7 us,
+// 64 sequences, 1024 workgroups, 22.2.
 template <int MT, int MI, bool BF16>
 __global__ __launch_bounds__(256, 3) void k_lora_up(LoraArgs p) {
     constexpr int SPLIT = BF16 ? 2 : 3, WR = MT / MI, WC = 4 / WR;   // waves along rows and columns

@@ -16,7 +16,8 @@ int norm_bwd_parts(int T, int H) {
     return std::min(T, H <= 2048 && T >= 4096 ? 512 : 256);
 }
 // The layer norm forms more sums per row, which more workgroups hide where a thread has two vectors (16384 x 4096:
-// 107 us with 512, 143 with 512 threads and 256; 16384 x 2048: 68 with 1024, 74 with 512 and one vector per thread),
+// 110 us with 512 workgroups, and when those took 107, 143 with 256 of 512 threads; 16384 x 2048: 68 with 1024, 74 with
+// 512 and one vector per thread),
 // once each has several rows (1000 x 4096: 17.1 us with 256, 19.8 with 512).
 int layernorm_bwd_parts(int T, int H) {
     if (H <= 1024 || H > 4096) return norm_bwd_parts(T, H);
@@ -130,10 +131,16 @@ GatedBwdPlan gated_bwd_plan(int T, int K, int I, bool dx, bool dw, bool dbias) {
     return p;
 }
 
-// Windows of 32 rows read an adapter's matrices half as often as those of 16, but leave CUs without a slot up to about two
-// thousand rows, and half empty where sequences are short (1000 rows in 3 sequences x 7168 x 2048, rank 64: 22.9
-// us with windows of 16, 26.5 with 32; 1000 in 100 x 4096 x 4096, rank 16: 18.0 and 20.3; 2047 in 40, rank 64: 32.8 and
-// 30.5; 16384 in 9, rank 32: 112 and 99; 64 rows: 104, up to 6% less than 32 at many sequences, 18% more at 5000 rows).
+// Windows of 32 rows read an adapter's matrices half as often as those of 16, from half as many workgroups, and are half
+// empty where sequences are short.  Both measured on 4096 x 4096 with 1 to 4000 sequences; the time with 32 over the
+// time with 16, its range (and mean):
+//   rows, 24 and more per sequence   500, 1000        1400, 1800       2047 to 3400     5000, 8000       16384, 32768
+//   ranks 16 to 64                   1.04-1.30 (1.13) 0.94-1.12 (1.04) 0.87-1.15 (1.00) 0.89-1.11 (1.00) 0.80-1.04 (0.92)
+//   rank 128                         0.97-1.30 (1.06) 0.82-1.04 (0.94) 0.76-1.07 (0.91) 0.86-0.95 (0.91) 0.74-0.78 (0.76)
+//   rows per sequence, 2047 to 16000 rows   4         8                12, 16           20, 24           32
+//   ranks 16 to 128                         1.14-1.28 1.05-1.22        0.96-1.14        0.91-1.14        0.87-1.08
+// So 32 from 2000 rows and 24 rows per sequence on.  Single sizes near those borders lie up to 15% on either side, with
+// how the slots fall on the CUs; rank 128 would gain from 1400 rows on, and rank 16 gains nothing before 32768.
 LoraPlan lora_plan(int T, int R, int S, bool bf16) {
     LoraPlan p;
     p.window = S && T >= 2000 && T / S >= 24 ? 32 : 16;
@@ -483,7 +490,7 @@ int check_lora(const moe_lora_args* a) {
     if (a->out_dtype != MOE_DTYPE_F32 && a->out_dtype != MOE_DTYPE_BF16)
         return fail(MOE_ERR_INVALID, "%s: out_dtype (%d) must be MOE_DTYPE_F32 or MOE_DTYPE_BF16", op, a->out_dtype);
     if (a->ld_x < K) return fail(MOE_ERR_INVALID, "%s: ld_x (%lld) must be >= K (%d)", op, (long long)a->ld_x, K);
-    if (a->ld_x > (1 << 24))   // 64 rows within 32-bit offsets
+    if (a->ld_x > (1 << 24))   // 32 rows of a window within 2^30 bytes, a quarter of what the kernel's offsets hold
         return fail(MOE_ERR_UNSUPPORTED, "%s: ld_x (%lld) must not exceed %d", op, (long long)a->ld_x, 1 << 24);
     if (a->ld_y < N || (a->residual && a->ld_residual < N))
         return fail(MOE_ERR_INVALID, "%s: ld_y (%lld) and ld_residual (%lld) must be >= N (%d)", op, (long long)a->ld_y,
