@@ -628,7 +628,9 @@ size_t moe_gated_linear_backward_workspace_size(int32_t T, int32_t K, int32_t I,
  * wrote (moe_linear without activation) as y and residual at once, the adapters are added to it; given another
  * y, that can be moe_linear's residual.
  * The inner product is a float32 sum; it goes to the matrix cores as two bf16 values (three for float32 y)
- * whose sum is within 2^-17 (2^-25) of it times the scale, and y is rounded once.
+ * whose sum is within 2^-17 (2^-25) of it times the scale, and y is rounded once.  Beyond bf16's largest value it is
+ * infinite.  Infinities and NaN stay in the rows of x and the adapters, and of b in the columns, that hold them; an
+ * infinite b, which meets both parts, may give NaN where the formula gives an infinity.
  *   T, K, N, R  K % 8 == 0, K <= 65536; N % 16 == 0, N <= 2^20; R % 8 == 0, R <= 256 (a smaller rank is
  *               padded with zeros); T <= 2^23, num_seqs <= 2^20.
  *   x           [T, ld_x] bf16, the first K columns used; ld_x <= 2^24.

@@ -510,8 +510,9 @@ class MoeLora(_Call):
     x bf16 [T, K]; adapter_ids int32 [num_seqs], a sequence without an adapter has one outside the range;
     seq_offsets int32 [num_seqs + 1] on the GPU, or None for one row per sequence.  residual and y [T, N] of
     out_dtype (bfloat16 or float32); rows of x, residual and y may be strided; y may be residual itself.
-    Rows outside the sequences are left as they were: a y that the object makes starts as 0, and a row that
-    was in a sequence of an earlier call keeps that call's values."""
+    Rows outside the sequences are left as they were: a y that the object makes starts as 0 (filled on the
+    stream that is current then, which a call on another stream has to come behind), and a row that was in a
+    sequence of an earlier call keeps that call's values."""
 
     def __init__(self, x: torch.Tensor, w: LoraWeights, adapter_ids: torch.Tensor,
                  seq_offsets: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,

@@ -1,5 +1,5 @@
 """Edges of the operators of a model's dense layers on the GPU: rows whose first column is far from the others and rows
-across the whole range in the layer norm's backward pass, activations of every bf16 value.
+across the whole range in the layer norm's backward pass, activations of every bf16 value, adapters that are not finite.
 
 Tolerances as in test_gpu_layer.py: u = 2^-24 is half a float32 step, 2^-8 half a bf16 step."""
 import numpy as np
@@ -75,3 +75,24 @@ def test_gated_backward_silu_of_every_value():
     far = 2.0 ** -118
     within(out[I:], act, 6.1 * U * np.abs(act) + far, "silu")
     within(out[:I], slope, 5.1 * U * p + 12.1 * U * np.abs(act) * n + U * np.abs(slope) + far, "slope")
+
+
+# ---- adapters -----------------------------------------------------------------------------
+@pytest.mark.parametrize("T,seqs,dt", [(40, None, torch.bfloat16), (70, [0, 0, 33, 70], torch.float32), (2300, [0, 900, 900, 2300], torch.bfloat16)])
+def test_lora_of_an_infinite_b(T, seqs, dt):
+    """An infinity and a NaN of b reach their own column in the rows of their own adapter, and nothing else."""
+    K, N, R, n = 264, 208, 40, 3
+    g = rng(54, T)
+    x, r = bf16(g.standard_normal((T, K)))[0], torch.from_numpy(g.standard_normal((T, N))).to(DEV, dt)
+    a, b = bf16(g.standard_normal((n, R, K)) / 16)[0], bf16(g.standard_normal((n, N, R)) / 8)[0]
+    ids = torch.from_numpy(g.integers(0, n, T) if seqs is None else np.array([1, 0, 2])).to(DEV, torch.int32)
+    off = None if seqs is None else torch.tensor(seqs, dtype=torch.int32, device=DEV)
+    want = M.moe_lora(x, M.LoraWeights(a, b), ids, off, r, dt)
+    bad = b.clone()
+    bad[1, 7, 3], bad[2, N - 1, R - 1] = float("inf"), float("nan")
+    got = M.moe_lora(x, M.LoraWeights(a, bad), ids, off, r, dt)
+    row = ids.cpu().numpy() if seqs is None else np.repeat([1, 0, 2], np.diff(seqs))
+    hit = np.zeros((T, N), bool)
+    hit[row == 1, 7], hit[row == 2, N - 1] = True, True
+    assert np.array_equal(~np.isfinite(host(got)), hit)
+    assert np.array_equal(host(got)[~hit], host(want)[~hit])
