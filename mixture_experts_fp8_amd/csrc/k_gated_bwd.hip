@@ -153,7 +153,9 @@ __device__ __forceinline__ void gated_dgu(const DguArgs& a, int unit, uint8_t* s
 #pragma unroll
             for (int j = 0; j < CW; ++j) {
                 const Act f = act_slope<ACT>(x[j]);
-                x[j] = z[j] * y[j] * f.s;
+                // (dh u beyond float32 comes back where the slope is small; dh is then above 1, and dh act' does not vanish)
+                const float zy = z[j] * y[j];
+                x[j] = fabsf(zy) < __builtin_inff() ? zy * f.s : z[j] * f.s * y[j];
                 y[j] = z[j] * f.a;
                 if (t >= a.T) x[j] = y[j] = 0.f;
                 sg[j] += x[j];

@@ -77,6 +77,30 @@ def test_gated_backward_silu_of_every_value():
     within(out[:I], slope, 5.1 * U * p + 12.1 * U * np.abs(act) * n + U * np.abs(slope) + far, "slope")
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_gated_backward_of_large_factors(act):
+    """dh u beyond float32 where the slope brings the product back: finite, and the formula's value."""
+    T, K, I = 70, 128, 96
+    g = rng(55)
+    gate = g.uniform(-9.0, -3.0, (T, I))      # slopes of 1e-1 to 1e-17
+    size = 10.0 ** g.uniform(10.0, 28.0, (T, I))
+    u = size * g.choice([-1.0, 1.0], (T, I))
+    gu, guf = bf16(np.concatenate([gate, u], 1))
+    dh, dhf = bf16(10.0 ** g.uniform(38.0, 41.0, (T, I)) / size)
+    w = M.LinearWeights.from_logical(torch.zeros(K, 2 * I, dtype=torch.uint8, device=DEV),
+                                     torch.full((1, 2), 127, dtype=torch.uint8, device=DEV), M.QUANT_SCHEMES["fp8"])
+    d = host(M.moe_gated_linear_backward(dh, gu, w, activation=act, want_dx=False)["dgu"])
+    v, mag = OD.gated_backward(dhf, guf[:, :I], guf[:, I:], act)
+    x = np.abs(guf[:, :I])
+    rel = 2 * (3 * np.maximum(x, x * x) + 40) * U      # (the bound of test_gated_linear_backward)
+    tol = np.concatenate([rel, rel], 1) * mag
+    fits = np.abs(v) < 3.3e38
+    assert (np.abs(dhf * guf[:, I:])[fits[:, :I]] > 3.5e38).sum() > 1000
+    within(d[fits], v[fits], (tol + UB * (np.abs(v) + tol) + TINY)[fits], "dgu")
+    over = np.abs(v) > 3.5e38
+    assert np.array_equal(d[over], np.sign(v[over]) * np.inf)
+
+
 # ---- adapters -----------------------------------------------------------------------------
 @pytest.mark.parametrize("T,seqs,dt", [(40, None, torch.bfloat16), (70, [0, 0, 33, 70], torch.float32), (2300, [0, 900, 900, 2300], torch.bfloat16)])
 def test_lora_of_an_infinite_b(T, seqs, dt):
