@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 import torch
 
-from oracle import dense as OD
+from oracle import dense as OD, layer as OL
 from test_gpu_layer import DEV, M, TINY, U, UB, bf16, f32, host, rng, within
 
 pytestmark = pytest.mark.gpu
@@ -52,6 +52,34 @@ def test_layernorm_backward_across_the_range(H):
     _norm_gradients(h, hf, 2)
     one = M.moe_add_layernorm_backward(h[3:4], h[3:4], torch.ones(H, device=DEV), 1e-5)
     assert all(torch.isfinite(t).all() for t in one.values())
+
+
+@pytest.mark.parametrize("norm", ["layer", "rms"])
+@pytest.mark.parametrize("H", [64, 1000, 4096, 20000])
+def test_norm_backward_of_the_smallest_rows(norm, H):
+    """Values at bf16's smallest steps with eps = 0, whose 1 / sqrt is beyond float32: gradients that bf16 holds are the
+    formula's, and 0 where dy is 0."""
+    g = rng(56, H)
+    v = g.integers(-3, 4, (5, H)) * TINY
+    v[4] = g.standard_normal(H) * 1e-37
+    h, hf = bf16(v)
+    dy, dyf = bf16(g.standard_normal((5, H)) * np.array([1e-3, 0, 1e-20, 1, 1])[:, None])
+    w, wf = f32(1 + 0.1 * g.standard_normal(H))
+    if norm == "layer":
+        out = M.moe_add_layernorm_backward(dy, h, w, 0.0)
+        dx, _, _, mag, _, _ = OD.layernorm_backward(dyf, hf, wf, 0.0)
+        tol = 10 * U * (1 + UB) * mag
+    else:
+        out = M.moe_add_rmsnorm_backward(dy, h, w, 0.0)
+        dx, _, mag, _ = OL.rmsnorm_backward(dyf, hf, wf, 0.0)
+        tol = 64 * U * (1 + UB) * mag          # (the bound of test_add_rmsnorm_backward)
+    got = host(out["dx"])
+    assert (got[1] == 0).all() and np.abs(dx[0]).max() > 1e35
+    fits = np.abs(dx) < 3.3e38
+    within(got[fits], dx[fits], (UB * np.abs(dx) + tol + TINY)[fits], "dx")
+    over = np.abs(dx) > 3.5e38
+    assert over[3].any() and np.array_equal(got[over], np.sign(dx[over]) * np.inf)
+    assert all(torch.isfinite(out[n]).all() for n in out if n != "dx")
 
 
 # ---- gated block, backward ----------------------------------------------------------------
