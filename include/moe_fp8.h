@@ -480,8 +480,8 @@ int moe_add_layernorm(const moe_add_layernorm_args* a);
 /* moe_add_layernorm_backward: as moe_add_rmsnorm_backward, with xhat = (h - m) * r and g = dy * weight:
  *   dx[t, :]   = bf16_RNE( r * (g - mean_c(g) - xhat * mean_c(g * xhat)) + dh );
  *   dweight[c] = sum_t dy[t, c] * xhat[t, c],  dbias[c] = sum_t dy[t, c]   (float32, each optional).
- * The rows' sums and xhat are formed in double, products and the two gradients' sums in float32.  Buffers as there;
- * workspace >=
+ * The rows' sums and xhat are formed in double, products and the two gradients' sums in float32 (dy * weight and
+ * its difference to the mean have to fit there).  Buffers as there; workspace >=
  * moe_add_layernorm_backward_workspace_size(T, H) bytes, used for dweight and dbias only (may be NULL
  * without both).  Deterministic. */
 typedef struct moe_add_layernorm_backward_args {
@@ -552,8 +552,10 @@ size_t moe_linear_workspace_size(int32_t T, int32_t K, int32_t N, int32_t quant)
 
 /* moe_gated_linear: the first half of a gated feed-forward block, both projections in one pass over x:
  *   [g | u] = dequant(xq, xs) @ dequant(w, w_scale) + bias,   h = bf16_RNE( act(g) * u ),
- * float32 sums as in moe_linear, rounded once.  w holds the gate projection in columns [0, I) and the up
- * projection in [I, 2I), as an expert's w13, in moe_linear's layouts with N = 2I.
+ * float32 sums as in moe_linear, rounded once (what the matrix instruction drops there is about 2^-16 of a sum of
+ * normal operands, so one bf16 value in a hundred is the exact sum's neighbour; a call's repeats are equal).  w
+ * holds the gate projection in columns [0, I) and the up projection in [I, 2I), as an expert's w13, in
+ * moe_linear's layouts with N = 2I.
  *   T, K, I    K % 128 == 0, K <= 32768; I % 32 == 0; T * K < 2^31, K * 2I < 2^31, T * 2I < 2^40.
  *   quant, xq, xs, w, w_scale, activation  as in moe_linear.
  *   bias       [2I] float32 (gate, then up) or NULL.

@@ -17,8 +17,7 @@ int norm_bwd_parts(int T, int H) {
 }
 // The layer norm forms more sums per row, which more workgroups hide where a thread has two vectors (16384 x 4096:
 // 110 us with 512 workgroups, and when those took 107, 143 with 256 of 512 threads; 16384 x 2048: 68 with 1024, 74 with
-// 512 and one vector per thread),
-// once each has several rows (1000 x 4096: 17.1 us with 256, 19.8 with 512).
+// 512 and one vector per thread), once each has several rows (1000 x 4096: 17.1 us with 256, 19.8 with 512).
 int layernorm_bwd_parts(int T, int H) {
     if (H <= 1024 || H > 4096) return norm_bwd_parts(T, H);
     return std::min(T, T < 4096 ? 256 : H <= 2048 ? 1024 : 512);
